@@ -19,6 +19,9 @@ C_FLAGS = ["-std=c11", "-O2", "-Wall", "-Wextra", "-Wpedantic", "-Werror",
            "-D__HIP_PLATFORM_AMD__"]  # selects the AMD half of the HIP runtime header
 
 SOURCES = ["hcr_kernels.hip", "hcr_matvec.hip", "hcr_api.cpp"]
+# the paged cache (include/hcr_paged.h), in the same library
+PAGED_SOURCES = ["hcr_append.hip", "hcr_attn.hip", "hcr_blocks.hip", "hcr_paged_api.cpp"]
+PAGED_HEADERS = ["hcr_paged_layout.h"]
 # the calibration kernels (include/hcr_calib.h): a library of their own, measurement only
 CALIB_LIB = os.path.join(PKG, "libhcr_calib.so")
 CALIB_SOURCES = ["hcr_calib.hip"]
@@ -64,12 +67,13 @@ def _code_only(text):
 
 
 def source_hash():
-    """sha256 over the code of libhcr.so's sources (its csrc/ files and headers, and include/hcr.h; not the
-    calibration library's), comments and whitespace left out, and the compiler flags; measurements taken
-    with hardware counters are valid only for the code they were taken on."""
+    """sha256 over the code of the read's and the matvec's sources (their csrc/ files and headers, and
+    include/hcr.h; not the calibration library's nor the paged cache's, which those kernels share no code
+    with), comments and whitespace left out, and the compiler flags; measurements taken with hardware counters
+    are valid only for the code they were taken on."""
     h = hashlib.sha256()
-    files = sorted(f for f in os.listdir(CSRC)
-                   if f.endswith((".hip", ".h", ".cpp")) and f not in CALIB_SOURCES)
+    apart = CALIB_SOURCES + PAGED_SOURCES + PAGED_HEADERS
+    files = sorted(f for f in os.listdir(CSRC) if f.endswith((".hip", ".h", ".cpp")) and f not in apart)
     paths = [os.path.join(CSRC, f) for f in files] + [os.path.join(ROOT, "include", "hcr.h")]
     for path in paths:
         with open(path) as fh:
@@ -128,7 +132,7 @@ def _hipcc_shared(path, sources, verbose):
 def build(verbose=False):
     """Compile every source into libhcr.so and the calibration kernels into libhcr_calib.so, then the
     C caller (always recompiles); returns the library path."""
-    _hipcc_shared(LIB, SOURCES, verbose)
+    _hipcc_shared(LIB, SOURCES + PAGED_SOURCES, verbose)
     _hipcc_shared(CALIB_LIB, CALIB_SOURCES, verbose)
     build_c_caller(verbose)
     return LIB

@@ -1,0 +1,320 @@
+// C ABI of the paged cache: argument checks, the handle and the plan of an attention call.  Every check runs on
+// the host before any HIP call.
+
+#include <stdint.h>
+#include <stdlib.h>
+
+#include "hcr_paged_layout.h"
+
+struct hcr_cache {
+  hcr::CacheArgs args;
+};
+
+namespace hcr {
+
+namespace {
+
+struct Span {
+  uintptr_t lo, hi;  // [lo, hi); lo == hi: absent
+};
+Span span(const void* p, size_t bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return p ? Span{a, a + bytes} : Span{0, 0};
+}
+bool overlap(Span a, Span b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+constexpr long long GRID_MAX = 1ll << 30;  // work-groups of a launch, and rows of a call
+
+size_t pages_elements(const CacheArgs& c) {
+  return ((size_t)c.n_pages * c.kv_heads * c.head_dim) << c.shift;
+}
+size_t means_elements(const CacheArgs& c) { return (size_t)c.n_pages * c.kv_heads * c.head_dim; }
+
+// The device arrays of a batch, which no output may overlap.
+struct BatchSpans {
+  Span s[3];
+};
+BatchSpans batch_spans(const BatchArgs& b) {
+  return BatchSpans{{span(b.q_start, ((size_t)b.n_seqs + 1) * 4), span(b.ctx_len, (size_t)b.n_seqs * 4),
+                     span(b.table, (size_t)b.n_seqs * b.table_stride * 4)}};
+}
+struct CacheSpans {
+  Span s[3];
+};
+CacheSpans cache_spans(const CacheArgs& c) {
+  return CacheSpans{{span(c.k, pages_elements(c) * 2), span(c.v, pages_elements(c) * 2),
+                     span(c.means, means_elements(c) * 2)}};
+}
+template <typename T>
+bool overlap_any(Span o, const T& t) {
+  for (const Span& s : t.s)
+    if (overlap(o, s)) return true;
+  return false;
+}
+
+// The ints of a batch against a cache and a number of heads; *b takes them.  1: nothing to do.
+int check_bounds(const CacheArgs& c, const hcr_batch* in, int heads, BatchArgs* b) {
+  if (!in) return HCR_EINVAL;
+  if (heads < 1 || heads % c.kv_heads || heads / c.kv_heads > GROUP_MAX) return HCR_EINVAL;
+  if (in->n_seqs < 0 || in->n_tokens < 0 || in->max_tokens < 0 || in->max_ctx < 0 || in->table_stride < 0)
+    return HCR_EINVAL;
+  if ((long long)in->table_stride << c.shift < in->max_ctx || in->max_ctx > 1 << 30) return HCR_EINVAL;
+  *b = BatchArgs{in->q_start, in->ctx_len,  in->block_table, in->table_stride,
+                 in->n_seqs,  in->n_tokens, in->max_tokens,  in->max_ctx};
+  if (b->max_tokens > b->n_tokens) b->max_tokens = b->n_tokens;
+  if (b->n_seqs == 0 || b->max_tokens == 0) return 1;
+  // rows and work-groups stay inside 32 bits
+  if ((long long)b->n_tokens * heads > GRID_MAX || (long long)b->n_seqs * b->max_tokens > GRID_MAX / heads ||
+      (long long)b->n_seqs * b->table_stride > GRID_MAX * 2)
+    return HCR_EINVAL;
+  return HCR_OK;
+}
+int check_arrays(const BatchArgs& b) {
+  if (!b.q_start || !b.ctx_len || (!b.table && b.table_stride)) return HCR_EINVAL;
+  if (!aligned(b.q_start, 4) || !aligned(b.ctx_len, 4) || !aligned(b.table, 4)) return HCR_EALIGN;
+  return HCR_OK;
+}
+
+// Rows of heads of one input: their span, or an error.
+int check_rows(const hcr_rows* r, int type, int n_tokens, int heads, int head_dim, Span* s) {
+  if (!r || !r->data) return HCR_EINVAL;
+  const long long unit = type == HCR_F32 ? 4 : 8, size = type == HCR_F32 ? 4 : 2;
+  const long long most = 1ll << 40;
+  if (r->token_stride < 0 || r->head_stride < 0 || r->token_stride > most || r->head_stride > most) return HCR_EINVAL;
+  if (!aligned(r->data, 16) || r->token_stride % unit || r->head_stride % unit) return HCR_EALIGN;
+  const long long last = (n_tokens - 1) * r->token_stride + (heads - 1) * r->head_stride + head_dim;
+  *s = span(r->data, (size_t)last * size);
+  return HCR_OK;
+}
+
+long long attn_grid(const CacheArgs& c, const BatchArgs& b, const AttnPlan& p, bool listed) {
+  const long long units = (long long)p.splits * b.n_seqs * (listed ? b.max_tokens : 1) * c.kv_heads;
+  return (units + XCDS - 1) / XCDS * XCDS * p.row_blocks;
+}
+
+size_t scratch_of(const CacheArgs& c, const BatchArgs& b, int heads, const AttnPlan& p) {
+  if (p.splits == 1) return 0;
+  return align256((size_t)b.n_tokens * heads * p.splits * (c.head_dim + 2) * 4);
+}
+
+int attn(hcr_cache_t h, const hcr_batch* batch, int heads, double scale, const void* q, const int* sel, int n_sel,
+         int out_type, void* out, void* scratch, size_t scratch_bytes, void* stream) {
+  if (!h) return HCR_EINVAL;
+  const CacheArgs& c = h->args;
+  AttnArgs a{};
+  a.c = c;
+  const int rc = check_bounds(c, batch, heads, &a.b);
+  if (rc < 0) return rc;
+  if (out_type != HCR_F32 && out_type != HCR_BF16) return HCR_EINVAL;
+  if (!(scale > -1e30 && scale < 1e30)) return HCR_EINVAL;  // NaN and infinite too
+  if (n_sel < 0 || (long long)n_sel << c.shift > GRID_MAX) return HCR_EINVAL;
+  if (rc == 1) return HCR_OK;
+  if (!q || !out) return HCR_EINVAL;
+  if (const int e = check_arrays(a.b)) return e;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(sel, 4) || !aligned(scratch, 256)) return HCR_EALIGN;
+  a.plan = attn_plan(c, a.b, heads, n_sel);
+  if (attn_grid(c, a.b, a.plan, n_sel > 0) > GRID_MAX) return HCR_EINVAL;
+  const size_t need = scratch_of(c, a.b, heads, a.plan);
+  if (need && (!scratch || scratch_bytes < need)) return HCR_ESCRATCH;
+  const size_t values = (size_t)a.b.n_tokens * heads * c.head_dim;
+  const Span so = span(out, values * (out_type == HCR_F32 ? 4 : 2)), sq = span(q, values * 2);
+  const Span ss = need ? span(scratch, need) : Span{0, 0};
+  const Span sl = span(sel, (size_t)a.b.n_tokens * c.kv_heads * n_sel * 4);
+  const Span written[] = {so, ss};
+  if (overlap(so, ss)) return HCR_EALIAS;
+  for (const Span& w : written)
+    if (overlap(w, sq) || overlap(w, sl) || overlap_any(w, cache_spans(c)) || overlap_any(w, batch_spans(a.b)))
+      return HCR_EALIAS;
+  a.q = static_cast<const uint16_t*>(q);
+  a.sel = sel;
+  a.n_sel = n_sel;
+  a.heads = heads;
+  a.group = heads / c.kv_heads;
+  a.out_type = out_type;
+  const double log2e = scale * 1.4426950408889634;
+  a.scale_hi = (float)log2e;
+  a.scale_lo = (float)(log2e - a.scale_hi);
+  a.out = out;
+  a.part = static_cast<float*>(scratch);
+  return launch_attn(a, stream);
+}
+
+}  // namespace
+
+AttnPlan attn_plan(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel) {
+  AttnPlan p{};
+  const int group = heads / c.kv_heads;
+  const int rows = n_sel ? group : b.max_tokens * group;
+  p.q_tiles = rows <= 16 ? 1 : rows <= 32 || c.head_dim == 256 ? 2 : 4;
+  p.row_blocks = ceil_div(rows, 16 * p.q_tiles);
+  const int tiles = n_sel ? n_sel << (c.shift - TILE_SHIFT) : ceil_div(b.max_ctx, TILE);
+  const long long units = (long long)b.n_seqs * c.kv_heads * p.row_blocks * (n_sel ? b.max_tokens : 1);
+  const int fill = c.head_dim == 256 ? 512 : 1024;  // work-groups that the chip holds at once
+  long long splits = (fill + units - 1) / units;
+  const int most = ceil_div(tiles, 2 * ATTN_WAVES);  // two tiles of a wave at least
+  if (splits > most) splits = most;
+  if (splits < 1) splits = 1;
+  p.chunk = ceil_div(tiles, (int)splits);
+  if (p.chunk < 1) p.chunk = 1;
+  p.splits = tiles ? ceil_div(tiles, p.chunk) : 1;
+  return p;
+}
+
+}  // namespace hcr
+
+using namespace hcr;
+
+extern "C" {
+
+size_t hcr_cache_pages_bytes(int n_pages, int kv_heads, int head_dim, int page) {
+  if (n_pages < 1 || kv_heads < 1 || !head_dim_ok(head_dim) || !page_ok(page)) return 0;
+  return (size_t)n_pages * kv_heads * head_dim * page * 2;
+}
+
+int hcr_cache_create(void* k_pages, void* v_pages, void* k_means, int n_pages, int kv_heads, int head_dim, int page,
+                     hcr_cache_t* out) {
+  if (!out) return HCR_EINVAL;
+  *out = nullptr;
+  if (!k_pages || !v_pages || n_pages < 1 || kv_heads < 1 || kv_heads > 4096 || !head_dim_ok(head_dim) ||
+      !page_ok(page))
+    return HCR_EINVAL;
+  if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(k_means, 16)) return HCR_EALIGN;
+  const CacheArgs c{static_cast<uint16_t*>(k_pages), static_cast<uint16_t*>(v_pages), static_cast<uint16_t*>(k_means),
+                    n_pages, kv_heads, head_dim, log2_of(page)};
+  const CacheSpans s = cache_spans(c);
+  if (overlap(s.s[0], s.s[1]) || overlap(s.s[0], s.s[2]) || overlap(s.s[1], s.s[2])) return HCR_EALIAS;
+  hcr_cache* h = static_cast<hcr_cache*>(malloc(sizeof(hcr_cache)));
+  if (!h) return HCR_EINVAL;
+  h->args = c;
+  *out = h;
+  return HCR_OK;
+}
+
+void hcr_cache_destroy(hcr_cache_t c) { free(c); }
+
+int hcr_cache_append(hcr_cache_t h, const hcr_batch* batch, int heads, int type, const hcr_rows* q, const hcr_rows* k,
+                     const hcr_rows* v, const float* q_norm, const float* k_norm, float eps, const float* rope,
+                     int rope_rows, int rope_dim, int rope_style, void* q_out, void* stream) {
+  if (!h) return HCR_EINVAL;
+  const CacheArgs& c = h->args;
+  AppendArgs a{};
+  a.c = c;
+  const int rc = check_bounds(c, batch, heads, &a.b);
+  if (rc < 0) return rc;
+  if (type != HCR_F32 && type != HCR_BF16) return HCR_EINVAL;
+  if (!(eps >= 0.f) || eps - eps != 0.f) return HCR_EINVAL;
+  if (rope_dim < 0 || rope_dim > c.head_dim || rope_dim % 8 || (rope_dim && !rope) ||
+      (rope_dim && rope_rows < a.b.max_ctx) ||
+      (rope_style != HCR_ROPE_HALVES && rope_style != HCR_ROPE_PAIRS))
+    return HCR_EINVAL;
+  if (rc == 1) return HCR_OK;
+  if (!q_out) return HCR_EINVAL;
+  if (const int e = check_arrays(a.b)) return e;
+  if (!aligned(q_out, 16) || !aligned(q_norm, 16) || !aligned(k_norm, 16) || !aligned(rope, 16)) return HCR_EALIGN;
+  Span in[6];
+  if (const int e = check_rows(q, type, a.b.n_tokens, heads, c.head_dim, &in[0])) return e;
+  if (const int e = check_rows(k, type, a.b.n_tokens, c.kv_heads, c.head_dim, &in[1])) return e;
+  if (const int e = check_rows(v, type, a.b.n_tokens, c.kv_heads, c.head_dim, &in[2])) return e;
+  in[3] = span(q_norm, (size_t)c.head_dim * 4);
+  in[4] = span(k_norm, (size_t)c.head_dim * 4);
+  in[5] = span(rope_dim ? rope : nullptr, (size_t)rope_rows * rope_dim * 4);
+  const long long pages = ((a.b.max_tokens - 1) >> c.shift) + 2;
+  if (a.b.n_seqs * pages * c.kv_heads * 2 > GRID_MAX) return HCR_EINVAL;
+  const Span so = span(q_out, (size_t)a.b.n_tokens * heads * c.head_dim * 2);
+  const CacheSpans sc = cache_spans(c);
+  if (overlap_any(so, sc) || overlap_any(so, batch_spans(a.b))) return HCR_EALIAS;
+  for (const Span& s : in)
+    if (overlap(so, s) || overlap_any(s, sc)) return HCR_EALIAS;
+  for (const Span& s : batch_spans(a.b).s)
+    if (overlap_any(s, sc)) return HCR_EALIAS;
+  a.q = *q;
+  a.k = *k;
+  a.v = *v;
+  a.heads = heads;
+  a.type = type;
+  a.q_norm = q_norm;
+  a.k_norm = k_norm;
+  a.rope = rope;
+  a.eps = eps;
+  a.rope_dim = rope_dim;
+  a.rope_style = rope_style;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  return launch_append(a, stream);
+}
+
+size_t hcr_attn_scratch_bytes(hcr_cache_t h, const hcr_batch* batch, int heads, int n_sel) {
+  BatchArgs b;
+  if (!h || check_bounds(h->args, batch, heads, &b) != HCR_OK || n_sel < 0 ||
+      (long long)n_sel << h->args.shift > GRID_MAX)
+    return 0;
+  return scratch_of(h->args, b, heads, attn_plan(h->args, b, heads, n_sel));
+}
+
+int hcr_attn(hcr_cache_t c, const hcr_batch* batch, int heads, double scale, const void* q, int out_type, void* out,
+             void* scratch, size_t scratch_bytes, void* stream) {
+  return attn(c, batch, heads, scale, q, nullptr, 0, out_type, out, scratch, scratch_bytes, stream);
+}
+
+int hcr_attn_blocks(hcr_cache_t c, const hcr_batch* batch, int heads, double scale, const void* q, const int* sel,
+                    int n_sel, int out_type, void* out, void* scratch, size_t scratch_bytes, void* stream) {
+  if (n_sel < 1 || !sel) return HCR_EINVAL;
+  return attn(c, batch, heads, scale, q, sel, n_sel, out_type, out, scratch, scratch_bytes, stream);
+}
+
+int hcr_block_scores(hcr_cache_t h, const hcr_batch* batch, int heads, const void* q, float* scores, int scores_stride,
+                     void* stream) {
+  if (!h || !h->args.means) return HCR_EINVAL;
+  const CacheArgs& c = h->args;
+  ScoreArgs a{};
+  a.c = c;
+  const int rc = check_bounds(c, batch, heads, &a.b);
+  if (rc < 0) return rc;
+  const int pages = a.b.max_ctx > 0 ? (a.b.max_ctx - 1) >> c.shift : 0;  // that a token can score
+  if (scores_stride < 0 || scores_stride < pages) return HCR_EINVAL;
+  if (rc == 1 || pages == 0) return HCR_OK;
+  if (!q || !scores) return HCR_EINVAL;
+  if (const int e = check_arrays(a.b)) return e;
+  if (!aligned(q, 16) || !aligned(scores, 16)) return HCR_EALIGN;
+  if ((long long)a.b.n_seqs * c.kv_heads * (pages / 16 + 1) > GRID_MAX) return HCR_EINVAL;
+  const Span so = span(scores, (size_t)a.b.n_tokens * c.kv_heads * scores_stride * 4);
+  if (overlap(so, span(q, (size_t)a.b.n_tokens * heads * c.head_dim * 2)) || overlap_any(so, cache_spans(c)) ||
+      overlap_any(so, batch_spans(a.b)))
+    return HCR_EALIAS;
+  a.q = static_cast<const uint16_t*>(q);
+  a.heads = heads;
+  a.group = heads / c.kv_heads;
+  a.scores = scores;
+  a.stride = scores_stride;
+  return launch_block_scores(a, stream);
+}
+
+int hcr_block_topk(hcr_cache_t h, const hcr_batch* batch, const float* scores, int scores_stride, int n_sel,
+                   int n_first, int n_last, int* sel, void* stream) {
+  if (!h) return HCR_EINVAL;
+  const CacheArgs& c = h->args;
+  TopkArgs a{};
+  const int rc = check_bounds(c, batch, c.kv_heads, &a.b);
+  if (rc < 0) return rc;
+  const int pages = a.b.max_ctx > 0 ? (a.b.max_ctx - 1) >> c.shift : 0;
+  if (n_sel < 1 || n_first < 0 || n_last < 1 || n_first > n_sel || n_last > n_sel - n_first) return HCR_EINVAL;
+  if (scores_stride < 0 || scores_stride < pages) return HCR_EINVAL;
+  if (rc == 1) return HCR_OK;
+  if (!sel || (!scores && pages)) return HCR_EINVAL;
+  if (const int e = check_arrays(a.b)) return e;
+  if (!aligned(scores, 16) || !aligned(sel, 4)) return HCR_EALIGN;
+  const size_t rows = (size_t)a.b.n_tokens * c.kv_heads;
+  const Span so = span(sel, rows * n_sel * 4);
+  if (overlap(so, span(scores, rows * scores_stride * 4)) || overlap_any(so, batch_spans(a.b))) return HCR_EALIAS;
+  a.scores = scores;
+  a.stride = scores_stride;
+  a.kv_heads = c.kv_heads;
+  a.shift = c.shift;
+  a.n_sel = n_sel;
+  a.n_first = n_first;
+  a.n_last = n_last;
+  a.sel = sel;
+  return launch_block_topk(a, stream);
+}
+
+}  // extern "C"

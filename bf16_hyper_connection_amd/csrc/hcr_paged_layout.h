@@ -1,0 +1,135 @@
+// Index arithmetic of the paged cache, shared by its kernels, the C ABI and a host-compiled test: where a
+// position's keys and values lie, which rows and positions a sequence has, how attention is split.
+// Host and device code include it.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "hcr_layout.h"
+#include "hcr_paged.h"
+
+#if defined(__HIPCC__)
+#define HCR_HD __host__ __device__ inline __attribute__((always_inline))
+#else
+#define HCR_HD inline
+#endif
+
+namespace hcr {
+
+// ---- geometry
+constexpr int GROUP_MAX = 64;  // heads of one kv head
+HCR_HD bool page_ok(int page) { return page == 32 || page == 64 || page == 128 || page == 256; }
+HCR_HD bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
+HCR_HD int log2_of(int pow2) {
+  int s = 0;
+  while ((1 << s) < pow2) ++s;
+  return s;
+}
+
+// What the kernels take of a cache and of a batch (by value).
+struct CacheArgs {
+  uint16_t* k;  // BF16 bits
+  uint16_t* v;
+  uint16_t* means;
+  int n_pages, kv_heads, head_dim, shift;  // page = 1 << shift
+};
+struct BatchArgs {
+  const int* q_start;
+  const int* ctx_len;
+  const int* table;
+  int table_stride, n_seqs, n_tokens, max_tokens, max_ctx;
+};
+
+// First element of head h of a page (k_pages and v_pages alike; 64 bits: a cache passes 2^31 elements).
+HCR_HD size_t head_base(const CacheArgs& c, int page, int h) {
+  return ((size_t)page * c.kv_heads + h) * ((size_t)c.head_dim << c.shift);
+}
+// Element of dimension d of slot s within a head's page.
+HCR_HD int k_at(int shift, int s, int d) { return (((d >> 3) << shift) + s) * 8 + (d & 7); }
+HCR_HD int v_at(int head_dim, int s, int d) { return ((s >> 3) * head_dim + d) * 8 + (s & 7); }
+
+// A sequence's rows [row, row + tokens) and the position of its first new token (negative where the sequence is
+// shorter than its window), held to the bounds of the batch whatever q_start and ctx_len say.
+struct Seq {
+  int row, tokens, first;
+};
+HCR_HD Seq seq_of(const BatchArgs& b, int s0, int s1, int ctx) {
+  Seq q{0, 0, 0};
+  if (s0 < 0 || s0 >= b.n_tokens || s1 <= s0) return q;
+  q.row = s0;
+  q.tokens = s1 - s0;
+  const int room = b.n_tokens - s0;
+  if (q.tokens > room) q.tokens = room;
+  if (q.tokens > b.max_tokens) q.tokens = b.max_tokens;
+  if (ctx > b.max_ctx) ctx = b.max_ctx;
+  if (ctx < 0) ctx = 0;
+  q.first = ctx - q.tokens;
+  return q;
+}
+// A table entry as a page of the cache, -1 where it is none.
+HCR_HD int page_or_none(int page, int n_pages) { return page >= 0 && page < n_pages ? page : -1; }
+
+HCR_HD int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// ---- attention: 16-row tiles of a unit's rows (a sequence's window x group, or one token's group for listed
+// pages), tiles of 32 positions, and splits of the length into chunks of tiles
+constexpr int TILE = 32;
+constexpr int TILE_SHIFT = 5;
+constexpr int ATTN_WAVES = 4;  // waves of a work-group, taking its chunk's tiles in turn
+
+// How a call is cut, from the bounds of the batch alone (the host plans, the device follows).
+struct AttnPlan {
+  int q_tiles;     // 16-row tiles a wave holds
+  int row_blocks;  // work-groups over a unit's rows
+  int splits;      // work-groups over the length
+  int chunk;       // tiles of one split
+};
+AttnPlan attn_plan(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel);
+
+struct AttnArgs {
+  CacheArgs c;
+  BatchArgs b;
+  const uint16_t* q;
+  const int* sel;  // null: every page
+  int n_sel, heads, group, out_type;
+  float scale_hi, scale_lo;  // scale / ln 2 (probabilities are powers of two) in two parts
+  void* out;
+  float* part;  // [n_tokens * heads][splits][D], then (m, l) pairs [n_tokens * heads][splits]
+  AttnPlan plan;
+};
+int launch_attn(const AttnArgs& a, void* stream);
+
+// ---- append
+struct AppendArgs {
+  CacheArgs c;
+  BatchArgs b;
+  hcr_rows q, k, v;
+  int heads, type;
+  const float *q_norm, *k_norm, *rope;
+  float eps;
+  int rope_dim, rope_style;
+  uint16_t* q_out;
+};
+int launch_append(const AppendArgs& a, void* stream);
+
+// ---- scores and selection
+struct ScoreArgs {
+  CacheArgs c;
+  BatchArgs b;
+  const uint16_t* q;
+  int heads, group;
+  float* scores;
+  int stride;
+};
+int launch_block_scores(const ScoreArgs& a, void* stream);
+
+struct TopkArgs {
+  BatchArgs b;
+  const float* scores;
+  int stride, kv_heads, shift, n_sel, n_first, n_last;
+  int* sel;
+};
+int launch_block_topk(const TopkArgs& a, void* stream);
+
+}  // namespace hcr

@@ -1,4 +1,5 @@
-"""FP64 CPU reference ("oracle") of the BF16 hyper-connection read, its Q8_0 sibling and the skinny BF16 matvec.
+"""FP64 CPU reference ("oracle") of the BF16 hyper-connection read, its Q8_0 sibling, the skinny BF16 matvec
+and the paged key-value cache.
 
 TEST INFRASTRUCTURE. Only ``tests/``, ``__graft_entry__.smoke()`` and the
 ``cpu_baseline`` leg of ``bench.py`` may import, call or run anything in this
@@ -18,3 +19,4 @@ from .reference import (  # noqa: F401
 )
 from .q8_0 import dequantize_q8_0, hc_read_q8_0, quantize_q8_0  # noqa: F401,E402
 from .matvec import matvec_bf16  # noqa: F401,E402
+from . import paged  # noqa: F401,E402
