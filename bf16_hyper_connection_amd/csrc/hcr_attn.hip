@@ -15,8 +15,17 @@
 // three (the whole FP32 value) for float ones, where two would be the largest error of all (1.1e-6 of the result's
 // norm instead of 1.5e-7; the third costs matrix products that the loop has time for).
 //
-// The length is split over work-groups and their waves; waves join in LDS, splits in a second launch, each by
-// (m, l, O) -> (max, sum of l 2^(m - max), sum of O 2^(m - max)), in a fixed order.
+// Work: the tiles of all sequences, one behind the other, are cut into equal runs, one for each work-group that the
+// chip holds at once (AttnPlan), so that unlike lengths and loose bounds cost nothing; a run goes from one sequence
+// on to the next.  The waves of a work-group take its tiles in turn and join in LDS; sequences that lie in several
+// runs are joined by a second launch; each join is (m, l, O) -> (max, sum of l 2^(m - max), sum of O 2^(m - max)),
+// in a fixed order.
+//
+// Bound by the bytes of keys and values.  Measured on MI355X (graphs of calls,
+// inputs rotated): one sequence of 420,000 positions, 48 heads of 256 over 8, 2 tokens: 568 us, 6.1 TB/s (a 4 GiB
+// device copy moves 4.8); 64 sequences of 1,000 to 8,192, 32 heads of 128 over 8: 216 us, 5.6 TB/s.  36 rows of 4
+// sequences of up to 9,001: 50 us, 3.3 TB/s, of which the first loads' way, the parts' (9 MB written and read) and
+// the second launch take about 15.
 
 #include <float.h>
 #include <hip/hip_runtime.h>
@@ -72,59 +81,232 @@ __device__ __forceinline__ void store4(void* out, int type, size_t at, const f32
   }
 }
 
+// A barrier for LDS alone: loads on their way to registers stay on their way.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// The sequences 64 at a time, one per lane.
+__device__ __forceinline__ Seq lane_seq(const BatchArgs& b, int first, int lane) {
+  const int i = first + lane;
+  if (i >= b.n_seqs) return Seq{0, 0, 0};
+  return seq_of(b, b.q_start[i], b.q_start[i + 1], b.ctx_len[i]);
+}
+__device__ __forceinline__ int tiles_of(const Seq& s) {
+  return s.tokens ? max(ceil_div(s.first + s.tokens, TILE), 1) : 0;
+}
+// Inclusive prefix sum over the first n lanes.
+__device__ __forceinline__ int lane_prefix(int v, int lane, int n) {
+  for (int o = 1; o < min(n, 64); o *= 2) {
+    const int y = __shfl_up(v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+__device__ __forceinline__ Seq of_lane(const Seq& s, int l) {
+  return Seq{__builtin_amdgcn_readlane(s.row, l), __builtin_amdgcn_readlane(s.tokens, l),
+             __builtin_amdgcn_readlane(s.first, l)};
+}
+
+// A set of rows among the tiles of all: its sequence and token (listed pages), its tiles [first, first + tiles).
+struct Set {
+  Seq seq;
+  int b, token, first, tiles;  // b < 0: none
+};
+// The sequence whose tiles hold tile x, or (x < 0) the one that row `row` belongs to; *all: the tiles of all.
+__device__ __forceinline__ Set find_seq(const BatchArgs& b, int x_run, int row, int lane, const AttnPlan& p, int* run) {
+  const int B = b.n_seqs;
+  const Seq s0 = lane_seq(b, 0, lane);
+  const int n0 = tiles_of(s0), upto0 = lane_prefix(n0, lane, B);
+  int all = __builtin_amdgcn_readlane(upto0, min(B, 64) - 1);
+  for (int i = 64; i < B; i += 64) {
+    const int t = lane_prefix(tiles_of(lane_seq(b, i, lane)), lane, B - i);
+    all += __builtin_amdgcn_readlane(t, min(B - i, 64) - 1);
+  }
+  *run = run_tiles(p, all);
+  const int x = x_run * *run;
+  int before = 0;
+  for (int i = 0; i < B; i += 64) {
+    const Seq s = i == 0 ? s0 : lane_seq(b, i, lane);
+    const int n = i == 0 ? n0 : tiles_of(s);
+    const int upto = i == 0 ? upto0 : before + lane_prefix(n, lane, B - i);
+    const bool mine = x_run >= 0 ? upto - n <= x && x < upto : row >= s.row && row < s.row + s.tokens;
+    const unsigned long long at = __ballot(mine);
+    if (at) {
+      const int l = __ffsll(at) - 1;
+      return Set{of_lane(s, l), i + l, 0, __builtin_amdgcn_readlane(upto - n, l), __builtin_amdgcn_readlane(n, l)};
+    }
+    before = __builtin_amdgcn_readlane(upto, min(B - i, 64) - 1);
+  }
+  return Set{Seq{0, 0, 0}, -1, 0, 0, 0};
+}
+// The sequence that row `row` belongs to (b < 0: none).
+__device__ __forceinline__ Set seq_of_row(const BatchArgs& b, int row, int lane) {
+  for (int i = 0; i < b.n_seqs; i += 64) {
+    const Seq s = lane_seq(b, i, lane);
+    const unsigned long long at = __ballot(row >= s.row && row < s.row + s.tokens);
+    if (at) {
+      const int l = __ffsll(at) - 1;
+      const Seq q = of_lane(s, l);
+      return Set{q, i + l, row - q.row, 0, 0};
+    }
+  }
+  return Set{Seq{0, 0, 0}, -1, 0, 0, 0};
+}
+// The set that holds tile x_run * run, or (x_run < 0) row `row`.
+template <bool SEL>
+__device__ __forceinline__ Set find_set(const AttnArgs& a, int x_run, int row, int lane, int* run) {
+  if (!SEL) return find_seq(a.b, x_run, row, lane, a.plan, run);
+  const int each = a.n_sel << (a.c.shift - TILE_SHIFT);
+  *run = run_tiles(a.plan, a.b.n_tokens * each);
+  if (x_run >= 0) row = x_run * *run / each;
+  if (row >= a.b.n_tokens) return Set{Seq{0, 0, 0}, -1, 0, a.b.n_tokens * each, 0};
+  Set s = seq_of_row(a.b, row, lane);
+  s.first = row * each;
+  s.tiles = each;
+  return s;
+}
+// The set behind this one (tiles 0: none).
+template <bool SEL>
+__device__ __forceinline__ Set next_set(const AttnArgs& a, const Set& s, int lane) {
+  const int first = s.first + s.tiles;
+  if (SEL) {
+    const int row = first / s.tiles;
+    if (row >= a.b.n_tokens) return Set{Seq{0, 0, 0}, -1, 0, first, 0};
+    Set t = seq_of_row(a.b, row, lane);
+    t.first = first;
+    t.tiles = s.tiles;
+    return t;
+  }
+  for (int b = s.b + 1; b < a.b.n_seqs; ++b) {
+    const Seq q = seq_of(a.b, a.b.q_start[b], a.b.q_start[b + 1], a.b.ctx_len[b]);
+    if (q.tokens) return Set{q, b, 0, first, tiles_of(q)};
+  }
+  return Set{Seq{0, 0, 0}, -1, 0, first, 0};
+}
+
+// A set's tiles [lo, hi) (counted from its own first) in one work-group: its rows' part of the softmax.
 template <int D, int MT, bool SEL>
-__global__ __launch_bounds__(64 * ATTN_WAVES) void attn_part(AttnArgs a) {
-  constexpr int KS = D / 32, DT = D / 16, W = ATTN_WAVES;
+__device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int h, int rb, int lo, int hi, bool only,
+                                         size_t slot, size_t slots, uint4* lds) {
+  constexpr int KS = D / 32, DT = D / 16;
   const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int RT = a.plan.row_waves, TG = a.plan.groups;  // waves: TG groups over the tiles x RT over the rows
+  const int rt = wave % RT, tg = wave / RT;
+  const Seq& seq = set.seq;
+  const int b = set.b, token = set.token;
 
-  // work-group -> (split, sequence[, token], kv head, row block); the row blocks of one unit run on one XCD (its
-  // L2 then serves all but the first), the first splits, which every sequence has, come first
-  const int RB = a.plan.row_blocks;
-  const int turn = blockIdx.x / XCDS;
-  const int rb = turn % RB;
-  int u = turn / RB * XCDS + blockIdx.x % XCDS;
-  const int windows = SEL ? a.b.max_tokens : 1;
-  if (u >= a.plan.splits * a.b.n_seqs * windows * a.c.kv_heads) return;
-  const int h = u % a.c.kv_heads;
-  u /= a.c.kv_heads;
-  const int token = SEL ? u % windows : 0;
-  u /= windows;
-  const int b = u % a.b.n_seqs;
-  const int split = u / a.b.n_seqs;
-
-  const Seq seq = seq_of(a.b, a.b.q_start[b], a.b.q_start[b + 1], a.b.ctx_len[b]);
   const int G = a.group;
-  const int rows = SEL ? (token < seq.tokens ? G : 0) : seq.tokens * G;
-  const int r0 = rb * 16 * MT;
-  if (r0 >= rows) return;
-  const int r_last = min(r0 + 16 * MT, rows) - 1;
+  const int rows = SEL ? G : seq.tokens * G;
+  const int first_row = rb * RT * 16 * MT;
+  if (first_row >= rows) return;
+  // a wave behind the last row takes the last row again, and stores nothing
+  const int r0 = min(first_row + rt * 16 * MT, rows - 1);
+  const bool idle = first_row + rt * 16 * MT >= rows;
+  const int r_last = min(first_row + RT * 16 * MT, rows) - 1;
   // positions a row sees: [0, len)
   const int len_max = seq.first + (SEL ? token : r_last / G) + 1;
   const int len_min = seq.first + (SEL ? token : r0 / G) + 1;
   const int psh = a.c.shift - TILE_SHIFT;
-  const int tiles = SEL ? a.n_sel << psh : ceil_div(max(len_max, 0), TILE);
-  const int lo = split * a.plan.chunk, hi = min(lo + a.plan.chunk, tiles);
-  if (lo >= hi && a.plan.splits > 1) return;  // not joined
+  const int tiles = set.tiles;
 
-  // the lane's query row of each 16-row tile, its operand and its length
+  // ---- the tiles of this group, one after the other: lo + tg, + TG, ..., those without a visible position left
+  // out.  Page list: lane l holds entry `from` + l, as the page's number (-1: none) and its index in the sequence.
+  const int page = 1 << a.c.shift;
+  const int key_row = 8 * (li >> 2) + (li & 3);  // position of key tile 0's row li
+  int from = lo >> psh, number = -1, index = -1;
+  auto list = [&]() {
+    const int idx = from + lane;
+    number = -1;
+    index = idx;
+    if (SEL) {
+      index = idx < a.n_sel ? a.sel[((size_t)(seq.row + token) * a.c.kv_heads + h) * a.n_sel + idx] : -1;
+      if (index >= 0 && len_max > 0 && index <= (len_max - 1) >> a.c.shift)
+        number = page_or_none(a.b.table[(size_t)b * a.b.table_stride + index], a.c.n_pages);
+    } else if (idx << psh < tiles) {
+      number = page_or_none(a.b.table[(size_t)b * a.b.table_stride + idx], a.c.n_pages);
+    }
+  };
+  int tile = lo + tg, p0 = 0;
+  // operands: the tile's place is the same for the whole wave, the lane's place in it for the whole kernel
+  const char *kp = nullptr, *vp = nullptr;
+  const uint32_t k_lane = ((uint32_t)(lg << a.c.shift) + key_row) * 16, v_lane = (uint32_t)(lg * D + li) * 16;
+  const uint32_t k_step = 4u << a.c.shift << 4;  // 32 dimensions on
+  auto find = [&]() {  // the next tile with visible positions, from `tile` on: its first position and operands
+    for (; tile < hi; tile += TG) {
+      if ((tile >> psh) - from >= 64) {
+        from = tile >> psh;
+        list();
+      }
+      const int at = (tile >> psh) - from;
+      const int pn = __builtin_amdgcn_readlane(number, at);
+      const int off = (tile << TILE_SHIFT) & (page - 1);
+      p0 = (__builtin_amdgcn_readlane(index, at) << a.c.shift) + off;
+      if (pn < 0 || p0 >= len_max) continue;
+      const size_t base = head_base(a.c, pn, h);
+      kp = reinterpret_cast<const char*>(a.c.k + base + off * 8);
+      vp = reinterpret_cast<const char*>(a.c.v + base + off * D);
+      tile += TG;
+      return true;
+    }
+    return false;
+  };
+  uint4 kf[2][KS], vf[DT];
+  auto load_keys = [&]() {
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const char* at = kp + k * k_step;
+      kf[0][k] = ld16(at + k_lane);
+      kf[1][k] = ld16(at + k_lane + 4 * 16);
+    }
+  };
+  auto load_values = [&]() {
+#pragma unroll
+    for (int d = 0; d < DT; ++d) vf[d] = ld16(vp + v_lane + 16 * 16 * d);
+  };
+
+  // Keys of the next tile are loaded behind their last use in this one, values likewise, so that one of the two is
+  // always on its way while the other is worked on; the first ones go out ahead of the query rows' way through LDS.
+  list();
+  // the lane's query row of each 16-row tile and its length; the rows as operands in LDS, one copy for all groups
+  // (in registers they would push the loop's operands out)
+  uint4* lds_q = lds + (size_t)rt * MT * KS * 64 + lane;  // [RT][MT][KS][64]
   uint4 qf[MT][KS];
   int len[MT];
-  size_t rid[MT];
+  int rid[MT];  // row of q and out: under 2^30
   bool live[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int r = r0 + 16 * m + li;
-    live[m] = r < rows;
+    live[m] = !idle && r < rows;
     const int rr = min(r, rows - 1);
     const int t = SEL ? token : rr / G, g = SEL ? rr : rr % G;
     len[m] = seq.first + t + 1;
-    rid[m] = (size_t)(seq.row + t) * a.heads + h * G + g;
-    const uint16_t* qp = a.q + rid[m] * D + 8 * lg;
+    rid[m] = (seq.row + t) * a.heads + h * G + g;
+    if (tg == 0) {
 #pragma unroll
-    for (int k = 0; k < KS; ++k) qf[m][k] = ld16(qp + 32 * k);
+      for (int k = 0; k < KS; ++k) qf[m][k] = ld16(a.q + (size_t)rid[m] * D + 8 * lg + 32 * k);
+    }
   }
-
+  // row waves alone keep step, so that the first one's misses are the others' hits in L1 (36 rows of D = 256: 314
+  // against 342 us; all of them find the same tiles)
+  const bool together = TG == 1 && RT > 1;
+  bool more = find();
+  if (more && !idle) {
+    load_keys();
+    load_values();
+  }
+  if (tg == 0) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int k = 0; k < KS; ++k) lds_q[(m * KS + k) * 64] = qf[m][k];
+    }
+  }
+  lds_barrier();
   f32x4 acc[MT][DT];
   float mx[MT], sum[MT];
 #pragma unroll
@@ -135,256 +317,301 @@ __global__ __launch_bounds__(64 * ATTN_WAVES) void attn_part(AttnArgs a) {
     for (int d = 0; d < DT; ++d) acc[m][d] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  const int page = 1 << a.c.shift;
-  const int key_row = 8 * (li >> 2) + (li & 3);  // position of key tile 0's row li
-  for (int pb = lo >> psh; pb << psh < hi; pb += 64) {
-    // lane l: page pb + l of the list, as the page's number (-1: none) and its index in the sequence
-    const int idx = pb + lane;
-    int index = -1, number = -1;
-    if (SEL) {
-      if (idx < a.n_sel) index = a.sel[((size_t)(seq.row + token) * a.c.kv_heads + h) * a.n_sel + idx];
-      if (index >= 0 && index <= (len_max - 1) >> a.c.shift && len_max > 0)
-        number = page_or_none(a.b.table[(size_t)b * a.b.table_stride + index], a.c.n_pages);
-    } else {
-      index = idx;
-      if (idx << psh < tiles) number = page_or_none(a.b.table[(size_t)b * a.b.table_stride + idx], a.c.n_pages);
+  while (more) {
+    if (idle) {
+      more = find();
+      if (together) __builtin_amdgcn_s_barrier();
+      continue;
     }
-    const int end = min(hi, (pb + 64) << psh);
-    int tile = max(lo, pb << psh);
-    tile += (wave - (tile - lo)) & (W - 1);  // this wave's: lo + wave, + W, ...
-    for (; tile < end; tile += W) {
-      const int at = (tile >> psh) - pb;
-      const int pn = __builtin_amdgcn_readlane(number, at);
-      if (pn < 0) continue;
-      const int off = (tile << TILE_SHIFT) & (page - 1);
-      const int p0 = (__builtin_amdgcn_readlane(index, at) << a.c.shift) + off;
-      if (p0 >= len_max) continue;
-      const size_t base = head_base(a.c, pn, h);
-      const uint16_t* kp = a.c.k + base + ((size_t)(lg << a.c.shift) + off + key_row) * 8;
-      const uint16_t* vp = a.c.v + base + ((size_t)((off >> 3) + lg) * D + li) * 8;
-      uint4 kf[2][KS], vf[DT];
+    const int now = p0;
+    const bool whole = now + TILE <= len_min;
+    f32x4 s[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      s[m][0] = s[m][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        kf[0][k] = ld16(kp + ((size_t)(4 * k) << a.c.shift) * 8);
-        kf[1][k] = ld16(kp + ((size_t)(4 * k) << a.c.shift) * 8 + 4 * 8);
-      }
+        const bf16x8 qk = as_bf16x8(lds_q[(m * KS + k) * 64]);
 #pragma unroll
-      for (int d = 0; d < DT; ++d) vf[d] = ld16(vp + 16 * 8 * d);
-
-      const bool whole = p0 + TILE <= len_min;
-      if (!whole) {
-        // values behind the last visible position may be anything: zeros in their place (their
-        // probabilities are zero, but zero times NaN is not)
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          uint32_t w[4] = {vf[d].x, vf[d].y, vf[d].z, vf[d].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int p = p0 + 8 * lg + 2 * e;
-            w[e] = p + 1 < len_max ? w[e] : p < len_max ? w[e] & 0xFFFFu : 0u;
-          }
-          vf[d] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        float s[8], y[8];  // products, and as exponents of two
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          f32x4 c = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int k = 0; k < KS; ++k)
-            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(kf[t][k]), as_bf16x8(qf[m][k]), c, 0, 0, 0);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            s[4 * t + i] = c[i];
-            y[4 * t + i] = c[i] * a.scale_hi;
-          }
-        }
-        if (!whole) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = p0 + 8 * lg + i < len[m] ? y[i] : -INFINITY;
-        }
-        float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
-        top = rows_max(top);
-        if (__any(top > mx[m] + 8.f)) {
-          const float now = fmaxf(mx[m], top);
-          const float f = exp2_of(mx[m] - now);
-          mx[m] = now;
-          sum[m] *= f;
-#pragma unroll
-          for (int d = 0; d < DT; ++d) acc[m][d] *= f;
-        }
-        // exponents with the scale in two parts: one rounding, of the difference from the maximum
-        float p[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          p[i] = exp2_of(__builtin_fmaf(s[i], a.scale_hi, __builtin_fmaf(s[i], a.scale_lo, -mx[m])));
-        if (!whole) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) p[i] = p0 + 8 * lg + i < len[m] ? p[i] : 0.f;
-        }
-        sum[m] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-        uint4 ph, pl;
-        split_hi_lo(p, ph, pl);
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-          acc[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(vf[d]), as_bf16x8(ph), acc[m][d], 0, 0, 0);
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-          acc[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(vf[d]), as_bf16x8(pl), acc[m][d], 0, 0, 0);
-        if (a.out_type == HCR_F32) {
-          const uint4 pr = split_rest(p, ph, pl);
-#pragma unroll
-          for (int d = 0; d < DT; ++d)
-            acc[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(vf[d]), as_bf16x8(pr), acc[m][d], 0, 0, 0);
-        }
+        for (int t = 0; t < 2; ++t)
+          s[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(kf[t][k]), qk, s[m][t], 0, 0, 0);
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
+    more = find();
+    if (together) __builtin_amdgcn_s_barrier();
+    if (more) load_keys();
+    __builtin_amdgcn_sched_barrier(0);
+
+    if (!whole) {
+      // values behind the last visible position may be anything: zeros in their place (their
+      // probabilities are zero, but zero times NaN is not)
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        uint32_t w[4] = {vf[d].x, vf[d].y, vf[d].z, vf[d].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int p = now + 8 * lg + 2 * e;
+          w[e] = p + 1 < len_max ? w[e] : p < len_max ? w[e] & 0xFFFFu : 0u;
+        }
+        vf[d] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      float y[8];  // as exponents of two
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = s[m][i >> 2][i & 3] * a.scale_hi;
+      if (!whole) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = now + 8 * lg + i < len[m] ? y[i] : -INFINITY;
+      }
+      float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
+      top = rows_max(top);
+      if (__any(top > mx[m] + 8.f)) {
+        const float high = fmaxf(mx[m], top);
+        const float f = exp2_of(mx[m] - high);
+        mx[m] = high;
+        sum[m] *= f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) acc[m][d] *= f;
+      }
+      // exponents with the scale in two parts: one rounding, of the difference from the maximum
+      float p[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float v = s[m][i >> 2][i & 3];
+        p[i] = exp2_of(__builtin_fmaf(v, a.scale_hi, __builtin_fmaf(v, a.scale_lo, -mx[m])));
+      }
+      if (!whole) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = now + 8 * lg + i < len[m] ? p[i] : 0.f;
+      }
+      sum[m] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+      uint4 ph, pl;
+      split_hi_lo(p, ph, pl);
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+        acc[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(vf[d]), as_bf16x8(ph), acc[m][d], 0, 0, 0);
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+        acc[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(vf[d]), as_bf16x8(pl), acc[m][d], 0, 0, 0);
+      if (a.out_type == HCR_F32) {
+        const uint4 pr = split_rest(p, ph, pl);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+          acc[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(vf[d]), as_bf16x8(pr), acc[m][d], 0, 0, 0);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (more) load_values();
+    __builtin_amdgcn_sched_barrier(0);
   }
 #pragma unroll
   for (int m = 0; m < MT; ++m) sum[m] = rows_sum(sum[m]);
 
-  // the waves joined by halves: the upper half writes, the lower half adds
-  __shared__ f32x4 lds_acc[W / 2][MT * DT][64];
-  __shared__ float lds_ml[W / 2][MT][2][64];
+  // the groups joined: every wave leaves its state in LDS and takes its share of its row tile's values
+  // (the values where the query rows were, which nobody reads behind the first barrier here)
+  f32x4* lds_acc = reinterpret_cast<f32x4*>(lds);                            // [TG][RT][MT * DT][64]
+  float* lds_m = reinterpret_cast<float*>(lds_acc + TG * RT * MT * DT * 64);  // [TG][RT][MT][16]
+  float* lds_l = lds_m + TG * RT * MT * 16;
+  float w_own[MT];  // what this wave's values weigh in the sum
+  if (TG > 1) {
 #pragma unroll
-  for (int half = W / 2; half >= 1; half /= 2) {
-    if (wave >= half && wave < 2 * half) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        lds_ml[wave - half][m][0][lane] = mx[m];
-        lds_ml[wave - half][m][1][lane] = sum[m];
-#pragma unroll
-        for (int d = 0; d < DT; ++d) lds_acc[wave - half][m * DT + d][lane] = acc[m][d];
+    for (int m = 0; m < MT; ++m) {
+      if (lg == 0) {
+        lds_m[(wave * MT + m) * 16 + li] = mx[m];
+        lds_l[(wave * MT + m) * 16 + li] = sum[m];
       }
     }
     __syncthreads();
-    if (wave < half) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const float m2 = lds_ml[wave][m][0][lane], l2 = lds_ml[wave][m][1][lane];
-        const float now = fmaxf(mx[m], m2);
-        const float f1 = exp2_of(mx[m] - now), f2 = exp2_of(m2 - now);
-        mx[m] = now;
-        sum[m] = sum[m] * f1 + l2 * f2;
+    for (int m = 0; m < MT; ++m) {
+      float top = -FLT_MAX, total = 0.f;
+      for (int g0 = 0; g0 < TG; g0 += 4) {
+        float gm[4], gl[4];
 #pragma unroll
-        for (int d = 0; d < DT; ++d) acc[m][d] = acc[m][d] * f1 + lds_acc[wave][m * DT + d][lane] * f2;
+        for (int i = 0; i < 4; ++i) {
+          const int at = ((min(g0 + i, TG - 1) * RT + rt) * MT + m) * 16 + li;
+          gm[i] = lds_m[at];
+          gl[i] = g0 + i < TG ? lds_l[at] : 0.f;
+        }
+        const float high = fmaxf(fmaxf(fmaxf(gm[0], gm[1]), fmaxf(gm[2], gm[3])), top);
+        total *= exp2_of(top - high);
+        top = high;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) total += gl[i] * exp2_of(gm[i] - top);
       }
+      w_own[m] = exp2_of(mx[m] - top);
+      mx[m] = top;
+      sum[m] = total;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) lds_acc[(wave * MT * DT + m * DT + d) * 64 + lane] = acc[m][d] * w_own[m];
     }
     __syncthreads();
   }
-  if (wave != 0) return;
 
-  const size_t all = (size_t)a.b.n_tokens * a.heads;
+  const int slot_rows = RT * MT * 16;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     if (!live[m]) continue;
-    if (a.plan.splits == 1) {
-      const float f = sum[m] > 0.f ? 1.f / sum[m] : 0.f;
+    const float f = !only ? 1.f : sum[m] > 0.f ? 1.f / sum[m] : 0.f;
+    const size_t at = slot * slot_rows + (rt * MT + m) * 16 + li;
+    auto put = [&](int d, f32x4 o) {
+      if (only)  // nothing to join: the outputs themselves
+        store4(a.out, a.out_type, (size_t)rid[m] * D + 16 * d + 4 * lg, o * f);
+      else
+        *reinterpret_cast<f32x4*>(a.part + at * D + 16 * d + 4 * lg) = o;
+    };
+    if (TG == 1) {
 #pragma unroll
-      for (int d = 0; d < DT; ++d) store4(a.out, a.out_type, rid[m] * D + 16 * d + 4 * lg, acc[m][d] * f);
+      for (int d = 0; d < DT; ++d) put(d, acc[m][d]);
     } else {
-      const size_t at = rid[m] * a.plan.splits + split;
+      for (int d = tg; d < DT; d += TG) {
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+        for (int g0 = 0; g0 < TG; g0 += 4) {
+          f32x4 v[4];
 #pragma unroll
-      for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(a.part + at * D + 16 * d + 4 * lg) = acc[m][d];
-      if (lg == 0) *reinterpret_cast<f32x2*>(a.part + all * a.plan.splits * D + at * 2) = f32x2{mx[m], sum[m]};
+          for (int i = 0; i < 4; ++i) v[i] = lds_acc[((min(g0 + i, TG - 1) * RT + rt) * MT * DT + m * DT + d) * 64 + lane];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o += g0 + i < TG ? v[i] : f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+        put(d, o);
+      }
     }
+    if (!only && tg == 0 && lg == 0)
+      *reinterpret_cast<f32x2*>(a.part + slots * slot_rows * D + at * 2) = f32x2{mx[m], sum[m]};
   }
 }
 
-// One row's splits joined: D / 4 lanes hold a row of 4 values each, the groups of lanes take the splits in turn
-// and join in LDS, in a fixed order.
+template <int D, int MT, bool SEL>
+__global__ __launch_bounds__(64 * attn_waves(D, MT)) void attn_part(AttnArgs a) {
+  extern __shared__ uint4 lds[];
+  const int lane = threadIdx.x & 63;
+  // work-group -> (run, kv head, row block); the row blocks of one run sit on one XCD (its L2 then serves all but
+  // the first)
+  const int RB = a.plan.row_blocks;
+  const int turn = blockIdx.x / XCDS;
+  const int rb = turn % RB;
+  const int u = turn / RB * XCDS + blockIdx.x % XCDS;
+  const int h = u % a.c.kv_heads, item = u / a.c.kv_heads;
+  if (item >= a.plan.items) return;
+  int run;
+  Set set = find_set<SEL>(a, item, 0, lane, &run);
+  const int begin = item * run;
+  const size_t slots = (size_t)a.c.kv_heads * RB * a.plan.items * 2;
+  const size_t slot = ((size_t)h * RB + rb) * a.plan.items * 2;
+  while (set.tiles > 0 && set.first < begin + run) {
+    if (set.b >= 0) {
+      const int lo = max(begin - set.first, 0), hi = min(begin + run - set.first, set.tiles);
+      attn_run<D, MT, SEL>(a, set, h, rb, lo, hi, lo == 0 && hi == set.tiles, slot + part_slot(item, run, set.first),
+                           slots, lds);
+    }
+    if (set.first + set.tiles >= begin + run) break;
+    set = next_set<SEL>(a, set, lane);
+    __syncthreads();  // the LDS of the set before is free
+  }
+}
+
+// One row's parts joined: D / 4 lanes hold a row of 4 values each, the groups of lanes take the parts in turn and
+// join in LDS, in a fixed order.
 template <int D, bool SEL>
 __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
-  constexpr int LANES = D / 4, GROUPS = 256 / LANES;
-  const int l = threadIdx.x % LANES, grp = threadIdx.x / LANES;
-  const int hq = blockIdx.x % a.heads, bt = blockIdx.x / a.heads;
-  const int t = bt % a.b.max_tokens, b = bt / a.b.max_tokens;
-  const Seq seq = seq_of(a.b, a.b.q_start[b], a.b.q_start[b + 1], a.b.ctx_len[b]);
-  if (t >= seq.tokens) return;
-  const size_t rid = (size_t)(seq.row + t) * a.heads + hq;
-  const size_t all = (size_t)a.b.n_tokens * a.heads;
-  const int len = max(seq.first + t + 1, 0);
-  const int n = SEL ? a.plan.splits : min(a.plan.splits, ceil_div(ceil_div(len, TILE), a.plan.chunk));
-  const float* ml = a.part + all * a.plan.splits * D + rid * a.plan.splits * 2;
-  const float* pa = a.part + rid * a.plan.splits * D + 4 * l;
+  constexpr int LANES = D / 4;
+  const int GROUPS = blockDim.x / LANES;
+  const int l = threadIdx.x % LANES, grp = threadIdx.x / LANES, lane = threadIdx.x & 63;
+  const int hq = blockIdx.x % a.heads, row = blockIdx.x / a.heads;
+  int run;
+  const Set set = find_set<SEL>(a, -1, row, lane, &run);
+  if (set.b < 0) return;
+  const int n = run_parts(set.first, set.tiles, run);
+  if (n == 1) return;  // the row is out already
+  const int h = hq / a.group, g0 = hq % a.group;
+  const int r = SEL ? g0 : (row - set.seq.row) * a.group + g0;  // of the set's rows
+  const int slot_rows = attn_rows(a.plan);
+  const size_t slots = (size_t)a.c.kv_heads * a.plan.row_blocks * a.plan.items * 2;
+  const size_t slot = ((size_t)h * a.plan.row_blocks + r / slot_rows) * a.plan.items * 2;
+  const int part0 = set.first / run;
+  const float* pa = a.part + (slot * slot_rows + r % slot_rows) * D + 4 * l;
+  const float* ml = a.part + slots * slot_rows * D + (slot * slot_rows + r % slot_rows) * 2;
   float mx = -FLT_MAX, sum = 0.f;
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int s = grp; s < n; s += GROUPS) {
-    const f32x2 v = ld2(ml + 2 * s);
-    const f32x4 o = ld4(pa + (size_t)s * D);
-    const float now = fmaxf(mx, v[0]);
-    const float f1 = exp2_of(mx - now), f2 = exp2_of(v[0] - now);
+  for (int s0 = grp; s0 < n; s0 += 4 * GROUPS) {
+    f32x2 v[4];
+    f32x4 o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // four at a time on their way; past the end the last one, as nothing
+      const int s = s0 + i * GROUPS;
+      const size_t to = (size_t)part_slot(part0 + min(s, n - 1), run, set.first) * slot_rows;
+      v[i] = ld2(ml + to * 2);
+      o[i] = ld4(pa + to * D);
+      if (s >= n) v[i] = f32x2{-FLT_MAX, 0.f};
+    }
+    float now = mx;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) now = fmaxf(now, v[i][0]);
+    const float f = exp2_of(mx - now);
     mx = now;
-    sum = sum * f1 + v[1] * f2;
-    acc = acc * f1 + o * f2;
+    sum *= f;
+    acc *= f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float w = s0 + i * GROUPS < n ? exp2_of(v[i][0] - now) : 0.f;
+      sum += v[i][1] * w;
+      acc += o[i] * w;
+    }
   }
   __shared__ f32x4 lds_acc[256];
-  __shared__ f32x2 lds_ml[GROUPS];
+  __shared__ f32x2 lds_ml[256 / LANES];
   lds_acc[threadIdx.x] = acc;
   if (l == 0) lds_ml[grp] = f32x2{mx, sum};
   __syncthreads();
   if (grp != 0) return;
-  float top = -FLT_MAX;
-#pragma unroll
-  for (int g = 0; g < GROUPS; ++g) top = fmaxf(top, lds_ml[g][0]);
+  mx = -FLT_MAX;
+  for (int g = 0; g < GROUPS; ++g) mx = fmaxf(mx, lds_ml[g][0]);
   sum = 0.f;
   acc = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
   for (int g = 0; g < GROUPS; ++g) {
-    const float f = exp2_of(lds_ml[g][0] - top);
+    const float f = exp2_of(lds_ml[g][0] - mx);
     sum += lds_ml[g][1] * f;
     acc += lds_acc[g * LANES + l] * f;
   }
   const float f = sum > 0.f ? 1.f / sum : 0.f;
-  store4(a.out, a.out_type, rid * D + 4 * l, acc * f);
+  store4(a.out, a.out_type, ((size_t)row * a.heads + hq) * D + 4 * l, acc * f);
 }
 
 namespace {
 
 template <int D, int MT, bool SEL>
 void run_part(const AttnArgs& a, int grid, hipStream_t st) {
-  hipLaunchKernelGGL((attn_part<D, MT, SEL>), dim3(grid), dim3(64 * ATTN_WAVES), 0, st, a);
+  hipLaunchKernelGGL((attn_part<D, MT, SEL>), dim3(grid), dim3(64 * a.plan.row_waves * a.plan.groups),
+                     attn_lds(D, a.plan), st, a);
 }
 template <int D, bool SEL>
-void run_part_rows(const AttnArgs& a, int grid, hipStream_t st) {
-  if (a.plan.q_tiles == 1) return run_part<D, 1, SEL>(a, grid, st);
-  if (D == 256 || a.plan.q_tiles == 2) return run_part<D, 2, SEL>(a, grid, st);
-  if constexpr (D != 256) return run_part<D, 4, SEL>(a, grid, st);
-}
-template <bool SEL>
 void run_attn(const AttnArgs& a, int grid, int join_grid, hipStream_t st) {
-  const bool join = a.plan.splits > 1;
-  switch (a.c.head_dim) {
-    case 64:
-      run_part_rows<64, SEL>(a, grid, st);
-      if (join) hipLaunchKernelGGL((attn_join<64, SEL>), dim3(join_grid), dim3(256), 0, st, a);
-      break;
-    case 128:
-      run_part_rows<128, SEL>(a, grid, st);
-      if (join) hipLaunchKernelGGL((attn_join<128, SEL>), dim3(join_grid), dim3(256), 0, st, a);
-      break;
-    default:
-      run_part_rows<256, SEL>(a, grid, st);
-      if (join) hipLaunchKernelGGL((attn_join<256, SEL>), dim3(join_grid), dim3(256), 0, st, a);
+  // a wave a row where rows have few parts, four where many
+  const int join = a.plan.items > 2 * (SEL ? a.b.n_tokens : a.b.n_seqs) ? 256 : 64;
+  if (a.plan.q_tiles == 1) {
+    run_part<D, 1, SEL>(a, grid, st);
+  } else if constexpr (D != 256) {
+    run_part<D, 2, SEL>(a, grid, st);
   }
+  if (join_grid) hipLaunchKernelGGL((attn_join<D, SEL>), dim3(join_grid), dim3(join), 0, st, a);
 }
 
 }  // namespace
 
 int launch_attn(const AttnArgs& a, void* stream) {
   const AttnPlan& p = a.plan;
-  const int units = p.splits * a.b.n_seqs * (a.sel ? a.b.max_tokens : 1) * a.c.kv_heads;
-  const int grid = ceil_div(units, XCDS) * XCDS * p.row_blocks;
-  const int join_grid = a.b.n_seqs * a.b.max_tokens * a.heads;
+  const int grid = ceil_div(p.items * a.c.kv_heads, XCDS) * XCDS * p.row_blocks;
+  const int join_grid = attn_joins(p, a.n_sel << (a.c.shift - TILE_SHIFT), a.b.n_tokens) ? a.b.n_tokens * a.heads : 0;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-  if (a.sel)
-    run_attn<true>(a, grid, join_grid, st);
-  else
-    run_attn<false>(a, grid, join_grid, st);
+  switch (a.c.head_dim) {
+    case 64: a.sel ? run_attn<64, true>(a, grid, join_grid, st) : run_attn<64, false>(a, grid, join_grid, st); break;
+    case 128: a.sel ? run_attn<128, true>(a, grid, join_grid, st) : run_attn<128, false>(a, grid, join_grid, st); break;
+    default: a.sel ? run_attn<256, true>(a, grid, join_grid, st) : run_attn<256, false>(a, grid, join_grid, st);
+  }
   return hipGetLastError() == hipSuccess ? HCR_OK : HCR_EHIP;
 }
 

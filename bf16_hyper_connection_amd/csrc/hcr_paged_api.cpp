@@ -66,7 +66,7 @@ int check_bounds(const CacheArgs& c, const hcr_batch* in, int heads, BatchArgs* 
   if (b->n_seqs == 0 || b->max_tokens == 0) return 1;
   // rows and work-groups stay inside 32 bits
   if ((long long)b->n_tokens * heads > GRID_MAX || (long long)b->n_seqs * b->max_tokens > GRID_MAX / heads ||
-      (long long)b->n_seqs * b->table_stride > GRID_MAX * 2)
+      (long long)b->n_seqs * ceil_div(b->max_ctx, TILE) > GRID_MAX)
     return HCR_EINVAL;
   return HCR_OK;
 }
@@ -88,14 +88,13 @@ int check_rows(const hcr_rows* r, int type, int n_tokens, int heads, int head_di
   return HCR_OK;
 }
 
-long long attn_grid(const CacheArgs& c, const BatchArgs& b, const AttnPlan& p, bool listed) {
-  const long long units = (long long)p.splits * b.n_seqs * (listed ? b.max_tokens : 1) * c.kv_heads;
-  return (units + XCDS - 1) / XCDS * XCDS * p.row_blocks;
+long long attn_grid(const CacheArgs& c, const AttnPlan& p) {
+  return ((long long)p.items * c.kv_heads + XCDS - 1) / XCDS * XCDS * p.row_blocks;
 }
 
-size_t scratch_of(const CacheArgs& c, const BatchArgs& b, int heads, const AttnPlan& p) {
-  if (p.splits == 1) return 0;
-  return align256((size_t)b.n_tokens * heads * p.splits * (c.head_dim + 2) * 4);
+size_t scratch_of(const CacheArgs& c, const BatchArgs& b, int n_sel, const AttnPlan& p) {
+  if (!attn_joins(p, n_sel << (c.shift - TILE_SHIFT), b.n_tokens)) return 0;
+  return align256((size_t)c.kv_heads * p.row_blocks * p.items * 2 * attn_rows(p) * (c.head_dim + 2) * 4);
 }
 
 int attn(hcr_cache_t h, const hcr_batch* batch, int heads, double scale, const void* q, const int* sel, int n_sel,
@@ -110,12 +109,13 @@ int attn(hcr_cache_t h, const hcr_batch* batch, int heads, double scale, const v
   if (!(scale > -1e30 && scale < 1e30)) return HCR_EINVAL;  // NaN and infinite too
   if (n_sel < 0 || (long long)n_sel << c.shift > GRID_MAX) return HCR_EINVAL;
   if (rc == 1) return HCR_OK;
+  if (((long long)n_sel << c.shift) / TILE * a.b.n_tokens > GRID_MAX) return HCR_EINVAL;  // tiles, in 32 bits
   if (!q || !out) return HCR_EINVAL;
   if (const int e = check_arrays(a.b)) return e;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(sel, 4) || !aligned(scratch, 256)) return HCR_EALIGN;
   a.plan = attn_plan(c, a.b, heads, n_sel);
-  if (attn_grid(c, a.b, a.plan, n_sel > 0) > GRID_MAX) return HCR_EINVAL;
-  const size_t need = scratch_of(c, a.b, heads, a.plan);
+  if (attn_grid(c, a.plan) > GRID_MAX) return HCR_EINVAL;
+  const size_t need = scratch_of(c, a.b, n_sel, a.plan);
   if (need && (!scratch || scratch_bytes < need)) return HCR_ESCRATCH;
   const size_t values = (size_t)a.b.n_tokens * heads * c.head_dim;
   const Span so = span(out, values * (out_type == HCR_F32 ? 4 : 2)), sq = span(q, values * 2);
@@ -142,22 +142,39 @@ int attn(hcr_cache_t h, const hcr_batch* batch, int heads, double scale, const v
 
 }  // namespace
 
+// Measured on MI355X, 8 kv heads, graphs of calls on rotated inputs (us a call):
+//   row tiles  two 16-row tiles a wave for D = 128 from 17 rows on: 24 rows 154 against 160, 64 rows 161 against 185
+//              (D = 64: 92 against 90, and D = 256 has no registers for it)
+//   waves      8 a work-group, one work-group a CU, for long sequences (D = 256, one sequence of 420,000: 568
+//              against 575 with 4; 64 of up to 8,192, D = 128: 216 against 218); 4, two work-groups a CU, where no
+//              sequence is longer than 2,048 (64 of up to 300: 28 against 34; one of 2,000, D = 256: 13.4
+//              against 14.5), since a short one is mostly the wait for its first loads
+//   rows       several row waves, D = 256: one group, as many work-groups as fit a CU (36 rows: 314 against 432
+//              with two groups), four row waves at most (96 rows: 484 against 544 with six in one work-group)
+//   lists      one work-group a list where there are lists enough, and nothing to join (32 tokens: 52 against 56)
 AttnPlan attn_plan(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel) {
+  constexpr int CUS = 256, SHORT = 64;  // tiles
   AttnPlan p{};
   const int group = heads / c.kv_heads;
   const int rows = n_sel ? group : b.max_tokens * group;
-  p.q_tiles = rows <= 16 ? 1 : rows <= 32 || c.head_dim == 256 ? 2 : 4;
-  p.row_blocks = ceil_div(rows, 16 * p.q_tiles);
+  const bool wide = c.head_dim == 256;
+  p.q_tiles = c.head_dim == 128 && rows > 16 ? 2 : 1;
+  const int row_tiles = ceil_div(rows, 16 * p.q_tiles);
+  p.row_blocks = ceil_div(row_tiles, wide ? 4 : 8);
+  p.row_waves = ceil_div(row_tiles, p.row_blocks);
   const int tiles = n_sel ? n_sel << (c.shift - TILE_SHIFT) : ceil_div(b.max_ctx, TILE);
-  const long long units = (long long)b.n_seqs * c.kv_heads * p.row_blocks * (n_sel ? b.max_tokens : 1);
-  const int fill = c.head_dim == 256 ? 512 : 1024;  // work-groups that the chip holds at once
-  long long splits = (fill + units - 1) / units;
-  const int most = ceil_div(tiles, 2 * ATTN_WAVES);  // two tiles of a wave at least
-  if (splits > most) splits = most;
-  if (splits < 1) splits = 1;
-  p.chunk = ceil_div(tiles, (int)splits);
-  if (p.chunk < 1) p.chunk = 1;
-  p.splits = tiles ? ceil_div(tiles, p.chunk) : 1;
+  const int waves = !n_sel && tiles <= SHORT ? 4 : 8;
+  p.groups = (wide && p.row_waves > 1) || p.row_waves > waves ? 1 : waves / p.row_waves;
+  if (p.groups > tiles) p.groups = tiles > 0 ? tiles : 1;
+  p.least = p.groups;
+  const int units = c.kv_heads * p.row_blocks;
+  const int fill = wide && p.row_waves > 1 ? CUS * (8 / p.row_waves) : CUS * (8 / waves);
+  const long long sets = n_sel ? b.n_tokens : b.n_seqs;
+  const long long most = (sets * (tiles > 0 ? tiles : 1) + p.least - 1) / p.least;
+  long long items = fill / units;
+  if (n_sel) items = items > sets ? items / sets * sets : sets;
+  if (items > most) items = most;
+  p.items = items > 1 ? (int)items : 1;
   return p;
 }
 
@@ -246,9 +263,9 @@ int hcr_cache_append(hcr_cache_t h, const hcr_batch* batch, int heads, int type,
 size_t hcr_attn_scratch_bytes(hcr_cache_t h, const hcr_batch* batch, int heads, int n_sel) {
   BatchArgs b;
   if (!h || check_bounds(h->args, batch, heads, &b) != HCR_OK || n_sel < 0 ||
-      (long long)n_sel << h->args.shift > GRID_MAX)
+      (long long)n_sel << h->args.shift > GRID_MAX / b.n_tokens * TILE)
     return 0;
-  return scratch_of(h->args, b, heads, attn_plan(h->args, b, heads, n_sel));
+  return scratch_of(h->args, b, n_sel, attn_plan(h->args, b, heads, n_sel));
 }
 
 int hcr_attn(hcr_cache_t c, const hcr_batch* batch, int heads, double scale, const void* q, int out_type, void* out,

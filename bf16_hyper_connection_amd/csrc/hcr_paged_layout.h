@@ -76,15 +76,45 @@ HCR_HD int ceil_div(int a, int b) { return (a + b - 1) / b; }
 // pages), tiles of 32 positions, and splits of the length into chunks of tiles
 constexpr int TILE = 32;
 constexpr int TILE_SHIFT = 5;
-constexpr int ATTN_WAVES = 4;  // waves of a work-group, taking its chunk's tiles in turn
+// Waves of a work-group at most: what its registers leave room for on a CU (one 16-row tile of D = 256 takes 243
+// of 512 registers of a lane, of D <= 128 at most 128, two tiles of D <= 128 up to 216).
+constexpr int attn_waves(int D, int q_tiles) { return D > 64 || q_tiles > 1 ? 8 : 16; }
 
-// How a call is cut, from the bounds of the batch alone (the host plans, the device follows).
+// How a call is cut.  Its sets of rows (a sequence's window; one token for listed pages) have their tiles one set
+// behind the other, and the work-groups of a kv head and row block take equal runs of them, whatever set they belong
+// to: as many work-groups as the chip holds at once, none with more to do than another, however unlike the lengths
+// are and however far below the bounds.  The host fixes the number of work-groups, the device the run's length.
 struct AttnPlan {
   int q_tiles;     // 16-row tiles a wave holds
-  int row_blocks;  // work-groups over a unit's rows
-  int splits;      // work-groups over the length
-  int chunk;       // tiles of one split
+  int row_waves;   // waves of a work-group over the rows
+  int groups;      // waves of a work-group over its tiles, for each of them
+  int row_blocks;  // work-groups over a set's rows
+  int items;       // work-groups over the tiles
+  int least;       // tiles that are worth a work-group
 };
+HCR_HD int attn_rows(const AttnPlan& p) { return p.row_waves * p.q_tiles * 16; }  // of a work-group
+// Tiles of one run, from those of all sets (every set has one at least: a set without positions writes its zeros).
+HCR_HD int run_tiles(const AttnPlan& p, int tiles_of_all) {
+  const int even = ceil_div(tiles_of_all, p.items);
+  return even > p.least ? even : p.least;
+}
+// The runs that a set's tiles [first, first + tiles) lie in: a row's parts, to be joined where there are several.
+// A run has two places for parts: of the set that began before it, and of the set that goes on behind it.
+HCR_HD int run_parts(int first, int tiles, int run) { return (first + tiles - 1) / run - first / run + 1; }
+HCR_HD int part_slot(int run_index, int run, int first) { return 2 * run_index + (first >= run_index * run); }
+// Whether a set may have several parts, to be joined by a second launch (listed pages, whose lengths the host knows:
+// not where runs are whole lists).
+HCR_HD bool attn_joins(const AttnPlan& p, int list_tiles, int n_tokens) {
+  if (list_tiles) return p.items > 1 && run_tiles(p, list_tiles * n_tokens) % list_tiles;
+  return p.items > 1;
+}
+// Bytes of LDS of a work-group: its query rows, in their place what its groups join in, and the groups' (m, l).
+HCR_HD int attn_lds_values(int D, const AttnPlan& p) {
+  return attn_rows(p) * D * (p.groups > 1 ? p.groups * 4 : 2);
+}
+HCR_HD int attn_lds(int D, const AttnPlan& p) {
+  return attn_lds_values(D, p) + (p.groups > 1 ? p.groups * attn_rows(p) * 8 : 0);
+}
 AttnPlan attn_plan(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel);
 
 struct AttnArgs {
@@ -95,7 +125,7 @@ struct AttnArgs {
   int n_sel, heads, group, out_type;
   float scale_hi, scale_lo;  // scale / ln 2 (probabilities are powers of two) in two parts
   void* out;
-  float* part;  // [n_tokens * heads][splits][D], then (m, l) pairs [n_tokens * heads][splits]
+  float* part;  // [kv_heads][row_blocks][items][2][rows][D], then (m, l) pairs [kv_heads][row_blocks][items][2][rows]
   AttnPlan plan;
 };
 int launch_attn(const AttnArgs& a, void* stream);

@@ -69,12 +69,13 @@ static const char* check_cells() {
   return nullptr;
 }
 
-// A plan covers every row and every tile, and the device's walk over it (as in the kernel) visits each tile of a
-// split once, in its waves' turns, never one outside.
+// A plan covers every row; the items of any lengths fit its bound and cover every tile once; LDS fits a CU.
 static const char* check_plans() {
+  unsigned seed = 1;
+  auto rnd = [&](int n) { return int((seed = seed * 1664525u + 1013904223u) >> 8) % n; };
   for (int D : {64, 128, 256})
     for (int page : {32, 64, 256})
-      for (int kv : {1, 8})
+      for (int kv : {1, 3, 8})
         for (int group : {1, 6, 16, 33, 64})
           for (int seqs : {1, 3, 64, 1000})
             for (int tokens : {1, 4, 100})
@@ -84,32 +85,38 @@ static const char* check_plans() {
                   const BatchArgs b{nullptr, nullptr, nullptr, ctx / page + 1, seqs, seqs * tokens, tokens, ctx};
                   const AttnPlan p = attn_plan(c, b, kv * group, n_sel);
                   const int rows = n_sel ? group : tokens * group;
-                  CHECK(p.q_tiles == 1 || p.q_tiles == 2 || (p.q_tiles == 4 && D != 256));
-                  CHECK(p.row_blocks * p.q_tiles * 16 >= rows && (p.row_blocks - 1) * p.q_tiles * 16 < rows);
-                  const int tiles = n_sel ? n_sel * (page / TILE) : (ctx + TILE - 1) / TILE;
-                  CHECK(p.splits >= 1 && p.chunk >= 1 && (long long)p.splits * p.chunk >= tiles);
-                  CHECK(p.splits == 1 || (p.splits - 1) * p.chunk < tiles);
+                  CHECK(p.q_tiles == 1 || (p.q_tiles == 2 && D != 256));
+                  CHECK(p.row_waves * p.groups <= attn_waves(D, p.q_tiles) && p.groups >= 1 && p.row_waves >= 1);
+                  CHECK(p.row_blocks * attn_rows(p) >= rows && (p.row_blocks - 1) * attn_rows(p) < rows);
+                  CHECK(attn_lds(D, p) <= 160 * 1024 && attn_lds(D, p) >= attn_rows(p) * D * 2);
+                  CHECK(p.least >= 1 && p.items >= 1);
+                  for (int turn = 0; turn < 3; ++turn) {  // lengths: all the longest, random, one long
+                    const int sets = n_sel ? seqs * tokens : seqs;
+                    if (sets > 2000) continue;
+                    std::vector<int> t(sets);
+                    const int most = n_sel ? n_sel * (page / TILE) : ceil_div(ctx, TILE);
+                    int all = 0;
+                    for (int& x : t) {
+                      x = n_sel || turn == 0 ? most : turn == 1 ? rnd(most + 1) : &x == &t[0] ? most : 0;
+                      if (x < 1) x = 1;
+                      all += x;
+                    }
+                    const int run = run_tiles(p, all);
+                    CHECK(run >= 1 && (long long)run * p.items >= all);
+                    std::vector<char> used(2 * p.items);
+                    int first = 0;
+                    for (int x : t) {  // every part of every set has a place of its own
+                      const int n = run_parts(first, x, run);
+                      CHECK(n >= 1 && (n == 1 || attn_joins(p, n_sel * (page / TILE), sets)));
+                      for (int k = 0; k < n && n > 1; ++k) {
+                        const int slot = part_slot(first / run + k, run, first);
+                        CHECK(slot >= 0 && slot < 2 * p.items && !used[slot]);
+                        used[slot] = 1;
+                      }
+                      first += x;
+                    }
+                  }
                 }
-  for (int psh : {0, 1, 3})
-    for (int chunk : {1, 3, 8, 100, 700})
-      for (int tiles : {1, 5, 8, 150, 1500}) {
-        std::vector<int> seen(tiles);
-        for (int lo = 0; lo < tiles; lo += chunk) {
-          const int hi = lo + chunk < tiles ? lo + chunk : tiles;
-          for (int wave = 0; wave < ATTN_WAVES; ++wave)
-            for (int pb = lo >> psh; pb << psh < hi; pb += 64) {
-              const int end = hi < (pb + 64) << psh ? hi : (pb + 64) << psh;
-              int tile = lo > pb << psh ? lo : pb << psh;
-              tile += (wave - (tile - lo)) & (ATTN_WAVES - 1);
-              for (; tile < end; tile += ATTN_WAVES) {
-                const int at = (tile >> psh) - pb;
-                CHECK(at >= 0 && at < 64 && tile >= lo && tile < hi && (tile - lo) % ATTN_WAVES == wave);
-                ++seen[tile];
-              }
-            }
-        }
-        for (int t = 0; t < tiles; ++t) CHECK(seen[t] == 1);
-      }
   return nullptr;
 }
 

@@ -241,7 +241,7 @@ def test_scratch_sizes(lib, cache):
     assert n > 0 and n % 256 == 0
     assert lib.hcr_attn_scratch_bytes(cache, ctypes.byref(b), 31, 0) == 0
     assert lib.hcr_attn_scratch_bytes(None, ctypes.byref(b), 32, 0) == 0
-    small = batch(max_ctx=64)
+    small = batch(n_seqs=1, max_ctx=64)
     assert lib.hcr_attn_scratch_bytes(cache, ctypes.byref(small), 32, 0) == 0
     assert attn(lib, cache, b, bytes_=n - 1) == hcr.HCR_ESCRATCH
 
