@@ -2,12 +2,14 @@
 // first rope_dim values rotated by the angles of the token's position, rounded once to BF16; q to its rows, k and
 // v into the pages, and the mean key of each page that the window completes.
 //
-// One launch.  A lane holds 4 consecutive dimensions, D / 4 lanes a head: the sum of squares is a butterfly inside
-// a row of 16 lanes and one or two row swaps; the partner of a rotated value (j, j + r/2) sits in another lane at
-// the same place, that of (2j, 2j + 1) in the same lane.  The first work-groups take (sequence, page, kv head, k or
-// v): the page's new tokens are staged in LDS, 64 slots at a time, and written in the page's order, so that a
-// prompt's pages go out as whole lines (a lane writes 8 dimensions of a slot, or 8 slots of a dimension).  The
-// others take query heads.  Nothing bounds it but the bytes of the rows, and for a few tokens the launch itself.
+// One launch.  A lane holds 8 consecutive dimensions (16 bytes of BF16), D / 8 lanes a head: the sum of squares is a
+// butterfly over them; the partner of a rotated value (j, j + r/2) sits in another lane at the same place, that of
+// (2j, 2j + 1) in the same lane.  The first work-groups take (sequence, page, kv head, k or v): the page's new tokens
+// are staged in LDS, 64 slots at a time, and written in the page's order, so that a prompt's pages go out as whole
+// lines (a lane writes 8 dimensions of a slot, or 8 slots of a dimension).  The others take query heads.  Loads of
+// several tokens go out together.  Nothing bounds it but the bytes of the rows, and for a few tokens the launch
+// itself.  Measured on MI355X (graphs of calls, inputs rotated): 4,352 tokens of 32 + 16 heads of 128, BF16, 28.3 us,
+// 3.9 TB/s (40.7 with 4 dimensions a lane and one token's load at a time); one token of 48 + 16 heads of 256 3.9 us.
 
 #include <hip/hip_runtime.h>
 
@@ -19,70 +21,108 @@ namespace hcr {
 constexpr int APPEND_THREADS = 256;
 constexpr int SLOTS = 64;  // slots of a page staged at a time
 
-// 4 consecutive values of a row
+struct Values {
+  float v[8];
+};
+// 8 consecutive values of a row, as loaded and as FP32
 template <bool F32>
-__device__ __forceinline__ f32x4 load4(const void* p, size_t at) {
+struct Raw {
+  uint4 u[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ __forceinline__ Raw<F32> load8(const void* p, size_t at) {
+  Raw<F32> r;
   if constexpr (F32) {
-    return ld4(static_cast<const float*>(p) + at);
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at);
+    r.u[0] = q[0];
+    r.u[1] = q[1];
   } else {
-    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
-    return f32x4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
-                 __uint_as_float(u.y & 0xFFFF0000u)};
+    r.u[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
   }
+  return r;
 }
-__device__ __forceinline__ uint2 round4(const f32x4& v) {
-  const f32x2 a = {v[0], v[1]}, b = {v[2], v[3]};
-  return make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector(a, bf16x2)),
-                    __builtin_bit_cast(uint32_t, __builtin_convertvector(b, bf16x2)));
+template <bool F32>
+__device__ __forceinline__ Values values(const Raw<F32>& r) {
+  Values x;
+  if constexpr (F32) {
+    const uint32_t w[8] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w, r.u[1].x, r.u[1].y, r.u[1].z, r.u[1].w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x.v[e] = __uint_as_float(w[e]);
+  } else {
+    const uint32_t w[4] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x.v[2 * e] = __uint_as_float(w[e] << 16);
+      x.v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+    }
+  }
+  return x;
+}
+__device__ __forceinline__ uint4 round8(const Values& x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const f32x2 a = {x.v[2 * e], x.v[2 * e + 1]};
+    w[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(a, bf16x2));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ Values load_f8(const float* p) {
+  return values<true>(load8<true>(p, 0));
 }
 
-// The sum over the LANES (16, 32 or 64) lanes of a head, in every one of them.
+// The sum over the LANES (8, 16 or 32) lanes of a head, in every one of them.
 template <int LANES>
 __device__ __forceinline__ float head_sum(float v) {
   v += dpp<0xB1>(v);
   v += dpp<0x4E>(v);
   v += dpp<0x141>(v);
-  v += dpp<0x140>(v);
-  if constexpr (LANES >= 32) {
+  if constexpr (LANES >= 16) v += dpp<0x140>(v);
+  if constexpr (LANES == 32) {
     const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  }
-  if constexpr (LANES == 64) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
   }
   return v;
 }
 
-// Norm and rotation of a head's values 4 l .. 4 l + 3 at position pos (every lane of the wave takes part).
+// Norm and rotation of a head's values 8 l .. 8 l + 7 at position pos (every lane of the wave takes part).
 template <int D>
-__device__ __forceinline__ f32x4 norm_rotate(f32x4 x, const float* w, const AppendArgs& a, int l, int pos) {
-  constexpr int LANES = D / 4;
+__device__ __forceinline__ Values norm_rotate(Values x, const float* w, const AppendArgs& a, int l, int pos) {
+  constexpr int LANES = D / 8;
   if (w) {
-    const float ss = head_sum<LANES>((x[0] * x[0] + x[1] * x[1]) + (x[2] * x[2] + x[3] * x[3]));
-    const float rs = 1.f / sqrtf(ss * (1.f / D) + a.eps);
-    x = x * rs * ld4(w + 4 * l);
+    const Values g = load_f8(w + 8 * l);
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss += x.v[e] * x.v[e];
+    const float rs = 1.f / sqrtf(head_sum<LANES>(ss) * (1.f / D) + a.eps);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x.v[e] = x.v[e] * rs * g.v[e];
   }
   if (a.rope_dim) {
     const float* row = a.rope + (size_t)pos * a.rope_dim;
     const int half = a.rope_dim >> 1;
-    const bool in = 4 * l < a.rope_dim;
+    const bool in = 8 * l < a.rope_dim;
     if (a.rope_style == HCR_ROPE_PAIRS) {
       if (in) {
-        const f32x2 c = ld2(row + 2 * l), s = ld2(row + half + 2 * l);
-        x = f32x4{x[0] * c[0] - x[1] * s[0], x[1] * c[0] + x[0] * s[0], x[2] * c[1] - x[3] * s[1],
-                  x[3] * c[1] + x[2] * s[1]};
+        const f32x4 c = ld4(row + 4 * l), s = ld4(row + half + 4 * l);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p = x.v[2 * e], q = x.v[2 * e + 1];
+          x.v[2 * e] = p * c[e] - q * s[e];
+          x.v[2 * e + 1] = q * c[e] + p * s[e];
+        }
       }
     } else {
-      const bool low = 4 * l < half;
-      const int from = (threadIdx.x & 63) + (in ? (low ? half >> 2 : -(half >> 2)) : 0);
-      f32x4 y;
+      const bool low = 8 * l < half;
+      const int from = (threadIdx.x & 63) + (in ? (low ? half >> 3 : -(half >> 3)) : 0);
+      Values y;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = __shfl(x[e], from);
+      for (int e = 0; e < 8; ++e) y.v[e] = __shfl(x.v[e], from);
       if (in) {
-        const int j = low ? 4 * l : 4 * l - half;
-        const f32x4 c = ld4(row + j), s = ld4(row + half + j);
-        x = low ? x * c - y * s : x * c + y * s;
+        const int j = low ? 8 * l : 8 * l - half;
+        const Values c = load_f8(row + j), s = load_f8(row + half + j);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x.v[e] = low ? x.v[e] * c.v[e] - y.v[e] * s.v[e] : x.v[e] * c.v[e] + y.v[e] * s.v[e];
       }
     }
   }
@@ -92,9 +132,10 @@ __device__ __forceinline__ f32x4 norm_rotate(f32x4 x, const float* w, const Appe
 // The new tokens of one page of one kv head: staged, written in the page's order, the mean key where complete.
 template <int D, bool F32>
 __device__ void append_page(const AppendArgs& a, const Seq& seq, int b, int pg, int h, bool key) {
-  constexpr int LANES = D / 4, PER = APPEND_THREADS / LANES;  // tokens of a pass
-  constexpr int ROW = D + 8;                                  // 16 bytes more: slots start in other banks
-  constexpr int C = D / 8;                                    // 16-byte chunks of a slot
+  constexpr int LANES = D / 8, PER = APPEND_THREADS / LANES;  // tokens of a pass
+  constexpr int PASSES = SLOTS / PER;
+  constexpr int ROW = D + 8;  // 16 bytes more: slots start in other banks
+  constexpr int C = D / 8;    // 16-byte chunks of a slot
   __shared__ uint16_t tile[SLOTS * ROW];
   const int page = 1 << a.c.shift, tid = threadIdx.x;
   const int ctx = seq.first + seq.tokens;
@@ -113,32 +154,40 @@ __device__ void append_page(const AppendArgs& a, const Seq& seq, int b, int pg, 
 
   for (int base = mean ? 0 : lo / SLOTS * SLOTS; base < hi; base += SLOTS) {
     const int s0 = max(lo, base), s1 = min(hi, base + SLOTS);  // new slots of this part (s0 >= s1: none)
-    for (int s = s0; s < s1; s += PER) {
-      const int slot = min(s + sub, s1 - 1);  // past the end: the last one again, for the wave's sums
-      const int pos = start + slot;
-      const size_t at = (size_t)(seq.row + pos - seq.first) * rows.token_stride + (size_t)h * rows.head_stride + 4 * l;
-      f32x4 x = load4<F32>(rows.data, at);
-      if (key) x = norm_rotate<D>(x, a.k_norm, a, l, pos);
-      if (s + sub < s1) *reinterpret_cast<uint2*>(&tile[(slot - base) * ROW + 4 * l]) = round4(x);
+    if (s0 < s1) {
+      Raw<F32> raw[PASSES];
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {  // past the end the last slot again: its line is there, nothing is branched
+        const int slot = min(s0 + p * PER + sub, s1 - 1);
+        raw[p] = load8<F32>(rows.data, (size_t)(seq.row + start + slot - seq.first) * rows.token_stride +
+                                           (size_t)h * rows.head_stride + 8 * l);
+      }
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        if (s0 + p * PER >= s1) break;
+        const int slot = min(s0 + p * PER + sub, s1 - 1);
+        Values x = values<F32>(raw[p]);
+        if (key) x = norm_rotate<D>(x, a.k_norm, a, l, start + slot);
+        if (s0 + p * PER + sub < s1) *reinterpret_cast<uint4*>(&tile[(slot - base) * ROW + 8 * l]) = round8(x);
+      }
     }
     __syncthreads();
     if (key) {
-      const int n = max(s1 - s0, 0);
-      for (int i = tid; i < n * C; i += APPEND_THREADS) {
-        const int c = i / n, slot = s0 + i % n;
-        *reinterpret_cast<uint4*>(out + k_at(a.c.shift, slot, 8 * c)) =
-            *reinterpret_cast<const uint4*>(&tile[(slot - base) * ROW + 8 * c]);
+      for (int i = tid; i < SLOTS * C; i += APPEND_THREADS) {
+        const int c = i / SLOTS, slot = base + i % SLOTS;
+        if (slot >= s0 && slot < s1)
+          *reinterpret_cast<uint4*>(out + k_at(a.c.shift, slot, 8 * c)) =
+              *reinterpret_cast<const uint4*>(&tile[(slot - base) * ROW + 8 * c]);
       }
       if (mean) {
         for (int slot = base + mg; slot < min(base + SLOTS, page); slot += MG) {
           const uint4 u = slot >= lo ? *reinterpret_cast<const uint4*>(&tile[(slot - base) * ROW + 8 * mc])
                                      : *reinterpret_cast<const uint4*>(out + k_at(a.c.shift, slot, 8 * mc));
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+          Raw<false> r;
+          r.u[0] = u;
+          const Values x = values<false>(r);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            total[2 * e] += __uint_as_float(w[e] << 16);
-            total[2 * e + 1] += __uint_as_float(w[e] & 0xFFFF0000u);
-          }
+          for (int e = 0; e < 8; ++e) total[e] += x.v[e];
         }
       }
     } else if (s0 < s1) {
@@ -177,10 +226,10 @@ __device__ void append_page(const AppendArgs& a, const Seq& seq, int b, int pg, 
   }
 }
 
-template <int D, bool F32>
-__global__ __launch_bounds__(APPEND_THREADS) void append(AppendArgs a, int kv_groups, int pages, int passes,
-                                                         int tokens_each) {
-  constexpr int LANES = D / 4, PER = APPEND_THREADS / LANES;
+// EACH tokens of a work-group of query heads, their loads together.
+template <int D, bool F32, int EACH>
+__global__ __launch_bounds__(APPEND_THREADS) void append(AppendArgs a, int kv_groups, int pages, int passes) {
+  constexpr int LANES = D / 8, PER = APPEND_THREADS / LANES;
   int g = blockIdx.x;
   if (g < kv_groups) {
     const bool key = g & 1;
@@ -196,34 +245,46 @@ __global__ __launch_bounds__(APPEND_THREADS) void append(AppendArgs a, int kv_gr
   g -= kv_groups;
   const int pass = g % passes;
   g /= passes;
-  const int parts = ceil_div(a.b.max_tokens, tokens_each);
+  const int parts = ceil_div(a.b.max_tokens, EACH);
   const int b = g / parts;
   const Seq seq = seq_of(a.b, a.b.q_start[b], a.b.q_start[b + 1], a.b.ctx_len[b]);
   const int l = threadIdx.x % LANES, head = pass * PER + threadIdx.x / LANES;
   const int hh = min(head, a.heads - 1);
-  const int t0 = g % parts * tokens_each, t1 = min(t0 + tokens_each, seq.tokens);
-  for (int t = t0; t < t1; ++t) {
+  const int t0 = g % parts * EACH;
+  if (t0 >= seq.tokens) return;
+  Raw<F32> raw[EACH];
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const int t = min(t0 + i, seq.tokens - 1);
+    raw[i] = load8<F32>(a.q.data, (size_t)(seq.row + t) * a.q.token_stride + (size_t)hh * a.q.head_stride + 8 * l);
+  }
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const int t = t0 + i;
+    if (t >= seq.tokens) break;
     const int pos = seq.first + t;
-    f32x4 x = load4<F32>(a.q.data, (size_t)(seq.row + t) * a.q.token_stride + (size_t)hh * a.q.head_stride + 4 * l);
-    x = norm_rotate<D>(x, a.q_norm, a, l, max(pos, 0));
-    if (pos < 0) x = f32x4{0.f, 0.f, 0.f, 0.f};
+    Values x = norm_rotate<D>(values<F32>(raw[i]), a.q_norm, a, l, max(pos, 0));
+    if (pos < 0) x = Values{};
     if (head < a.heads)
-      *reinterpret_cast<uint2*>(a.q_out + ((size_t)(seq.row + t) * a.heads + head) * D + 4 * l) = round4(x);
+      *reinterpret_cast<uint4*>(a.q_out + ((size_t)(seq.row + t) * a.heads + head) * D + 8 * l) = round8(x);
   }
 }
 
-template <int D>
-void run_append(const AppendArgs& a, hipStream_t st) {
-  constexpr int PER = APPEND_THREADS / (D / 4);
+template <int D, bool F32, int EACH>
+void run(const AppendArgs& a, hipStream_t st) {
   const int pages = ((a.b.max_tokens - 1) >> a.c.shift) + 2;
   const int kv_groups = a.b.n_seqs * pages * a.c.kv_heads * 2;
-  const int passes = ceil_div(a.heads, PER);
-  const int each = a.b.max_tokens >= 64 ? 8 : 1;  // tokens of a work-group, one where there are few
-  const int grid = kv_groups + a.b.n_seqs * ceil_div(a.b.max_tokens, each) * passes;
+  const int passes = ceil_div(a.heads, APPEND_THREADS / (D / 8));
+  const int grid = kv_groups + a.b.n_seqs * ceil_div(a.b.max_tokens, EACH) * passes;
+  hipLaunchKernelGGL((append<D, F32, EACH>), dim3(grid), dim3(APPEND_THREADS), 0, st, a, kv_groups, pages, passes);
+}
+template <int D>
+void run_append(const AppendArgs& a, hipStream_t st) {
+  const bool many = a.b.max_tokens >= 32;  // a work-group a token where there are few
   if (a.type == HCR_F32)
-    hipLaunchKernelGGL((append<D, true>), dim3(grid), dim3(APPEND_THREADS), 0, st, a, kv_groups, pages, passes, each);
+    many ? run<D, true, 4>(a, st) : run<D, true, 1>(a, st);
   else
-    hipLaunchKernelGGL((append<D, false>), dim3(grid), dim3(APPEND_THREADS), 0, st, a, kv_groups, pages, passes, each);
+    many ? run<D, false, 4>(a, st) : run<D, false, 1>(a, st);
 }
 
 int launch_append(const AppendArgs& a, void* stream) {

@@ -221,7 +221,7 @@ int hcr_cache_append(hcr_cache_t h, const hcr_batch* batch, int heads, int type,
   if (rc < 0) return rc;
   if (type != HCR_F32 && type != HCR_BF16) return HCR_EINVAL;
   if (!(eps >= 0.f) || eps - eps != 0.f) return HCR_EINVAL;
-  if (rope_dim < 0 || rope_dim > c.head_dim || rope_dim % 8 || (rope_dim && !rope) ||
+  if (rope_dim < 0 || rope_dim > c.head_dim || rope_dim % 16 || (rope_dim && !rope) ||
       (rope_dim && rope_rows < a.b.max_ctx) ||
       (rope_style != HCR_ROPE_HALVES && rope_style != HCR_ROPE_PAIRS))
     return HCR_EINVAL;

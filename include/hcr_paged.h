@@ -100,7 +100,7 @@ size_t hcr_cache_pages_bytes(int n_pages, int kv_heads, int head_dim, int page);
  *   q_norm, k_norm  float [D] or NULL; eps >= 0
  *   rope       float [rope_rows][rope_dim]: cos of rope_dim / 2 angles, then their
  *              sin; row p for position p, rope_rows >= max_ctx.  NULL with rope_dim 0
- *   rope_dim   0..D, a multiple of 8;  rope_style HCR_ROPE_HALVES or HCR_ROPE_PAIRS
+ *   rope_dim   0..D, a multiple of 16;  rope_style HCR_ROPE_HALVES or HCR_ROPE_PAIRS
  * Rows of q, k and v may lie side by side in one projection's output.  The window's
  * rows must not overlap the cache or q_out.
  * Errors: HCR_EINVAL, HCR_EALIGN, HCR_EALIAS, HCR_EHIP. */

@@ -169,7 +169,7 @@ def append(lib, h, b, heads=32, type_=0, q=(Q, 6144, 128), k=(Q + 16384, 6144, 1
     (dict(heads=4), hcr.HCR_EINVAL), (dict(type_=3), hcr.HCR_EINVAL), (dict(q=None), hcr.HCR_EINVAL),
     (dict(k=(None, 6144, 128)), hcr.HCR_EINVAL), (dict(v=(Q, -6144, 128)), hcr.HCR_EINVAL),
     (dict(eps=-1.0), hcr.HCR_EINVAL), (dict(eps=float("nan")), hcr.HCR_EINVAL), (dict(eps=float("inf")), hcr.HCR_EINVAL),
-    (dict(rope=None), hcr.HCR_EINVAL), (dict(dim=136), hcr.HCR_EINVAL), (dict(dim=20), hcr.HCR_EINVAL),
+    (dict(rope=None), hcr.HCR_EINVAL), (dict(dim=136), hcr.HCR_EINVAL), (dict(dim=24), hcr.HCR_EINVAL),
     (dict(dim=-8), hcr.HCR_EINVAL), (dict(rows=4999), hcr.HCR_EINVAL), (dict(style=2), hcr.HCR_EINVAL),
     (dict(out=None), hcr.HCR_EINVAL), (dict(out=O + 8), hcr.HCR_EALIGN), (dict(q_norm=WN + 4), hcr.HCR_EALIGN),
     (dict(q=(Q + 8, 6144, 128)), hcr.HCR_EALIGN), (dict(k=(Q, 6146, 128)), hcr.HCR_EALIGN),

@@ -251,7 +251,7 @@ def test_append_windows(head_dim, page, kv, group, dtype, pairs):
     _append(s, kv * group, dtype, head_dim // 4, pairs, True)
 
 
-@pytest.mark.parametrize("rope_dim", [0, 8, 24, 128])
+@pytest.mark.parametrize("rope_dim", [0, 16, 48, 128])
 @pytest.mark.parametrize("norm", [True, False])
 def test_append_rotations(rope_dim, norm):
     s = pu.scene(21, 2, 128, 64, [(5, 70), (2, 300)], visible=[65, 298])
