@@ -152,37 +152,41 @@ class PagedCache:
             fn(vp(h))
             self.handle = None
 
-    def _call(self, name, batch, stream, *args):
+    def _call(self, fn, batch, stream, *args):
         """The entry point on the cache's device, its stream last."""
         if batch.device != self.device:
             raise ValueError(f"batch: on {self.device}")
-        st = torch._C._cuda_getCurrentRawStream(self.device.index) if stream is None else stream
-        fn = getattr(self._L, name)
-        if torch.cuda.current_device() == self.device.index:
-            rc = fn(*args, st)
+        index = self.device.index
+        st = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream
+        if torch._C._cuda_getDevice() == index:
+            rc = fn(self.handle, *args, st)
         else:
             with torch.cuda.device(self.device):
-                rc = fn(*args, st)
+                rc = fn(self.handle, *args, st)
         if rc != HCR_OK:
-            raise HCRError(rc, name)
+            raise HCRError(rc, fn.__name__)
+
+    # The checks below run at every call, ahead of kernels of a few microseconds: each reads a property once.
 
     def _heads_of(self, q):
         """(rows, heads) of q, BF16 [n_tokens][heads][head_dim]."""
-        if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != self.head_dim or not q.is_contiguous() or \
-                q.device != self.device:
+        shape = q.shape
+        if q.dtype is not torch.bfloat16 or len(shape) != 3 or shape[2] != self.head_dim or \
+                not q.is_contiguous() or q.device != self.device:
             raise ValueError(f"q: contiguous bfloat16 [n_tokens][heads][{self.head_dim}] on {self.device}")
-        return q.shape[0], q.shape[1]
+        return shape[0], shape[1]
 
     def _given(self, name, t, shape, dtype):
-        if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous() or t.device != self.device:
+        if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.device != self.device:
             raise ValueError(f"{name}: expected contiguous {dtype} {shape} on {self.device}")
-        return t
 
-    def _rows(self, name, x, heads, n, dtype):
-        if x.dim() != 3 or x.shape[0] != n or x.shape[2] != self.head_dim or x.dtype != dtype or \
-                x.device != self.device or (x.stride(2) != 1) or (heads is not None and x.shape[1] != heads):
-            raise ValueError(f"{name}: {dtype} [{n}][{heads}][{self.head_dim}] on {self.device}, its heads contiguous")
-        return hcr_rows(x.data_ptr(), x.stride(0), x.stride(1))
+    def _rows(self, name, x, shape, dtype):
+        if x.shape != shape or x.dtype is not dtype or x.device != self.device:
+            raise ValueError(f"{name}: expected {dtype} {shape} on {self.device}")
+        by_token, by_head, by_value = x.stride()
+        if by_value != 1:
+            raise ValueError(f"{name}: the values of a head side by side")
+        return hcr_rows(x.data_ptr(), by_token, by_head)
 
     def append(self, batch, q, k, v, q_norm=None, k_norm=None, eps=1e-6, rope=None, interleaved=False, q_out=None,
                stream=None):
@@ -194,15 +198,17 @@ class PagedCache:
         rope_dim / 2 angles (None: no rotation); ``interleaved`` rotates pairs (2j, 2j + 1) instead of
         (j, j + rope_dim / 2).  Pages that the window completes get their mean key.
         """
-        if q.dtype not in _TYPES or q.dim() != 3:
+        dtype, D = q.dtype, self.head_dim
+        if dtype not in _TYPES or q.dim() != 3:
             raise ValueError("q: float32 or bfloat16 [n_tokens][heads][head_dim]")
-        n, heads = q.shape[0], q.shape[1]
-        rq = self._rows("q", q, heads, n, q.dtype)
-        rk = self._rows("k", k, self.kv_heads, n, q.dtype)
-        rv = self._rows("v", v, self.kv_heads, n, q.dtype)
-        for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-            if w is not None:
-                self._given(name, w, (self.head_dim,), torch.float32)
+        n, heads, _ = q.shape
+        rq = self._rows("q", q, (n, heads, D), dtype)
+        rk = self._rows("k", k, (n, self.kv_heads, D), dtype)
+        rv = self._rows("v", v, (n, self.kv_heads, D), dtype)
+        if q_norm is not None:
+            self._given("q_norm", q_norm, (D,), torch.float32)
+        if k_norm is not None:
+            self._given("k_norm", k_norm, (D,), torch.float32)
         rope_rows = rope_dim = 0
         if rope is not None:
             if rope.dim() != 2:
@@ -210,16 +216,16 @@ class PagedCache:
             rope_rows, rope_dim = rope.shape
             self._given("rope", rope, (rope_rows, rope_dim), torch.float32)
         if q_out is None:
-            q_out = torch.empty((n, heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
+            q_out = torch.empty((n, heads, D), dtype=torch.bfloat16, device=self.device)
         else:
-            self._given("q_out", q_out, (n, heads, self.head_dim), torch.bfloat16)
-        self._call("hcr_cache_append", batch, stream, self.handle, batch._of(n), heads, _TYPES[q.dtype], rq, rk, rv,
+            self._given("q_out", q_out, (n, heads, D), torch.bfloat16)
+        self._call(self._L.hcr_cache_append, batch, stream, batch._of(n), heads, _TYPES[dtype], rq, rk, rv,
                    None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(), eps,
-                   rope.data_ptr() if rope_dim else None, rope_rows, rope_dim, int(bool(interleaved)),
-                   q_out.data_ptr())
+                   rope.data_ptr() if rope_dim else None, rope_rows, rope_dim,
+                   HCR_ROPE_PAIRS if interleaved else HCR_ROPE_HALVES, q_out.data_ptr())
         return q_out
 
-    def _attend(self, name, batch, q, sel, scale, out, out_dtype, scratch, stream):
+    def _attend(self, fn, batch, q, sel, scale, out, out_dtype, scratch, stream):
         n, heads = self._heads_of(q)
         if out is None:
             out = torch.empty((n, heads, self.head_dim), dtype=out_dtype, device=self.device)
@@ -236,9 +242,9 @@ class PagedCache:
             raise ValueError(f"scratch: a contiguous tensor on {self.device}")
         room = 0 if scratch is None else scratch.numel() * scratch.element_size()
         listed = () if sel is None else (sel.data_ptr(), n_sel)
-        self._call(name, batch, stream, self.handle, c_batch, heads,
-                   self.head_dim ** -0.5 if scale is None else scale, q.data_ptr(), *listed, _TYPES[out.dtype],
-                   out.data_ptr(), None if scratch is None else scratch.data_ptr(), room)
+        self._call(fn, batch, stream, c_batch, heads, self.head_dim ** -0.5 if scale is None else scale,
+                   q.data_ptr(), *listed, _TYPES[out.dtype], out.data_ptr(),
+                   None if scratch is None else scratch.data_ptr(), room)
         return out
 
     def attend(self, batch, q, scale=None, out=None, out_dtype=torch.float32, scratch=None, stream=None):
@@ -248,7 +254,7 @@ class PagedCache:
         returns float32 (``out_dtype``, or ``out``'s) [n_tokens][heads][head_dim].  ``scratch``: at least
         ``scratch_bytes`` of device memory; calls that share one are ordered on one stream.
         """
-        return self._attend("hcr_attn", batch, q, None, scale, out, out_dtype, scratch, stream)
+        return self._attend(self._L.hcr_attn, batch, q, None, scale, out, out_dtype, scratch, stream)
 
     def attend_blocks(self, batch, q, sel, scale=None, out=None, out_dtype=torch.float32, scratch=None, stream=None):
         """``attend`` over the pages listed in ``sel``, int32 [n_tokens][kv_heads][n_sel] (-1: none)."""
@@ -256,7 +262,7 @@ class PagedCache:
         if sel.dim() != 3:
             raise ValueError(f"sel: int32 [{n}][{self.kv_heads}][n_sel]")
         self._given("sel", sel, (n, self.kv_heads, sel.shape[2]), torch.int32)
-        return self._attend("hcr_attn_blocks", batch, q, sel, scale, out, out_dtype, scratch, stream)
+        return self._attend(self._L.hcr_attn_blocks, batch, q, sel, scale, out, out_dtype, scratch, stream)
 
     def scratch_bytes(self, batch, n_tokens, heads, n_sel=0):
         """Bytes that ``attend`` (n_sel 0) or ``attend_blocks`` needs for this batch."""
@@ -275,7 +281,7 @@ class PagedCache:
             if scores.dim() != 3:
                 raise ValueError(f"scores: float32 [{n}][{self.kv_heads}][pages]")
             self._given("scores", scores, (n, self.kv_heads, scores.shape[2]), torch.float32)
-        self._call("hcr_block_scores", batch, stream, self.handle, batch._of(n), heads, q.data_ptr(),
+        self._call(self._L.hcr_block_scores, batch, stream, batch._of(n), heads, q.data_ptr(),
                    scores.data_ptr(), scores.shape[2])
         return scores
 
@@ -293,6 +299,6 @@ class PagedCache:
             sel = torch.empty((n, self.kv_heads, max(n_sel, 0)), dtype=torch.int32, device=self.device)
         else:
             self._given("sel", sel, (n, self.kv_heads, n_sel), torch.int32)
-        self._call("hcr_block_topk", batch, stream, self.handle, batch._of(n), scores.data_ptr(), scores.shape[2],
+        self._call(self._L.hcr_block_topk, batch, stream, batch._of(n), scores.data_ptr(), scores.shape[2],
                    n_sel, n_first, n_last, sel.data_ptr())
         return sel
