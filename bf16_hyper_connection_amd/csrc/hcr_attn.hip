@@ -187,90 +187,169 @@ __device__ __forceinline__ Set next_set(const AttnArgs& a, const Set& s, int lan
   return Set{Seq{0, 0, 0}, -1, 0, first, 0};
 }
 
-// A set's tiles [lo, hi) (counted from its own first) in one work-group: its rows' part of the softmax.
-template <int D, int MT, bool SEL>
-__device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int h, int rb, int lo, int hi, bool only,
-                                         size_t slot, size_t slots, uint4* lds) {
-  constexpr int KS = D / 32, DT = D / 16;
-  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int RT = a.plan.row_waves, TG = a.plan.groups;  // waves: TG groups over the tiles x RT over the rows
-  const int rt = wave % RT, tg = wave / RT;
-  const Seq& seq = set.seq;
-  const int b = set.b, token = set.token;
+// The rows of a set that a work-group takes, and which positions they see: [0, len).
+struct Rows {
+  int first, count;      // of the set's rows; the work-group's first one, the set's number
+  int len_min, len_max;  // of the work-group's rows
+  __device__ __forceinline__ Rows(const AttnArgs& a, const Set& set, bool listed, int rb) {
+    first = rb * attn_rows(a.plan);
+    count = listed ? a.group : set.seq.tokens * a.group;
+    const int last = min(first + attn_rows(a.plan), count) - 1;
+    len_min = set.seq.first + (listed ? set.token : first / a.group) + 1;
+    len_max = set.seq.first + (listed ? set.token : last / a.group) + 1;
+  }
+};
 
-  const int G = a.group;
-  const int rows = SEL ? G : seq.tokens * G;
-  const int first_row = rb * RT * 16 * MT;
-  if (first_row >= rows) return;
-  // a wave behind the last row takes the last row again, and stores nothing
-  const int r0 = min(first_row + rt * 16 * MT, rows - 1);
-  const bool idle = first_row + rt * 16 * MT >= rows;
-  const int r_last = min(first_row + RT * 16 * MT, rows) - 1;
-  // positions a row sees: [0, len)
-  const int len_max = seq.first + (SEL ? token : r_last / G) + 1;
-  const int len_min = seq.first + (SEL ? token : r0 / G) + 1;
-  const int psh = a.c.shift - TILE_SHIFT;
-  const int tiles = set.tiles;
-
-  // ---- the tiles of this group, one after the other: lo + tg, + TG, ..., those without a visible position left
-  // out.  Page list: lane l holds entry `from` + l, as the page's number (-1: none) and its index in the sequence.
-  const int page = 1 << a.c.shift;
-  const int key_row = 8 * (li >> 2) + (li & 3);  // position of key tile 0's row li
-  int from = lo >> psh, number = -1, index = -1;
-  auto list = [&]() {
+// The tiles of a set from `tile` to `hi`, every `step`-th, those without a visible position left out.  Lane l holds
+// entry `from` + l of the page list, as the page's number (-1: none) and its index in the sequence.
+template <int D, bool SEL>
+struct Tiles {
+  const AttnArgs& a;
+  const Set& set;
+  const int h, len_max, lane, psh, hi, step;
+  int tile, from, number, index;
+  int p0;               // of the tile found: its first position,
+  const char *kp, *vp;  // its keys and values (the same for the whole wave)
+  __device__ __forceinline__ Tiles(const AttnArgs& a_, const Set& set_, int h_, int len, int lane_, int lo, int hi_,
+                                   int skip, int step_)
+      : a(a_), set(set_), h(h_), len_max(len), lane(lane_), psh(a_.c.shift - TILE_SHIFT), hi(hi_), step(step_),
+        tile(lo + skip), from(lo >> psh), number(-1), index(-1), p0(0), kp(nullptr), vp(nullptr) {
+    list();
+  }
+  __device__ __forceinline__ void list() {
     const int idx = from + lane;
+    const int* table = a.b.table + (size_t)set.b * a.b.table_stride;
     number = -1;
     index = idx;
     if (SEL) {
-      index = idx < a.n_sel ? a.sel[((size_t)(seq.row + token) * a.c.kv_heads + h) * a.n_sel + idx] : -1;
+      index = idx < a.n_sel ? a.sel[((size_t)(set.seq.row + set.token) * a.c.kv_heads + h) * a.n_sel + idx] : -1;
       if (index >= 0 && len_max > 0 && index <= (len_max - 1) >> a.c.shift)
-        number = page_or_none(a.b.table[(size_t)b * a.b.table_stride + index], a.c.n_pages);
-    } else if (idx << psh < tiles) {
-      number = page_or_none(a.b.table[(size_t)b * a.b.table_stride + idx], a.c.n_pages);
+        number = page_or_none(table[index], a.c.n_pages);
+    } else if (idx << a.c.shift < len_max) {
+      number = page_or_none(table[idx], a.c.n_pages);
     }
-  };
-  int tile = lo + tg, p0 = 0;
-  // operands: the tile's place is the same for the whole wave, the lane's place in it for the whole kernel
-  const char *kp = nullptr, *vp = nullptr;
-  const uint32_t k_lane = ((uint32_t)(lg << a.c.shift) + key_row) * 16, v_lane = (uint32_t)(lg * D + li) * 16;
-  const uint32_t k_step = 4u << a.c.shift << 4;  // 32 dimensions on
-  auto find = [&]() {  // the next tile with visible positions, from `tile` on: its first position and operands
-    for (; tile < hi; tile += TG) {
+  }
+  __device__ __forceinline__ bool find() {
+    for (; tile < hi; tile += step) {
       if ((tile >> psh) - from >= 64) {
         from = tile >> psh;
         list();
       }
       const int at = (tile >> psh) - from;
       const int pn = __builtin_amdgcn_readlane(number, at);
-      const int off = (tile << TILE_SHIFT) & (page - 1);
+      const int off = (tile << TILE_SHIFT) & ((1 << a.c.shift) - 1);
       p0 = (__builtin_amdgcn_readlane(index, at) << a.c.shift) + off;
       if (pn < 0 || p0 >= len_max) continue;
       const size_t base = head_base(a.c, pn, h);
       kp = reinterpret_cast<const char*>(a.c.k + base + off * 8);
       vp = reinterpret_cast<const char*>(a.c.v + base + off * D);
-      tile += TG;
+      tile += step;
       return true;
     }
     return false;
-  };
+  }
+};
+
+// Values behind the last visible position may be anything: zeros in their place (their probabilities are zero, but
+// zero times NaN is not).  p: the position of the first of 8.
+__device__ __forceinline__ uint4 visible8(const uint4& v, int p, int len) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = p + 2 * e + 1 < len ? w[e] : p + 2 * e < len ? w[e] & 0xFFFFu : 0u;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The lane's 8 products s of one row as probabilities against the row's running maximum; its sum and values follow
+// where the maximum moves.  p0: the position of the first of 8; whole: every row sees all of them.
+template <int DT>
+__device__ __forceinline__ void probabilities(const AttnArgs& a, const f32x4 (&s)[2], bool whole, int p0, int len,
+                                              float& mx, float& sum, f32x4 (&acc)[DT], float (&p)[8]) {
+  float y[8];  // as exponents of two
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = s[i >> 2][i & 3] * a.scale_hi;
+  if (!whole) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = p0 + i < len ? y[i] : -INFINITY;
+  }
+  float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
+  top = rows_max(top);
+  if (__any(top > mx + 8.f)) {
+    const float high = fmaxf(mx, top);
+    const float f = exp2_of(mx - high);
+    mx = high;
+    sum *= f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) acc[d] *= f;
+  }
+  // exponents with the scale in two parts: one rounding, of the difference from the maximum
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = s[i >> 2][i & 3];
+    p[i] = exp2_of(__builtin_fmaf(v, a.scale_hi, __builtin_fmaf(v, a.scale_lo, -mx)));
+  }
+  if (!whole) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = p0 + i < len ? p[i] : 0.f;
+  }
+  sum += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+}
+
+__device__ __forceinline__ f32x4 mfma(const uint4& x, const uint4& y, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(x), as_bf16x8(y), c, 0, 0, 0);
+}
+
+// One row's values out: its outputs where the work-group had all of its tiles, else its part for the join.
+struct Out {
+  const AttnArgs& a;
+  const bool only;
+  const size_t slot, slots;
+  __device__ __forceinline__ void values(int D, int rid, int slot_row, int d, const f32x4& o, float sum) const {
+    if (only)
+      store4(a.out, a.out_type, (size_t)rid * D + d, o * (sum > 0.f ? 1.f / sum : 0.f));
+    else
+      *reinterpret_cast<f32x4*>(a.part + (slot * attn_rows(a.plan) + slot_row) * D + d) = o;
+  }
+  __device__ __forceinline__ void state(int D, int slot_row, float mx, float sum) const {
+    const size_t rows = attn_rows(a.plan);
+    if (!only) *reinterpret_cast<f32x2*>(a.part + slots * rows * D + (slot * rows + slot_row) * 2) = f32x2{mx, sum};
+  }
+};
+
+// A set's tiles [lo, hi) (counted from its own first) in one work-group: its rows' part of the softmax.
+template <int D, int MT, bool SEL>
+__device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int h, int rb, int lo, int hi,
+                                         const Out& out, uint4* lds) {
+  constexpr int KS = D / 32, DT = D / 16;
+  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int RT = a.plan.row_waves, TG = a.plan.groups;  // waves: TG groups over the tiles x RT over the rows
+  const int rt = wave % RT, tg = wave / RT;
+  const int G = a.group;
+  const Rows rows(a, set, SEL, rb);
+  if (rows.first >= rows.count) return;
+  // a wave behind the last row takes the last row again, and stores nothing
+  const int r0 = rows.first + rt * 16 * MT;
+  const bool idle = r0 >= rows.count;
+  Tiles<D, SEL> tiles(a, set, h, rows.len_max, lane, lo, hi, tg, TG);
+
+  // Keys of the next tile are loaded behind their last use in this one, values likewise, so that one of the two is
+  // always on its way while the other is worked on; the first ones go out ahead of the query rows' way through LDS.
+  const uint32_t k_lane = ((uint32_t)(lg << a.c.shift) + 8 * (li >> 2) + (li & 3)) * 16;  // key tile 0's row li
+  const uint32_t v_lane = (uint32_t)(lg * D + li) * 16;
+  const uint32_t k_step = 4u << a.c.shift << 4;  // 32 dimensions on
   uint4 kf[2][KS], vf[DT];
   auto load_keys = [&]() {
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
-      const char* at = kp + k * k_step;
+      const char* at = tiles.kp + k * k_step;
       kf[0][k] = ld16(at + k_lane);
       kf[1][k] = ld16(at + k_lane + 4 * 16);
     }
   };
   auto load_values = [&]() {
 #pragma unroll
-    for (int d = 0; d < DT; ++d) vf[d] = ld16(vp + v_lane + 16 * 16 * d);
+    for (int d = 0; d < DT; ++d) vf[d] = ld16(tiles.vp + v_lane + 16 * 16 * d);
   };
-
-  // Keys of the next tile are loaded behind their last use in this one, values likewise, so that one of the two is
-  // always on its way while the other is worked on; the first ones go out ahead of the query rows' way through LDS.
-  list();
   // the lane's query row of each 16-row tile and its length; the rows as operands in LDS, one copy for all groups
   // (in registers they would push the loop's operands out)
   uint4* lds_q = lds + (size_t)rt * MT * KS * 64 + lane;  // [RT][MT][KS][64]
@@ -280,12 +359,11 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
   bool live[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    const int r = r0 + 16 * m + li;
-    live[m] = !idle && r < rows;
-    const int rr = min(r, rows - 1);
-    const int t = SEL ? token : rr / G, g = SEL ? rr : rr % G;
-    len[m] = seq.first + t + 1;
-    rid[m] = (seq.row + t) * a.heads + h * G + g;
+    const int r = min(r0 + 16 * m + li, rows.count - 1);
+    live[m] = r0 + 16 * m + li < rows.count;
+    const int t = SEL ? set.token : r / G, g = SEL ? r : r % G;
+    len[m] = set.seq.first + t + 1;
+    rid[m] = (set.seq.row + t) * a.heads + h * G + g;
     if (tg == 0) {
 #pragma unroll
       for (int k = 0; k < KS; ++k) qf[m][k] = ld16(a.q + (size_t)rid[m] * D + 8 * lg + 32 * k);
@@ -294,7 +372,7 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
   // row waves alone keep step, so that the first one's misses are the others' hits in L1 (36 rows of D = 256: 314
   // against 342 us; all of them find the same tiles)
   const bool together = TG == 1 && RT > 1;
-  bool more = find();
+  bool more = tiles.find();
   if (more && !idle) {
     load_keys();
     load_values();
@@ -319,88 +397,47 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
 
   while (more) {
     if (idle) {
-      more = find();
+      more = tiles.find();
       if (together) __builtin_amdgcn_s_barrier();
       continue;
     }
-    const int now = p0;
-    const bool whole = now + TILE <= len_min;
+    const int now = tiles.p0;
+    const bool whole = now + TILE <= rows.len_min;
     f32x4 s[MT][2];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       s[m][0] = s[m][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        const bf16x8 qk = as_bf16x8(lds_q[(m * KS + k) * 64]);
+        const uint4 qk = lds_q[(m * KS + k) * 64];
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-          s[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(kf[t][k]), qk, s[m][t], 0, 0, 0);
+        for (int t = 0; t < 2; ++t) s[m][t] = mfma(kf[t][k], qk, s[m][t]);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    more = find();
+    more = tiles.find();
     if (together) __builtin_amdgcn_s_barrier();
     if (more) load_keys();
     __builtin_amdgcn_sched_barrier(0);
 
     if (!whole) {
-      // values behind the last visible position may be anything: zeros in their place (their
-      // probabilities are zero, but zero times NaN is not)
 #pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        uint32_t w[4] = {vf[d].x, vf[d].y, vf[d].z, vf[d].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int p = now + 8 * lg + 2 * e;
-          w[e] = p + 1 < len_max ? w[e] : p < len_max ? w[e] & 0xFFFFu : 0u;
-        }
-        vf[d] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      for (int d = 0; d < DT; ++d) vf[d] = visible8(vf[d], now + 8 * lg, rows.len_max);
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      float y[8];  // as exponents of two
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = s[m][i >> 2][i & 3] * a.scale_hi;
-      if (!whole) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = now + 8 * lg + i < len[m] ? y[i] : -INFINITY;
-      }
-      float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
-      top = rows_max(top);
-      if (__any(top > mx[m] + 8.f)) {
-        const float high = fmaxf(mx[m], top);
-        const float f = exp2_of(mx[m] - high);
-        mx[m] = high;
-        sum[m] *= f;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) acc[m][d] *= f;
-      }
-      // exponents with the scale in two parts: one rounding, of the difference from the maximum
       float p[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float v = s[m][i >> 2][i & 3];
-        p[i] = exp2_of(__builtin_fmaf(v, a.scale_hi, __builtin_fmaf(v, a.scale_lo, -mx[m])));
-      }
-      if (!whole) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = now + 8 * lg + i < len[m] ? p[i] : 0.f;
-      }
-      sum[m] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+      probabilities<DT>(a, s[m], whole, now + 8 * lg, len[m], mx[m], sum[m], acc[m], p);
       uint4 ph, pl;
       split_hi_lo(p, ph, pl);
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
-        acc[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(vf[d]), as_bf16x8(ph), acc[m][d], 0, 0, 0);
+      for (int d = 0; d < DT; ++d) acc[m][d] = mfma(vf[d], ph, acc[m][d]);
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
-        acc[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(vf[d]), as_bf16x8(pl), acc[m][d], 0, 0, 0);
+      for (int d = 0; d < DT; ++d) acc[m][d] = mfma(vf[d], pl, acc[m][d]);
       if (a.out_type == HCR_F32) {
         const uint4 pr = split_rest(p, ph, pl);
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-          acc[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(vf[d]), as_bf16x8(pr), acc[m][d], 0, 0, 0);
+        for (int d = 0; d < DT; ++d) acc[m][d] = mfma(vf[d], pr, acc[m][d]);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -451,36 +488,28 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
     __syncthreads();
   }
 
-  const int slot_rows = RT * MT * 16;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     if (!live[m]) continue;
-    const float f = !only ? 1.f : sum[m] > 0.f ? 1.f / sum[m] : 0.f;
-    const size_t at = slot * slot_rows + (rt * MT + m) * 16 + li;
-    auto put = [&](int d, f32x4 o) {
-      if (only)  // nothing to join: the outputs themselves
-        store4(a.out, a.out_type, (size_t)rid[m] * D + 16 * d + 4 * lg, o * f);
-      else
-        *reinterpret_cast<f32x4*>(a.part + at * D + 16 * d + 4 * lg) = o;
-    };
+    const int slot_row = (rt * MT + m) * 16 + li;
     if (TG == 1) {
 #pragma unroll
-      for (int d = 0; d < DT; ++d) put(d, acc[m][d]);
+      for (int d = 0; d < DT; ++d) out.values(D, rid[m], slot_row, 16 * d + 4 * lg, acc[m][d], sum[m]);
     } else {
       for (int d = tg; d < DT; d += TG) {
         f32x4 o = {0.f, 0.f, 0.f, 0.f};
         for (int g0 = 0; g0 < TG; g0 += 4) {
           f32x4 v[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = lds_acc[((min(g0 + i, TG - 1) * RT + rt) * MT * DT + m * DT + d) * 64 + lane];
+          for (int i = 0; i < 4; ++i)
+            v[i] = lds_acc[((min(g0 + i, TG - 1) * RT + rt) * MT * DT + m * DT + d) * 64 + lane];
 #pragma unroll
           for (int i = 0; i < 4; ++i) o += g0 + i < TG ? v[i] : f32x4{0.f, 0.f, 0.f, 0.f};
         }
-        put(d, o);
+        out.values(D, rid[m], slot_row, 16 * d + 4 * lg, o, sum[m]);
       }
     }
-    if (!only && tg == 0 && lg == 0)
-      *reinterpret_cast<f32x2*>(a.part + slots * slot_rows * D + at * 2) = f32x2{mx[m], sum[m]};
+    if (tg == 0 && lg == 0) out.state(D, slot_row, mx[m], sum[m]);
   }
 }
 
@@ -504,8 +533,8 @@ __global__ __launch_bounds__(64 * attn_waves(D, MT)) void attn_part(AttnArgs a) 
   while (set.tiles > 0 && set.first < begin + run) {
     if (set.b >= 0) {
       const int lo = max(begin - set.first, 0), hi = min(begin + run - set.first, set.tiles);
-      attn_run<D, MT, SEL>(a, set, h, rb, lo, hi, lo == 0 && hi == set.tiles, slot + part_slot(item, run, set.first),
-                           slots, lds);
+      const Out out{a, lo == 0 && hi == set.tiles, slot + part_slot(item, run, set.first), slots};
+      attn_run<D, MT, SEL>(a, set, h, rb, lo, hi, out, lds);
     }
     if (set.first + set.tiles >= begin + run) break;
     set = next_set<SEL>(a, set, lane);
@@ -593,7 +622,7 @@ void run_attn(const AttnArgs& a, int grid, int join_grid, hipStream_t st) {
   const int join = a.plan.items > 2 * (SEL ? a.b.n_tokens : a.b.n_seqs) ? 256 : 64;
   if (a.plan.q_tiles == 1) {
     run_part<D, 1, SEL>(a, grid, st);
-  } else if constexpr (D != 256) {
+  } else if constexpr (D == 128) {
     run_part<D, 2, SEL>(a, grid, st);
   }
   if (join_grid) hipLaunchKernelGGL((attn_join<D, SEL>), dim3(join_grid), dim3(join), 0, st, a);
