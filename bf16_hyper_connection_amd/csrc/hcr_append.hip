@@ -8,8 +8,8 @@
 // are staged in LDS, 64 slots at a time, and written in the page's order, so that a prompt's pages go out as whole
 // lines (a lane writes 8 dimensions of a slot, or 8 slots of a dimension).  The others take query heads.  Loads of
 // several tokens go out together.  Nothing bounds it but the bytes of the rows, and for a few tokens the launch
-// itself.  Measured on MI355X (graphs of calls, inputs rotated): 4,352 tokens of 32 + 16 heads of 128, BF16, 28.3 us,
-// 3.9 TB/s (40.7 with 4 dimensions a lane and one token's load at a time); one token of 48 + 16 heads of 256 3.9 us.
+// itself.  Measured on MI355X (graphs of calls, inputs rotated): 4,352 tokens of 32 + 16 heads of 128, BF16, 27.4 us,
+// 4.0 TB/s (28.5 with loads that stay in the caches; 40.7 with 4 dimensions a lane and one token's load at a time); one token of 48 + 16 heads of 256 3.9 us.
 
 #include <hip/hip_runtime.h>
 
@@ -34,10 +34,10 @@ __device__ __forceinline__ Raw<F32> load8(const void* p, size_t at) {
   Raw<F32> r;
   if constexpr (F32) {
     const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at);
-    r.u[0] = q[0];
-    r.u[1] = q[1];
+    r.u[0] = ldw16(q);
+    r.u[1] = ldw16(q + 1);
   } else {
-    r.u[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+    r.u[0] = ldw16(static_cast<const uint16_t*>(p) + at);
   }
   return r;
 }
@@ -68,7 +68,8 @@ __device__ __forceinline__ uint4 round8(const Values& x) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 __device__ __forceinline__ Values load_f8(const float* p) {
-  return values<true>(load8<true>(p, 0));
+  const f32x4 a = ld4(p), b = ld4(p + 4);
+  return Values{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
 }
 
 // The sum over the LANES (8, 16 or 32) lanes of a head, in every one of them.

@@ -21,11 +21,10 @@
 // runs are joined by a second launch; each join is (m, l, O) -> (max, sum of l 2^(m - max), sum of O 2^(m - max)),
 // in a fixed order.
 //
-// Bound by the bytes of keys and values.  Measured on MI355X (graphs of calls,
-// inputs rotated): one sequence of 420,000 positions, 48 heads of 256 over 8, 2 tokens: 568 us, 6.1 TB/s (a 4 GiB
-// device copy moves 4.8); 64 sequences of 1,000 to 8,192, 32 heads of 128 over 8: 216 us, 5.6 TB/s.  36 rows of 4
-// sequences of up to 9,001: 50 us, 3.3 TB/s, of which the first loads' way, the parts' (9 MB written and read) and
-// the second launch take about 15.
+// Bound by the bytes of keys and values.  Measured on MI355X (graphs of calls, inputs rotated): one sequence of
+// 420,000 positions, 48 heads of 256 over 8, 2 tokens: 528 us, 6.5 TB/s (a 4 GiB device copy moves 4.8); 64 sequences
+// of 1,000 to 8,192, 32 heads of 128 over 8: 193 us, 6.3 TB/s.  36 rows of 4 sequences of up to 9,001: 51 us, 3.3 TB/s,
+// of which the first loads' way, the parts' (9 MB written and read) and the second launch take about 15.
 
 #include <float.h>
 #include <hip/hip_runtime.h>
@@ -39,6 +38,14 @@ typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 
 __device__ __forceinline__ bf16x8 as_bf16x8(const uint4& u) { return __builtin_bit_cast(bf16x8, u); }
 __device__ __forceinline__ uint4 ld16(const void* p) { return *static_cast<const uint4*>(p); }
+// Keys and values: past the caches where nobody else reads them (ONCE).  Measured on MI355X: 64 sequences of up to
+// 8,192 positions 193 against 215 us, 420,000 positions 529 against 590; with three row waves on the same tiles 62
+// against 51.
+template <bool ONCE>
+__device__ __forceinline__ uint4 ld_kv(const void* p) {
+  if constexpr (ONCE) return ldw16(p);
+  return ld16(p);
+}
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // The larger of each value over the 4 lane rows (lanes l, l ^ 16, l ^ 32, l ^ 48).
@@ -316,7 +323,7 @@ struct Out {
 };
 
 // A set's tiles [lo, hi) (counted from its own first) in one work-group: its rows' part of the softmax.
-template <int D, int MT, bool SEL>
+template <int D, int MT, bool SEL, bool ONCE>
 __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int h, int rb, int lo, int hi,
                                          const Out& out, uint4* lds) {
   constexpr int KS = D / 32, DT = D / 16;
@@ -342,13 +349,13 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
       const char* at = tiles.kp + k * k_step;
-      kf[0][k] = ld16(at + k_lane);
-      kf[1][k] = ld16(at + k_lane + 4 * 16);
+      kf[0][k] = ld_kv<ONCE>(at + k_lane);
+      kf[1][k] = ld_kv<ONCE>(at + k_lane + 4 * 16);
     }
   };
   auto load_values = [&]() {
 #pragma unroll
-    for (int d = 0; d < DT; ++d) vf[d] = ld16(tiles.vp + v_lane + 16 * 16 * d);
+    for (int d = 0; d < DT; ++d) vf[d] = ld_kv<ONCE>(tiles.vp + v_lane + 16 * 16 * d);
   };
   // the lane's query row of each 16-row tile and its length; the rows as operands in LDS, one copy for all groups
   // (in registers they would push the loop's operands out)
@@ -513,7 +520,7 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
   }
 }
 
-template <int D, int MT, bool SEL>
+template <int D, int MT, bool SEL, bool ONCE>
 __global__ __launch_bounds__(64 * attn_waves(D, MT)) void attn_part(AttnArgs a) {
   extern __shared__ uint4 lds[];
   const int lane = threadIdx.x & 63;
@@ -534,7 +541,7 @@ __global__ __launch_bounds__(64 * attn_waves(D, MT)) void attn_part(AttnArgs a) 
     if (set.b >= 0) {
       const int lo = max(begin - set.first, 0), hi = min(begin + run - set.first, set.tiles);
       const Out out{a, lo == 0 && hi == set.tiles, slot + part_slot(item, run, set.first), slots};
-      attn_run<D, MT, SEL>(a, set, h, rb, lo, hi, out, lds);
+      attn_run<D, MT, SEL, ONCE>(a, set, h, rb, lo, hi, out, lds);
     }
     if (set.first + set.tiles >= begin + run) break;
     set = next_set<SEL>(a, set, lane);
@@ -613,8 +620,13 @@ namespace {
 
 template <int D, int MT, bool SEL>
 void run_part(const AttnArgs& a, int grid, hipStream_t st) {
-  hipLaunchKernelGGL((attn_part<D, MT, SEL>), dim3(grid), dim3(64 * a.plan.row_waves * a.plan.groups),
-                     attn_lds(D, a.plan), st, a);
+  const dim3 threads(64 * a.plan.row_waves * a.plan.groups);
+  const int lds = attn_lds(D, a.plan);
+  // one wave's rows, and not several tokens' lists, which mostly name the same pages
+  if (a.plan.row_waves * a.plan.row_blocks == 1 && (!SEL || a.b.max_tokens == 1))
+    hipLaunchKernelGGL((attn_part<D, MT, SEL, true>), dim3(grid), threads, lds, st, a);
+  else
+    hipLaunchKernelGGL((attn_part<D, MT, SEL, false>), dim3(grid), threads, lds, st, a);
 }
 template <int D, bool SEL>
 void run_attn(const AttnArgs& a, int grid, int join_grid, hipStream_t st) {
