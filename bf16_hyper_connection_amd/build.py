@@ -21,7 +21,7 @@ C_FLAGS = ["-std=c11", "-O2", "-Wall", "-Wextra", "-Wpedantic", "-Werror",
 SOURCES = ["hcr_kernels.hip", "hcr_matvec.hip", "hcr_api.cpp"]
 # the paged cache (include/hcr_paged.h), in the same library
 PAGED_SOURCES = ["hcr_append.hip", "hcr_attn.hip", "hcr_blocks.hip", "hcr_paged_api.cpp"]
-PAGED_HEADERS = ["hcr_paged_layout.h"]
+PAGED_HEADERS = ["hcr_paged_device.h", "hcr_paged_layout.h"]
 # the calibration kernels (include/hcr_calib.h): a library of their own, measurement only
 CALIB_LIB = os.path.join(PKG, "libhcr_calib.so")
 CALIB_SOURCES = ["hcr_calib.hip"]

@@ -9,16 +9,15 @@
 // lines (a lane writes 8 dimensions of a slot, or 8 slots of a dimension).  The others take query heads.  Loads of
 // several tokens go out together.  Nothing bounds it but the bytes of the rows, and for a few tokens the launch
 // itself.  Measured on MI355X (graphs of calls, inputs rotated): 4,352 tokens of 32 + 16 heads of 128, BF16, 27.4 us,
-// 4.0 TB/s (28.5 with loads that stay in the caches; 40.7 with 4 dimensions a lane and one token's load at a time); one token of 48 + 16 heads of 256 3.9 us.
+// 4.0 TB/s (28.5 with loads that stay in the caches; 40.7 with 4 dimensions a lane and one token's load at a time);
+// one token of 48 + 16 heads of 256 3.9 us.
 
 #include <hip/hip_runtime.h>
 
-#include "hcr_device.h"
-#include "hcr_paged_layout.h"
+#include "hcr_paged_device.h"
 
 namespace hcr {
 
-constexpr int APPEND_THREADS = 256;
 constexpr int SLOTS = 64;  // slots of a page staged at a time
 
 struct Values {
@@ -273,19 +272,17 @@ __global__ __launch_bounds__(APPEND_THREADS) void append(AppendArgs a, int kv_gr
 
 template <int D, bool F32, int EACH>
 void run(const AppendArgs& a, hipStream_t st) {
-  const int pages = ((a.b.max_tokens - 1) >> a.c.shift) + 2;
-  const int kv_groups = a.b.n_seqs * pages * a.c.kv_heads * 2;
-  const int passes = ceil_div(a.heads, APPEND_THREADS / (D / 8));
-  const int grid = kv_groups + a.b.n_seqs * ceil_div(a.b.max_tokens, EACH) * passes;
-  hipLaunchKernelGGL((append<D, F32, EACH>), dim3(grid), dim3(APPEND_THREADS), 0, st, a, kv_groups, pages, passes);
+  const AppendGrid g = append_grid(a.c, a.b, a.heads);
+  hipLaunchKernelGGL((append<D, F32, EACH>), dim3(g.groups), dim3(APPEND_THREADS), 0, st, a, (int)g.kv_groups, g.pages,
+                     g.passes);
 }
 template <int D>
 void run_append(const AppendArgs& a, hipStream_t st) {
-  const bool many = a.b.max_tokens >= 32;  // a work-group a token where there are few
+  const bool many = append_each(a.b) > 1;
   if (a.type == HCR_F32)
-    many ? run<D, true, 4>(a, st) : run<D, true, 1>(a, st);
+    many ? run<D, true, APPEND_EACH>(a, st) : run<D, true, 1>(a, st);
   else
-    many ? run<D, false, 4>(a, st) : run<D, false, 1>(a, st);
+    many ? run<D, false, APPEND_EACH>(a, st) : run<D, false, 1>(a, st);
 }
 
 int launch_append(const AppendArgs& a, void* stream) {

@@ -29,8 +29,7 @@
 #include <float.h>
 #include <hip/hip_runtime.h>
 
-#include "hcr_device.h"
-#include "hcr_paged_layout.h"
+#include "hcr_paged_device.h"
 
 namespace hcr {
 
@@ -95,12 +94,6 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// The sequences 64 at a time, one per lane.
-__device__ __forceinline__ Seq lane_seq(const BatchArgs& b, int first, int lane) {
-  const int i = first + lane;
-  if (i >= b.n_seqs) return Seq{0, 0, 0};
-  return seq_of(b, b.q_start[i], b.q_start[i + 1], b.ctx_len[i]);
-}
 __device__ __forceinline__ int tiles_of(const Seq& s) {
   return s.tokens ? max(ceil_div(s.first + s.tokens, TILE), 1) : 0;
 }
@@ -112,11 +105,6 @@ __device__ __forceinline__ int lane_prefix(int v, int lane, int n) {
   }
   return v;
 }
-__device__ __forceinline__ Seq of_lane(const Seq& s, int l) {
-  return Seq{__builtin_amdgcn_readlane(s.row, l), __builtin_amdgcn_readlane(s.tokens, l),
-             __builtin_amdgcn_readlane(s.first, l)};
-}
-
 // A set of rows among the tiles of all: its sequence and token (listed pages), its tiles [first, first + tiles).
 struct Set {
   Seq seq;
@@ -149,18 +137,10 @@ __device__ __forceinline__ Set find_seq(const BatchArgs& b, int x_run, int row, 
   }
   return Set{Seq{0, 0, 0}, -1, 0, 0, 0};
 }
-// The sequence that row `row` belongs to (b < 0: none).
-__device__ __forceinline__ Set seq_of_row(const BatchArgs& b, int row, int lane) {
-  for (int i = 0; i < b.n_seqs; i += 64) {
-    const Seq s = lane_seq(b, i, lane);
-    const unsigned long long at = __ballot(row >= s.row && row < s.row + s.tokens);
-    if (at) {
-      const int l = __ffsll(at) - 1;
-      const Seq q = of_lane(s, l);
-      return Set{q, i + l, row - q.row, 0, 0};
-    }
-  }
-  return Set{Seq{0, 0, 0}, -1, 0, 0, 0};
+// A token's set for listed pages, each of `tiles` tiles.
+__device__ __forceinline__ Set listed_set(const AttnArgs& a, int row, int tiles, int lane) {
+  const RowOf r = seq_of_row(a.b, row, lane);
+  return Set{r.seq, r.b, r.token, row * tiles, tiles};
 }
 // The set that holds tile x_run * run, or (x_run < 0) row `row`.
 template <bool SEL>
@@ -170,10 +150,7 @@ __device__ __forceinline__ Set find_set(const AttnArgs& a, int x_run, int row, i
   *run = run_tiles(a.plan, a.b.n_tokens * each);
   if (x_run >= 0) row = x_run * *run / each;
   if (row >= a.b.n_tokens) return Set{Seq{0, 0, 0}, -1, 0, a.b.n_tokens * each, 0};
-  Set s = seq_of_row(a.b, row, lane);
-  s.first = row * each;
-  s.tiles = each;
-  return s;
+  return listed_set(a, row, each, lane);
 }
 // The set behind this one (tiles 0: none).
 template <bool SEL>
@@ -182,10 +159,7 @@ __device__ __forceinline__ Set next_set(const AttnArgs& a, const Set& s, int lan
   if (SEL) {
     const int row = first / s.tiles;
     if (row >= a.b.n_tokens) return Set{Seq{0, 0, 0}, -1, 0, first, 0};
-    Set t = seq_of_row(a.b, row, lane);
-    t.first = first;
-    t.tiles = s.tiles;
-    return t;
+    return listed_set(a, row, s.tiles, lane);
   }
   for (int b = s.b + 1; b < a.b.n_seqs; ++b) {
     const Seq q = seq_of(a.b, a.b.q_start[b], a.b.q_start[b + 1], a.b.ctx_len[b]);
@@ -232,6 +206,8 @@ struct Tiles {
       index = idx < a.n_sel ? a.sel[((size_t)(set.seq.row + set.token) * a.c.kv_heads + h) * a.n_sel + idx] : -1;
       if (index >= 0 && len_max > 0 && index <= (len_max - 1) >> a.c.shift)
         number = page_or_none(table[index], a.c.n_pages);
+      else
+        index = 0;  // not used
     } else if (idx << a.c.shift < len_max) {
       number = page_or_none(table[idx], a.c.n_pages);
     }

@@ -4,8 +4,7 @@
 #include <float.h>
 #include <hip/hip_runtime.h>
 
-#include "hcr_device.h"
-#include "hcr_paged_layout.h"
+#include "hcr_paged_device.h"
 
 namespace hcr {
 
@@ -180,13 +179,10 @@ __global__ __launch_bounds__(64 * WAVES) void block_topk(TopkArgs a) {
   __shared__ uint32_t counts[2][WAVES];
   __shared__ uint32_t found[3][2];  // the digit, and how many keys lie above it
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int h = blockIdx.x % a.kv_heads;
-  const int bt = blockIdx.x / a.kv_heads;
-  const int t = bt % a.b.max_tokens, b = bt / a.b.max_tokens;
-  const Seq seq = seq_of(a.b, a.b.q_start[b], a.b.q_start[b + 1], a.b.ctx_len[b]);
-  if (t >= seq.tokens) return;
-  const size_t row = (size_t)(seq.row + t) * a.kv_heads + h;
-  const int pos = seq.first + t;
+  const RowOf of = seq_of_row(a.b, blockIdx.x / a.kv_heads, lane);
+  if (of.b < 0) return;
+  const size_t row = blockIdx.x;  // of scores and sel: token and kv head
+  const int pos = of.seq.first + of.token;
   const int count = pos < 0 ? 0 : (pos >> a.shift) + 1;  // pages up to the token's own
   int* sel = a.sel + row * a.n_sel;
   if (count <= a.n_sel) {
@@ -296,7 +292,7 @@ __global__ __launch_bounds__(64 * WAVES) void block_topk(TopkArgs a) {
 
 int launch_block_topk(const TopkArgs& a, void* stream) {
   (void)hipGetLastError();
-  const dim3 grid(a.b.n_seqs * a.b.max_tokens * a.kv_heads);
+  const dim3 grid(a.b.n_tokens * a.kv_heads);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   // as many waves as hold every score of the longest row
   if (a.b.max_ctx >> a.shift <= 4 * 64 * TOPK_KEYS)

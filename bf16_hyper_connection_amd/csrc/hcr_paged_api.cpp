@@ -24,7 +24,8 @@ Span span(const void* p, size_t bytes) {
 bool overlap(Span a, Span b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-constexpr long long GRID_MAX = 1ll << 30;  // work-groups of a launch, and rows of a call
+constexpr long long ROWS_MAX = 1ll << 30;  // rows of heads of a call, positions, tiles: 32 bits hold them
+constexpr long long THREADS_MAX = (1ll << 32) - 1;  // of a launch
 
 size_t pages_elements(const CacheArgs& c) {
   return ((size_t)c.n_pages * c.kv_heads * c.head_dim) << c.shift;
@@ -65,10 +66,15 @@ int check_bounds(const CacheArgs& c, const hcr_batch* in, int heads, BatchArgs* 
   if (b->max_tokens > b->n_tokens) b->max_tokens = b->n_tokens;
   if (b->n_seqs == 0 || b->max_tokens == 0) return 1;
   // rows and work-groups stay inside 32 bits
-  if ((long long)b->n_tokens * heads > GRID_MAX || (long long)b->n_seqs * b->max_tokens > GRID_MAX / heads ||
-      (long long)b->n_seqs * ceil_div(b->max_ctx, TILE) > GRID_MAX)
+  if ((long long)b->n_tokens * heads > ROWS_MAX || (long long)b->n_seqs * b->max_tokens > ROWS_MAX / heads ||
+      (long long)b->n_seqs * ceil_div(b->max_ctx, TILE) > ROWS_MAX)
     return HCR_EINVAL;
   return HCR_OK;
+}
+// Page lists whose positions and tiles (all tokens' together) 32 bits hold.
+bool lists_fit(const CacheArgs& c, const BatchArgs& b, int n_sel) {
+  return n_sel >= 0 && (long long)n_sel << c.shift <= ROWS_MAX &&
+         ((long long)n_sel << (c.shift - TILE_SHIFT)) * b.n_tokens <= ROWS_MAX;
 }
 int check_arrays(const BatchArgs& b) {
   if (!b.q_start || !b.ctx_len || (!b.table && b.table_stride)) return HCR_EINVAL;
@@ -107,14 +113,14 @@ int attn(hcr_cache_t h, const hcr_batch* batch, int heads, double scale, const v
   if (rc < 0) return rc;
   if (out_type != HCR_F32 && out_type != HCR_BF16) return HCR_EINVAL;
   if (!(scale > -1e30 && scale < 1e30)) return HCR_EINVAL;  // NaN and infinite too
-  if (n_sel < 0 || (long long)n_sel << c.shift > GRID_MAX) return HCR_EINVAL;
+  if (!lists_fit(c, a.b, n_sel)) return HCR_EINVAL;
   if (rc == 1) return HCR_OK;
-  if (((long long)n_sel << c.shift) / TILE * a.b.n_tokens > GRID_MAX) return HCR_EINVAL;  // tiles, in 32 bits
   if (!q || !out) return HCR_EINVAL;
   if (const int e = check_arrays(a.b)) return e;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(sel, 4) || !aligned(scratch, 256)) return HCR_EALIGN;
   a.plan = attn_plan(c, a.b, heads, n_sel);
-  if (attn_grid(c, a.plan) > GRID_MAX) return HCR_EINVAL;
+  if (attn_grid(c, a.plan) * 64 * 16 > THREADS_MAX || (long long)a.b.n_tokens * heads * 256 > THREADS_MAX)
+    return HCR_EINVAL;
   const size_t need = scratch_of(c, a.b, n_sel, a.plan);
   if (need && (!scratch || scratch_bytes < need)) return HCR_ESCRATCH;
   const size_t values = (size_t)a.b.n_tokens * heads * c.head_dim;
@@ -236,8 +242,7 @@ int hcr_cache_append(hcr_cache_t h, const hcr_batch* batch, int heads, int type,
   in[3] = span(q_norm, (size_t)c.head_dim * 4);
   in[4] = span(k_norm, (size_t)c.head_dim * 4);
   in[5] = span(rope_dim ? rope : nullptr, (size_t)rope_rows * rope_dim * 4);
-  const long long pages = ((a.b.max_tokens - 1) >> c.shift) + 2;
-  if (a.b.n_seqs * pages * c.kv_heads * 2 > GRID_MAX) return HCR_EINVAL;
+  if (append_grid(c, a.b, heads).groups * APPEND_THREADS > THREADS_MAX) return HCR_EINVAL;
   const Span so = span(q_out, (size_t)a.b.n_tokens * heads * c.head_dim * 2);
   const CacheSpans sc = cache_spans(c);
   if (overlap_any(so, sc) || overlap_any(so, batch_spans(a.b))) return HCR_EALIAS;
@@ -262,9 +267,7 @@ int hcr_cache_append(hcr_cache_t h, const hcr_batch* batch, int heads, int type,
 
 size_t hcr_attn_scratch_bytes(hcr_cache_t h, const hcr_batch* batch, int heads, int n_sel) {
   BatchArgs b;
-  if (!h || check_bounds(h->args, batch, heads, &b) != HCR_OK || n_sel < 0 ||
-      (long long)n_sel << h->args.shift > GRID_MAX / b.n_tokens * TILE)
-    return 0;
+  if (!h || check_bounds(h->args, batch, heads, &b) != HCR_OK || !lists_fit(h->args, b, n_sel)) return 0;
   return scratch_of(h->args, b, n_sel, attn_plan(h->args, b, heads, n_sel));
 }
 
@@ -293,7 +296,7 @@ int hcr_block_scores(hcr_cache_t h, const hcr_batch* batch, int heads, const voi
   if (!q || !scores) return HCR_EINVAL;
   if (const int e = check_arrays(a.b)) return e;
   if (!aligned(q, 16) || !aligned(scores, 16)) return HCR_EALIGN;
-  if ((long long)a.b.n_seqs * c.kv_heads * (pages / 16 + 1) > GRID_MAX) return HCR_EINVAL;
+  if ((long long)a.b.n_seqs * c.kv_heads * (pages / 64 + 1) * 256 > THREADS_MAX) return HCR_EINVAL;
   const Span so = span(scores, (size_t)a.b.n_tokens * c.kv_heads * scores_stride * 4);
   if (overlap(so, span(q, (size_t)a.b.n_tokens * heads * c.head_dim * 2)) || overlap_any(so, cache_spans(c)) ||
       overlap_any(so, batch_spans(a.b)))
@@ -321,6 +324,7 @@ int hcr_block_topk(hcr_cache_t h, const hcr_batch* batch, const float* scores, i
   if (const int e = check_arrays(a.b)) return e;
   if (!aligned(scores, 16) || !aligned(sel, 4)) return HCR_EALIGN;
   const size_t rows = (size_t)a.b.n_tokens * c.kv_heads;
+  if (rows * 1024 > (size_t)THREADS_MAX) return HCR_EINVAL;
   const Span so = span(sel, rows * n_sel * 4);
   if (overlap(so, span(scores, rows * scores_stride * 4)) || overlap_any(so, batch_spans(a.b))) return HCR_EALIAS;
   a.scores = scores;

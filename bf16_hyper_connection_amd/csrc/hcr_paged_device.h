@@ -1,0 +1,38 @@
+// Device helpers of the paged cache's kernels: which sequence a row of the batch belongs to.
+#pragma once
+
+#include "hcr_device.h"
+#include "hcr_paged_layout.h"
+
+namespace hcr {
+
+// The sequences 64 at a time, one per lane.
+__device__ __forceinline__ Seq lane_seq(const BatchArgs& b, int first, int lane) {
+  const int i = first + lane;
+  if (i >= b.n_seqs) return Seq{0, 0, 0};
+  return seq_of(b, b.q_start[i], b.q_start[i + 1], b.ctx_len[i]);
+}
+__device__ __forceinline__ Seq of_lane(const Seq& s, int l) {
+  return Seq{__builtin_amdgcn_readlane(s.row, l), __builtin_amdgcn_readlane(s.tokens, l),
+             __builtin_amdgcn_readlane(s.first, l)};
+}
+
+// The sequence that row `row` of the batch belongs to and its token among the sequence's new ones (b < 0: none).
+struct RowOf {
+  Seq seq;
+  int b, token;
+};
+__device__ __forceinline__ RowOf seq_of_row(const BatchArgs& b, int row, int lane) {
+  for (int i = 0; i < b.n_seqs; i += 64) {
+    const Seq s = lane_seq(b, i, lane);
+    const unsigned long long at = __ballot(row >= s.row && row < s.row + s.tokens);
+    if (at) {
+      const int l = __ffsll(at) - 1;
+      const Seq q = of_lane(s, l);
+      return RowOf{q, i + l, row - q.row};
+    }
+  }
+  return RowOf{Seq{0, 0, 0}, -1, 0};
+}
+
+}  // namespace hcr

@@ -142,6 +142,22 @@ struct AppendArgs {
   uint16_t* q_out;
 };
 int launch_append(const AppendArgs& a, void* stream);
+constexpr int APPEND_THREADS = 256;
+constexpr int APPEND_EACH = 4;  // tokens of a work-group of query heads, one where there are few
+HCR_HD int append_each(const BatchArgs& b) { return b.max_tokens >= 32 ? APPEND_EACH : 1; }
+// Work-groups: first those of (sequence, page, kv head, k or v), then those of (sequence, tokens, query heads).
+struct AppendGrid {
+  int pages, passes;  // pages that a window can touch; work-groups over the query heads
+  long long kv_groups, groups;
+};
+HCR_HD AppendGrid append_grid(const CacheArgs& c, const BatchArgs& b, int heads) {
+  AppendGrid g;
+  g.pages = ((b.max_tokens - 1) >> c.shift) + 2;
+  g.passes = ceil_div(heads, APPEND_THREADS / (c.head_dim / 8));
+  g.kv_groups = (long long)b.n_seqs * g.pages * c.kv_heads * 2;
+  g.groups = g.kv_groups + (long long)b.n_seqs * ceil_div(b.max_tokens, append_each(b)) * g.passes;
+  return g;
+}
 
 // ---- scores and selection
 struct ScoreArgs {
