@@ -137,6 +137,11 @@ __device__ __forceinline__ Set find_seq(const BatchArgs& b, int x_run, int row, 
   }
   return Set{Seq{0, 0, 0}, -1, 0, 0, 0};
 }
+// A sequence's set where no other is counted.
+__device__ __forceinline__ Set seq_set(const BatchArgs& b, int i) {
+  const Seq q = seq_of(b, b.q_start[i], b.q_start[i + 1], b.ctx_len[i]);
+  return Set{q, q.tokens ? i : -1, 0, 0, tiles_of(q)};
+}
 // A token's set for listed pages, each of `tiles` tiles.
 __device__ __forceinline__ Set listed_set(const AttnArgs& a, int row, int tiles, int lane) {
   const RowOf r = seq_of_row(a.b, row, lane);
@@ -509,8 +514,14 @@ __global__ __launch_bounds__(64 * attn_waves(D, MT)) void attn_part(AttnArgs a) 
   const int h = u % a.c.kv_heads, item = u / a.c.kv_heads;
   if (item >= a.plan.items) return;
   int run;
-  Set set = find_set<SEL>(a, item, 0, lane, &run);
-  const int begin = item * run;
+  Set set;
+  if (a.plan.whole) {
+    set = SEL ? listed_set(a, item, a.n_sel << (a.c.shift - TILE_SHIFT), lane) : seq_set(a.b, item);
+    run = set.tiles;
+  } else {
+    set = find_set<SEL>(a, item, 0, lane, &run);
+  }
+  const int begin = a.plan.whole ? set.first : item * run;
   const size_t slots = (size_t)a.c.kv_heads * RB * a.plan.items * 2;
   const size_t slot = ((size_t)h * RB + rb) * a.plan.items * 2;
   while (set.tiles > 0 && set.first < begin + run) {
@@ -621,7 +632,7 @@ void run_attn(const AttnArgs& a, int grid, int join_grid, hipStream_t st) {
 int launch_attn(const AttnArgs& a, void* stream) {
   const AttnPlan& p = a.plan;
   const int grid = ceil_div(p.items * a.c.kv_heads, XCDS) * XCDS * p.row_blocks;
-  const int join_grid = attn_joins(p, a.n_sel << (a.c.shift - TILE_SHIFT), a.b.n_tokens) ? a.b.n_tokens * a.heads : 0;
+  const int join_grid = attn_joins(p) ? a.b.n_tokens * a.heads : 0;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   (void)hipGetLastError();
   switch (a.c.head_dim) {

@@ -98,8 +98,8 @@ long long attn_grid(const CacheArgs& c, const AttnPlan& p) {
   return ((long long)p.items * c.kv_heads + XCDS - 1) / XCDS * XCDS * p.row_blocks;
 }
 
-size_t scratch_of(const CacheArgs& c, const BatchArgs& b, int n_sel, const AttnPlan& p) {
-  if (!attn_joins(p, n_sel << (c.shift - TILE_SHIFT), b.n_tokens)) return 0;
+size_t scratch_of(const CacheArgs& c, const AttnPlan& p) {
+  if (!attn_joins(p)) return 0;
   return align256((size_t)c.kv_heads * p.row_blocks * p.items * 2 * attn_rows(p) * (c.head_dim + 2) * 4);
 }
 
@@ -121,7 +121,7 @@ int attn(hcr_cache_t h, const hcr_batch* batch, int heads, double scale, const v
   a.plan = attn_plan(c, a.b, heads, n_sel);
   if (attn_grid(c, a.plan) * 64 * 16 > THREADS_MAX || (long long)a.b.n_tokens * heads * 256 > THREADS_MAX)
     return HCR_EINVAL;
-  const size_t need = scratch_of(c, a.b, n_sel, a.plan);
+  const size_t need = scratch_of(c, a.plan);
   if (need && (!scratch || scratch_bytes < need)) return HCR_ESCRATCH;
   const size_t values = (size_t)a.b.n_tokens * heads * c.head_dim;
   const Span so = span(out, values * (out_type == HCR_F32 ? 4 : 2)), sq = span(q, values * 2);
@@ -148,18 +148,25 @@ int attn(hcr_cache_t h, const hcr_batch* batch, int heads, double scale, const v
 
 }  // namespace
 
-// Measured on MI355X, 8 kv heads, graphs of calls on rotated inputs (us a call):
+// Measured on MI355X, 8 kv heads, graphs of calls on rotated inputs (us a call), lengths from an eighth of the
+// longest up to it:
 //   row tiles  two 16-row tiles a wave for D = 128 from 17 rows on: 24 rows 154 against 160, 64 rows 161 against 185
 //              (D = 64: 92 against 90, and D = 256 has no registers for it)
-//   waves      8 a work-group, one work-group a CU, for long sequences (D = 256, one sequence of 420,000: 568
-//              against 575 with 4; 64 of up to 8,192, D = 128: 216 against 218); 4, two work-groups a CU, where no
-//              sequence is longer than 2,048 (64 of up to 300: 28 against 34; one of 2,000, D = 256: 13.4
-//              against 14.5), since a short one is mostly the wait for its first loads
 //   rows       several row waves, D = 256: one group, as many work-groups as fit a CU (36 rows: 314 against 432
 //              with two groups), four row waves at most (96 rows: 484 against 544 with six in one work-group)
-//   lists      one work-group a list where there are lists enough, and nothing to join (32 tokens: 52 against 56)
+//   whole      a work-group a set and no join, where the chip is full of them or they end soon.  512 work-groups,
+//              D = 128: up to 300 positions 14 against 28, 700 24 against 33, 4,000 93 against 104; 256: 700 16
+//              against 28, 2,000 35 against 39 (D = 256 66 against 64), 8,192 127 against 101; 8: 300 7.1 against
+//              9.7, 700 9.2 against 9.7, 1,200 11.4 against 9.6.  Beyond 4,096 the runs stay, although lengths as
+//              even as these would still gain 5 % (8,192: 184 against 194): one long sequence among short ones
+//              would hold a single CU for the whole call.  36 rows of D = 256: 700 63 against 74, 2,000 158
+//              against 153
+//   waves      8 a work-group, one work-group a CU, for long sequences (D = 256, one sequence of 420,000: 568
+//              against 575 with 4); 4, two work-groups a CU, for runs where no sequence is longer than 2,048 (one of
+//              2,000, D = 256: 13.4 against 14.5) and for many sets of up to 512 (300: 14 against 17), since a short
+//              one is mostly the wait for its first loads
 AttnPlan attn_plan(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel) {
-  constexpr int CUS = 256, SHORT = 64;  // tiles
+  constexpr int CUS = 256;
   AttnPlan p{};
   const int group = heads / c.kv_heads;
   const int rows = n_sel ? group : b.max_tokens * group;
@@ -168,19 +175,28 @@ AttnPlan attn_plan(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel)
   const int row_tiles = ceil_div(rows, 16 * p.q_tiles);
   p.row_blocks = ceil_div(row_tiles, wide ? 4 : 8);
   p.row_waves = ceil_div(row_tiles, p.row_blocks);
+  const bool alone = wide && p.row_waves > 1;  // row waves fill a work-group
+
   const int tiles = n_sel ? n_sel << (c.shift - TILE_SHIFT) : ceil_div(b.max_ctx, TILE);
-  const int waves = !n_sel && tiles <= SHORT ? 4 : 8;
-  p.groups = (wide && p.row_waves > 1) || p.row_waves > waves ? 1 : waves / p.row_waves;
-  if (p.groups > tiles) p.groups = tiles > 0 ? tiles : 1;
-  p.least = p.groups;
   const int units = c.kv_heads * p.row_blocks;
-  const int fill = wide && p.row_waves > 1 ? CUS * (8 / p.row_waves) : CUS * (8 / waves);
   const long long sets = n_sel ? b.n_tokens : b.n_seqs;
+  const long long full = sets * units;  // work-groups of whole sets
+  p.whole = full < CUS              ? tiles <= (wide ? 12 : 24)
+            : n_sel                 ? 1  // lists are alike
+            : alone                 ? tiles <= 32
+            : full < 2 * CUS        ? tiles <= 64
+                                    : tiles <= 128;
+  const int waves = p.whole ? (full >= 2 * CUS && tiles <= 16 ? 4 : 8) : (!n_sel && tiles <= 64 ? 4 : 8);
+  p.groups = alone || p.row_waves > waves ? 1 : waves / p.row_waves;
+  if (p.groups > tiles) p.groups = tiles > 0 ? tiles : 1;
+
+  p.least = p.groups;
   const long long most = (sets * (tiles > 0 ? tiles : 1) + p.least - 1) / p.least;
+  const int fill = alone ? CUS * (8 / p.row_waves) : CUS * (8 / waves);
   long long items = fill / units;
-  if (n_sel) items = items > sets ? items / sets * sets : sets;
+  if (n_sel) items = items > sets ? items / sets * sets : sets;  // lists cut alike
   if (items > most) items = most;
-  p.items = items > 1 ? (int)items : 1;
+  p.items = p.whole ? (int)sets : items > 1 ? (int)items : 1;
   return p;
 }
 
@@ -268,7 +284,7 @@ int hcr_cache_append(hcr_cache_t h, const hcr_batch* batch, int heads, int type,
 size_t hcr_attn_scratch_bytes(hcr_cache_t h, const hcr_batch* batch, int heads, int n_sel) {
   BatchArgs b;
   if (!h || check_bounds(h->args, batch, heads, &b) != HCR_OK || !lists_fit(h->args, b, n_sel)) return 0;
-  return scratch_of(h->args, b, n_sel, attn_plan(h->args, b, heads, n_sel));
+  return scratch_of(h->args, attn_plan(h->args, b, heads, n_sel));
 }
 
 int hcr_attn(hcr_cache_t c, const hcr_batch* batch, int heads, double scale, const void* q, int out_type, void* out,

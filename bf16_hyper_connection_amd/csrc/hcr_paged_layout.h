@@ -91,6 +91,7 @@ struct AttnPlan {
   int row_blocks;  // work-groups over a set's rows
   int items;       // work-groups over the tiles
   int least;       // tiles that are worth a work-group
+  int whole;       // a work-group for each set instead, with all of its tiles: nothing to join
 };
 HCR_HD int attn_rows(const AttnPlan& p) { return p.row_waves * p.q_tiles * 16; }  // of a work-group
 // Tiles of one run, from those of all sets (every set has one at least: a set without positions writes its zeros).
@@ -102,12 +103,8 @@ HCR_HD int run_tiles(const AttnPlan& p, int tiles_of_all) {
 // A run has two places for parts: of the set that began before it, and of the set that goes on behind it.
 HCR_HD int run_parts(int first, int tiles, int run) { return (first + tiles - 1) / run - first / run + 1; }
 HCR_HD int part_slot(int run_index, int run, int first) { return 2 * run_index + (first >= run_index * run); }
-// Whether a set may have several parts, to be joined by a second launch (listed pages, whose lengths the host knows:
-// not where runs are whole lists).
-HCR_HD bool attn_joins(const AttnPlan& p, int list_tiles, int n_tokens) {
-  if (list_tiles) return p.items > 1 && run_tiles(p, list_tiles * n_tokens) % list_tiles;
-  return p.items > 1;
-}
+// Whether a set may have several parts, to be joined by a second launch.
+HCR_HD bool attn_joins(const AttnPlan& p) { return p.items > 1 && !p.whole; }
 // Bytes of LDS of a work-group: its query rows, in their place what its groups join in, and the groups' (m, l).
 HCR_HD int attn_lds_values(int D, const AttnPlan& p) {
   return attn_rows(p) * D * (p.groups > 1 ? p.groups * 4 : 2);

@@ -90,6 +90,10 @@ static const char* check_plans() {
                   CHECK(p.row_blocks * attn_rows(p) >= rows && (p.row_blocks - 1) * attn_rows(p) < rows);
                   CHECK(attn_lds(D, p) <= 160 * 1024 && attn_lds(D, p) >= attn_rows(p) * D * 2);
                   CHECK(p.least >= 1 && p.items >= 1);
+                  if (p.whole) {
+                    CHECK(p.items == (n_sel ? seqs * tokens : seqs) && !attn_joins(p));
+                    continue;
+                  }
                   for (int turn = 0; turn < 3; ++turn) {  // lengths: all the longest, random, one long
                     const int sets = n_sel ? seqs * tokens : seqs;
                     if (sets > 2000) continue;
@@ -107,7 +111,7 @@ static const char* check_plans() {
                     int first = 0;
                     for (int x : t) {  // every part of every set has a place of its own
                       const int n = run_parts(first, x, run);
-                      CHECK(n >= 1 && (n == 1 || attn_joins(p, n_sel * (page / TILE), sets)));
+                      CHECK(n >= 1 && (n == 1 || attn_joins(p)));
                       for (int k = 0; k < n && n > 1; ++k) {
                         const int slot = part_slot(first / run + k, run, first);
                         CHECK(slot >= 0 && slot < 2 * p.items && !used[slot]);

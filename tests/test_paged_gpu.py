@@ -86,6 +86,44 @@ def test_attend_split_lengths(head_dim, page, kv, group, T):
     pu.check_rows(out, want, tol, "splits")
 
 
+@pytest.mark.parametrize("head_dim,kv,group,T", [(128, 1, 4, 1), (64, 1, 2, 3), (256, 1, 6, 4)])
+def test_attend_runs_over_many_short_sequences(head_dim, kv, group, T):
+    """More sequences than a wave has lanes, one of them long: runs that hold several sequences, begin and end
+    inside one, or skip sequences without new tokens."""
+    g = gen.rng(99, head_dim)
+    windows = [(int(t), int(c)) for t, c in zip(g.integers(0, T + 1, 150), g.integers(0, 90, 150))]
+    windows[70] = (T, 6000)
+    windows[149] = (1, 33)
+    s = pu.scene(12, kv, head_dim, 32, windows)
+    out, want, tol = _attend(s, kv * group)
+    pu.check_rows(out, want, tol, "runs")
+
+
+@pytest.mark.parametrize("head_dim,kv,group,most", [(128, 2, 2, 500), (64, 2, 1, 2000), (256, 2, 1, 300), (128, 2, 9, 400)])
+def test_attend_many_sequences(head_dim, kv, group, most):
+    """A work-group a sequence, more of them than the chip holds at once."""
+    g = gen.rng(100, head_dim)
+    s = pu.scene(13, kv, head_dim, 64, [(1, int(c)) for c in g.integers(0, most, 270)] + [(2, most)])
+    out, want, tol = _attend(s, kv * group, out_dtype=torch.bfloat16)
+    pu.check_rows(out, want, tol, "many")
+
+
+def test_lengths_and_rows_beyond_the_bounds_are_cut():
+    """ctx_len above max_ctx counts as max_ctx, rows past n_tokens and past max_tokens do not exist."""
+    s = pu.scene(14, 2, 128, 64, [(2, 640), (3, 200)])
+    q = pu.queries(14, 4, 4, 128)
+    keys, values = pu.decoded(s)
+    cut = (np.array([0, 2, 4], np.int32), np.array([600, 200], np.int32), s.table)  # the second: rows 2 and 3
+    want = oracle.paged.attend(cut, keys, values, oracle.bf16_bits_to_f64(q), 0.1)
+    batch = pu.dev_batch(s, max_tokens=2, max_ctx=600)
+    out = pu.dev_cache(s).attend(batch, pu.dev_bits(q), scale=0.1)
+    pu.check_rows(out, want, pu.rows_tolerance(oracle.bf16_bits_to_f64(q), 20.0, 0.1, 640, False), "cut")
+    batch.q_start.copy_(torch.tensor([-3, 2 ** 31 - 1, 1], dtype=torch.int32))  # no sequence has rows
+    again = torch.full_like(out, 3.0)
+    pu.dev_cache(s).attend(batch, pu.dev_bits(q), scale=0.1, out=again)
+    assert torch.all(again == 3.0)
+
+
 def test_attend_with_loose_bounds():
     """Bounds above what the sequences have (as a captured graph keeps them), rows behind the last sequence's."""
     s = pu.scene(5, 2, 128, 64, [(2, 100), (1, 700)], table_extra=40)
@@ -158,6 +196,16 @@ def test_attend_blocks(head_dim, page, kv, group, out_dtype):
     out, want, tol = _attend(s, kv * group, out_dtype=out_dtype, sel=sel)
     assert torch.all(out[2] == 0)
     pu.check_rows(out, want, tol, "blocks")
+
+
+def test_attend_blocks_many_tokens():
+    """More sequences than a wave has lanes, a list for each of their tokens; rows behind the last one's."""
+    g = gen.rng(101, 1)
+    windows = [(int(t), int(c)) for t, c in zip(g.integers(0, 4, 90), g.integers(1, 300, 90))]
+    s = pu.scene(15, 2, 64, 32, windows)
+    sel = g.integers(-1, 10, size=(s.n_tokens + 3, 2, 5)).astype(np.int32)
+    out, want, tol = _attend(s, 6, sel=sel, extra_rows=3)
+    pu.check_rows(out, want, tol, "tokens")
 
 
 def test_attend_blocks_long_list():
@@ -310,6 +358,26 @@ def _scores_of(kind, n, kv, pages):
     for value in (np.nan, np.inf, -np.inf, -0.0, 0.0, 1e-45, -1e-45, np.finfo(np.float32).min):
         x[g.random(x.shape) < 0.1] = value
     return x
+
+
+def test_block_topk_of_ragged_windows():
+    """Rows of more sequences than a wave has lanes, windows of 0 to 5 tokens."""
+    g = gen.rng(102, 1)
+    page, kv = 32, 3
+    tokens = g.integers(0, 6, 100)
+    starts = np.concatenate([[0], np.cumsum(tokens)]).astype(np.int32)
+    lens = (tokens + g.integers(0, 2500, 100)).astype(np.int32)
+    table = np.zeros((100, 80), np.int32)
+    n = int(starts[-1])
+    scores = g.standard_normal((n + 2, kv, 80)).astype(np.float32)
+    want = oracle.paged.block_topk((starts, lens, table), page, scores, 9, 2, 1)
+    cache = paged.PagedCache.allocate(1, kv, 64, page)
+    batch = paged.Batch(torch.from_numpy(starts).cuda(), torch.from_numpy(lens).cuda(),
+                        torch.from_numpy(table).cuda(), 5, 2560)
+    sel = torch.full((n + 2, kv, 9), 77, dtype=torch.int32, device="cuda")
+    cache.block_topk(batch, torch.from_numpy(scores).cuda(), 9, n_first=2, n_last=1, sel=sel)
+    got = sel.cpu().numpy()
+    assert all(np.array_equal(got[r], w) for r, w in want.items()) and np.all(got[n:] == 77)
 
 
 @pytest.mark.parametrize("kind", ["normal", "level", "few", "odd"])
