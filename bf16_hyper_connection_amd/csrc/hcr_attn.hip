@@ -435,12 +435,11 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
 #pragma unroll
   for (int m = 0; m < MT; ++m) sum[m] = rows_sum(sum[m]);
 
-  // the groups joined: every wave leaves its state in LDS and takes its share of its row tile's values
-  // (the values where the query rows were, which nobody reads behind the first barrier here)
-  f32x4* lds_acc = reinterpret_cast<f32x4*>(lds);                            // [TG][RT][MT * DT][64]
-  float* lds_m = reinterpret_cast<float*>(lds_acc + TG * RT * MT * DT * 64);  // [TG][RT][MT][16]
+  // the groups joined, a 16-row tile at a time: every wave leaves its values in LDS and takes its share of the row
+  // tile's (the values where the query rows were, which nobody reads behind the first barrier here)
+  f32x4* lds_acc = reinterpret_cast<f32x4*>(lds);                       // [TG][RT][DT][64]
+  float* lds_m = reinterpret_cast<float*>(lds_acc + TG * RT * DT * 64);  // [TG][RT][MT][16]
   float* lds_l = lds_m + TG * RT * MT * 16;
-  float w_own[MT];  // what this wave's values weigh in the sum
   if (TG > 1) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -450,54 +449,50 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
       }
     }
     __syncthreads();
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      float top = -FLT_MAX, total = 0.f;
-      for (int g0 = 0; g0 < TG; g0 += 4) {
-        float gm[4], gl[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int at = ((min(g0 + i, TG - 1) * RT + rt) * MT + m) * 16 + li;
-          gm[i] = lds_m[at];
-          gl[i] = g0 + i < TG ? lds_l[at] : 0.f;
-        }
-        const float high = fmaxf(fmaxf(fmaxf(gm[0], gm[1]), fmaxf(gm[2], gm[3])), top);
-        total *= exp2_of(top - high);
-        top = high;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) total += gl[i] * exp2_of(gm[i] - top);
-      }
-      w_own[m] = exp2_of(mx[m] - top);
-      mx[m] = top;
-      sum[m] = total;
-#pragma unroll
-      for (int d = 0; d < DT; ++d) lds_acc[(wave * MT * DT + m * DT + d) * 64 + lane] = acc[m][d] * w_own[m];
-    }
-    __syncthreads();
   }
-
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    if (!live[m]) continue;
     const int slot_row = (rt * MT + m) * 16 + li;
     if (TG == 1) {
+      if (live[m]) {
 #pragma unroll
-      for (int d = 0; d < DT; ++d) out.values(D, rid[m], slot_row, 16 * d + 4 * lg, acc[m][d], sum[m]);
-    } else {
-      for (int d = tg; d < DT; d += TG) {
-        f32x4 o = {0.f, 0.f, 0.f, 0.f};
-        for (int g0 = 0; g0 < TG; g0 += 4) {
-          f32x4 v[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            v[i] = lds_acc[((min(g0 + i, TG - 1) * RT + rt) * MT * DT + m * DT + d) * 64 + lane];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o += g0 + i < TG ? v[i] : f32x4{0.f, 0.f, 0.f, 0.f};
-        }
-        out.values(D, rid[m], slot_row, 16 * d + 4 * lg, o, sum[m]);
+        for (int d = 0; d < DT; ++d) out.values(D, rid[m], slot_row, 16 * d + 4 * lg, acc[m][d], sum[m]);
+        if (lg == 0) out.state(D, slot_row, mx[m], sum[m]);
       }
+      continue;
     }
-    if (tg == 0 && lg == 0) out.state(D, slot_row, mx[m], sum[m]);
+    float top = -FLT_MAX, total = 0.f;
+    for (int g0 = 0; g0 < TG; g0 += 4) {
+      float gm[4], gl[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = ((min(g0 + i, TG - 1) * RT + rt) * MT + m) * 16 + li;
+        gm[i] = lds_m[at];
+        gl[i] = g0 + i < TG ? lds_l[at] : 0.f;
+      }
+      const float high = fmaxf(fmaxf(fmaxf(gm[0], gm[1]), fmaxf(gm[2], gm[3])), top);
+      total *= exp2_of(top - high);
+      top = high;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) total += gl[i] * exp2_of(gm[i] - top);
+    }
+    const float own = exp2_of(mx[m] - top);  // what this wave's values weigh in the sum
+    if (m > 0) __syncthreads();              // the tile before is taken
+#pragma unroll
+    for (int d = 0; d < DT; ++d) lds_acc[(wave * DT + d) * 64 + lane] = acc[m][d] * own;
+    __syncthreads();
+    for (int d = tg; d < DT; d += TG) {
+      f32x4 o = {0.f, 0.f, 0.f, 0.f};
+      for (int g0 = 0; g0 < TG; g0 += 4) {
+        f32x4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = lds_acc[((min(g0 + i, TG - 1) * RT + rt) * DT + d) * 64 + lane];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o += g0 + i < TG ? v[i] : f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+      if (live[m]) out.values(D, rid[m], slot_row, 16 * d + 4 * lg, o, total);
+    }
+    if (live[m] && tg == 0 && lg == 0) out.state(D, slot_row, top, total);
   }
 }
 
@@ -621,7 +616,7 @@ void run_attn(const AttnArgs& a, int grid, int join_grid, hipStream_t st) {
   const int join = a.plan.items > 2 * (SEL ? a.b.n_tokens : a.b.n_seqs) ? 256 : 64;
   if (a.plan.q_tiles == 1) {
     run_part<D, 1, SEL>(a, grid, st);
-  } else if constexpr (D == 128) {
+  } else if constexpr (D != 64) {
     run_part<D, 2, SEL>(a, grid, st);
   }
   if (join_grid) hipLaunchKernelGGL((attn_join<D, SEL>), dim3(join_grid), dim3(join), 0, st, a);

@@ -150,17 +150,19 @@ int attn(hcr_cache_t h, const hcr_batch* batch, int heads, double scale, const v
 
 // Measured on MI355X, 8 kv heads, graphs of calls on rotated inputs (us a call), lengths from an eighth of the
 // longest up to it:
-//   row tiles  two 16-row tiles a wave for D = 128 from 17 rows on: 24 rows 154 against 160, 64 rows 161 against 185
-//              (D = 64: 92 against 90, and D = 256 has no registers for it)
+//   row tiles  two 16-row tiles a wave from 17 rows on.  D = 128: 24 rows 154 against 160, 64 rows 161 against 185.
+//              D = 256 up to 32 rows, a wave a SIMD: 24 rows of 4 sequences of 90,010 260 against 302, of 64 of
+//              4,000 197 against 257.  Not D = 64 (92 against 90), nor three for D = 256 (36 rows 283 against 303,
+//              but 57 against 51 at 9,001: the accumulators no longer fit beside the operands)
 //   rows       several row waves, D = 256: one group, as many work-groups as fit a CU (36 rows: 314 against 432
 //              with two groups), four row waves at most (96 rows: 484 against 544 with six in one work-group)
 //   whole      a work-group a set and no join, where the chip is full of them or they end soon.  512 work-groups,
 //              D = 128: up to 300 positions 14 against 28, 700 24 against 33, 4,000 93 against 104; 256: 700 16
 //              against 28, 2,000 35 against 39 (D = 256 66 against 64), 8,192 127 against 101; 8: 300 7.1 against
-//              9.7, 700 9.2 against 9.7, 1,200 11.4 against 9.6.  Beyond 4,096 the runs stay, although lengths as
-//              even as these would still gain 5 % (8,192: 184 against 194): one long sequence among short ones
-//              would hold a single CU for the whole call.  36 rows of D = 256: 700 63 against 74, 2,000 158
-//              against 153
+//              9.7, 700 9.2 against 9.7, 1,200 11.4 against 9.6 (earlier for D = 256, whose tiles are twice the
+//              bytes: a CU alone takes about 35 GB/s).  36 rows of D = 256: 700 63 against 74, 2,000 158 against
+//              153.  Beyond 4,096 the runs stay, although lengths as even as these would still gain 5 % (8,192: 184
+//              against 194): one long sequence among short ones would hold a single CU for the whole call
 //   waves      8 a work-group, one work-group a CU, for long sequences (D = 256, one sequence of 420,000: 568
 //              against 575 with 4); 4, two work-groups a CU, for runs where no sequence is longer than 2,048 (one of
 //              2,000, D = 256: 13.4 against 14.5) and for many sets of up to 512 (300: 14 against 17), since a short
@@ -171,28 +173,30 @@ AttnPlan attn_plan(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel)
   const int group = heads / c.kv_heads;
   const int rows = n_sel ? group : b.max_tokens * group;
   const bool wide = c.head_dim == 256;
-  p.q_tiles = c.head_dim == 128 && rows > 16 ? 2 : 1;
+  p.q_tiles = rows > 16 && (c.head_dim == 128 || (wide && rows <= 32)) ? 2 : 1;
   const int row_tiles = ceil_div(rows, 16 * p.q_tiles);
   p.row_blocks = ceil_div(row_tiles, wide ? 4 : 8);
   p.row_waves = ceil_div(row_tiles, p.row_blocks);
+  const int most_waves = attn_waves(c.head_dim, p.q_tiles);
   const bool alone = wide && p.row_waves > 1;  // row waves fill a work-group
 
   const int tiles = n_sel ? n_sel << (c.shift - TILE_SHIFT) : ceil_div(b.max_ctx, TILE);
   const int units = c.kv_heads * p.row_blocks;
   const long long sets = n_sel ? b.n_tokens : b.n_seqs;
   const long long full = sets * units;  // work-groups of whole sets
-  p.whole = full < CUS              ? tiles <= (wide ? 12 : 24)
+  p.whole = full < CUS              ? tiles <= (!wide ? 24 : rows > 16 ? 6 : 12)
             : n_sel                 ? 1  // lists are alike
             : alone                 ? tiles <= 32
             : full < 2 * CUS        ? tiles <= 64
                                     : tiles <= 128;
-  const int waves = p.whole ? (full >= 2 * CUS && tiles <= 16 ? 4 : 8) : (!n_sel && tiles <= 64 ? 4 : 8);
+  const bool few = p.whole ? full >= 2 * CUS && tiles <= 16 : !n_sel && tiles <= 64;
+  const int waves = few || most_waves == 4 ? 4 : 8;
   p.groups = alone || p.row_waves > waves ? 1 : waves / p.row_waves;
   if (p.groups > tiles) p.groups = tiles > 0 ? tiles : 1;
 
   p.least = p.groups;
   const long long most = (sets * (tiles > 0 ? tiles : 1) + p.least - 1) / p.least;
-  const int fill = alone ? CUS * (8 / p.row_waves) : CUS * (8 / waves);
+  const int fill = most_waves == 4 ? CUS : alone ? CUS * (8 / p.row_waves) : CUS * (8 / waves);
   long long items = fill / units;
   if (n_sel) items = items > sets ? items / sets * sets : sets;  // lists cut alike
   if (items > most) items = most;

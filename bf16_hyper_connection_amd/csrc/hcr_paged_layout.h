@@ -77,8 +77,8 @@ HCR_HD int ceil_div(int a, int b) { return (a + b - 1) / b; }
 constexpr int TILE = 32;
 constexpr int TILE_SHIFT = 5;
 // Waves of a work-group at most: what its registers leave room for on a CU (one 16-row tile of D = 256 takes 243
-// of 512 registers of a lane, of D <= 128 at most 128, two tiles of D <= 128 up to 216).
-constexpr int attn_waves(int D, int q_tiles) { return D > 64 || q_tiles > 1 ? 8 : 16; }
+// of 512 registers of a lane, two 326; of D = 128 147 and 198; of D = 64 100).
+constexpr int attn_waves(int D, int q_tiles) { return D == 64 ? 16 : D == 256 && q_tiles > 1 ? 4 : 8; }
 
 // How a call is cut.  Its sets of rows (a sequence's window; one token for listed pages) have their tiles one set
 // behind the other, and the work-groups of a kv head and row block take equal runs of them, whatever set they belong
@@ -105,12 +105,11 @@ HCR_HD int run_parts(int first, int tiles, int run) { return (first + tiles - 1)
 HCR_HD int part_slot(int run_index, int run, int first) { return 2 * run_index + (first >= run_index * run); }
 // Whether a set may have several parts, to be joined by a second launch.
 HCR_HD bool attn_joins(const AttnPlan& p) { return p.items > 1 && !p.whole; }
-// Bytes of LDS of a work-group: its query rows, in their place what its groups join in, and the groups' (m, l).
-HCR_HD int attn_lds_values(int D, const AttnPlan& p) {
-  return attn_rows(p) * D * (p.groups > 1 ? p.groups * 4 : 2);
-}
+// Bytes of LDS of a work-group: its query rows, in their place what its groups join in, a 16-row tile of each wave
+// at a time, and the groups' (m, l).
 HCR_HD int attn_lds(int D, const AttnPlan& p) {
-  return attn_lds_values(D, p) + (p.groups > 1 ? p.groups * attn_rows(p) * 8 : 0);
+  const int rows = attn_rows(p);
+  return p.groups > 1 ? p.groups * (p.row_waves * 16 * D * 4 + rows * 8) : rows * D * 2;
 }
 AttnPlan attn_plan(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel);
 

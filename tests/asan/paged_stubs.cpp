@@ -85,7 +85,7 @@ static const char* check_plans() {
                   const BatchArgs b{nullptr, nullptr, nullptr, ctx / page + 1, seqs, seqs * tokens, tokens, ctx};
                   const AttnPlan p = attn_plan(c, b, kv * group, n_sel);
                   const int rows = n_sel ? group : tokens * group;
-                  CHECK(p.q_tiles == 1 || (p.q_tiles == 2 && D != 256));
+                  CHECK(p.q_tiles == 1 || (p.q_tiles == 2 && D != 64));
                   CHECK(p.row_waves * p.groups <= attn_waves(D, p.q_tiles) && p.groups >= 1 && p.row_waves >= 1);
                   CHECK(p.row_blocks * attn_rows(p) >= rows && (p.row_blocks - 1) * attn_rows(p) < rows);
                   CHECK(attn_lds(D, p) <= 160 * 1024 && attn_lds(D, p) >= attn_rows(p) * D * 2);
