@@ -110,24 +110,52 @@ struct Set {
   Seq seq;
   int b, token, first, tiles;  // b < 0: none
 };
-// The sequence whose tiles hold tile x, or (x < 0) the one that row `row` belongs to; *all: the tiles of all.
-__device__ __forceinline__ Set find_seq(const BatchArgs& b, int x_run, int row, int lane, const AttnPlan& p, int* run) {
+// How the call's tiles are cut: runs of `run` tiles, each set in runs of its own (`apart`) or not.
+struct Cut {
+  int run;
+  bool apart;
+};
+// The sequence that run x begins in (x < 0: the one that row `row` belongs to).
+__device__ __forceinline__ Set find_seq(const BatchArgs& b, int x, int row, int lane, const AttnPlan& p, Cut* cut) {
   const int B = b.n_seqs;
   const Seq s0 = lane_seq(b, 0, lane);
-  const int n0 = tiles_of(s0), upto0 = lane_prefix(n0, lane, B);
+  const int n0 = tiles_of(s0);
+  int upto0 = lane_prefix(n0, lane, B);
   int all = __builtin_amdgcn_readlane(upto0, min(B, 64) - 1);
   for (int i = 64; i < B; i += 64) {
     const int t = lane_prefix(tiles_of(lane_seq(b, i, lane)), lane, B - i);
     all += __builtin_amdgcn_readlane(t, min(B - i, 64) - 1);
   }
-  *run = run_tiles(p, all);
-  const int x = x_run * *run;
+  *cut = Cut{run_tiles(p, all), false};
+  if (B <= 64) {  // the sequences' runs counted, once or twice
+    int run = cut->run;
+    int runs = ceil_div(n0, run), upto = lane_prefix(runs, lane, B);
+    bool fits = __builtin_amdgcn_readlane(upto, B - 1) <= p.items;
+    if (!fits) {
+      run = run_tiles_apart(p, all, B);
+      fits = run > 0;
+      if (fits) {
+        runs = ceil_div(n0, run);
+        upto = lane_prefix(runs, lane, B);
+      }
+    }
+    if (fits) {
+      *cut = Cut{run, true};
+      const bool mine = x >= 0 ? upto - runs <= x && x < upto : row >= s0.row && row < s0.row + s0.tokens;
+      const unsigned long long at = __ballot(mine);
+      if (!at) return Set{Seq{0, 0, 0}, -1, 0, 0, 0};
+      const int l = __ffsll(at) - 1;
+      return Set{of_lane(s0, l), l, 0, __builtin_amdgcn_readlane(upto - runs, l) * run,
+                 __builtin_amdgcn_readlane(n0, l)};
+    }
+  }
+  const int tile = x * cut->run;
   int before = 0;
   for (int i = 0; i < B; i += 64) {
     const Seq s = i == 0 ? s0 : lane_seq(b, i, lane);
     const int n = i == 0 ? n0 : tiles_of(s);
     const int upto = i == 0 ? upto0 : before + lane_prefix(n, lane, B - i);
-    const bool mine = x_run >= 0 ? upto - n <= x && x < upto : row >= s.row && row < s.row + s.tokens;
+    const bool mine = x >= 0 ? upto - n <= tile && tile < upto : row >= s.row && row < s.row + s.tokens;
     const unsigned long long at = __ballot(mine);
     if (at) {
       const int l = __ffsll(at) - 1;
@@ -142,30 +170,25 @@ __device__ __forceinline__ Set seq_set(const BatchArgs& b, int i) {
   const Seq q = seq_of(b, b.q_start[i], b.q_start[i + 1], b.ctx_len[i]);
   return Set{q, q.tokens ? i : -1, 0, 0, tiles_of(q)};
 }
-// A token's set for listed pages, each of `tiles` tiles.
-__device__ __forceinline__ Set listed_set(const AttnArgs& a, int row, int tiles, int lane) {
+// A token's set for listed pages: its list begins at tile `first`.
+__device__ __forceinline__ Set listed_set(const AttnArgs& a, int row, int first, int lane) {
   const RowOf r = seq_of_row(a.b, row, lane);
-  return Set{r.seq, r.b, r.token, row * tiles, tiles};
+  return Set{r.seq, r.b, r.token, first, a.n_sel << (a.c.shift - TILE_SHIFT)};
 }
-// The set that holds tile x_run * run, or (x_run < 0) row `row`.
+// The set that run x begins in, or (x < 0) row `row`'s.
 template <bool SEL>
-__device__ __forceinline__ Set find_set(const AttnArgs& a, int x_run, int row, int lane, int* run) {
-  if (!SEL) return find_seq(a.b, x_run, row, lane, a.plan, run);
-  const int each = a.n_sel << (a.c.shift - TILE_SHIFT);
-  *run = run_tiles(a.plan, a.b.n_tokens * each);
-  if (x_run >= 0) row = x_run * *run / each;
-  if (row >= a.b.n_tokens) return Set{Seq{0, 0, 0}, -1, 0, a.b.n_tokens * each, 0};
-  return listed_set(a, row, each, lane);
+__device__ __forceinline__ Set find_set(const AttnArgs& a, int x, int row, int lane, Cut* cut) {
+  if (!SEL) return find_seq(a.b, x, row, lane, a.plan, cut);
+  const int tiles = a.n_sel << (a.c.shift - TILE_SHIFT);
+  *cut = Cut{run_tiles_listed(a.plan, tiles, a.b.n_tokens), true};
+  const int runs = ceil_div(tiles, cut->run);
+  if (x >= 0) row = x / runs;
+  if (row >= a.b.n_tokens) return Set{Seq{0, 0, 0}, -1, 0, 0, 0};
+  return listed_set(a, row, row * runs * cut->run, lane);
 }
-// The set behind this one (tiles 0: none).
-template <bool SEL>
-__device__ __forceinline__ Set next_set(const AttnArgs& a, const Set& s, int lane) {
+// The sequence with new tokens behind this one, its tiles next (tiles 0: none).
+__device__ __forceinline__ Set next_seq(const AttnArgs& a, const Set& s) {
   const int first = s.first + s.tiles;
-  if (SEL) {
-    const int row = first / s.tiles;
-    if (row >= a.b.n_tokens) return Set{Seq{0, 0, 0}, -1, 0, first, 0};
-    return listed_set(a, row, s.tiles, lane);
-  }
   for (int b = s.b + 1; b < a.b.n_seqs; ++b) {
     const Seq q = seq_of(a.b, a.b.q_start[b], a.b.q_start[b + 1], a.b.ctx_len[b]);
     if (q.tokens) return Set{q, b, 0, first, tiles_of(q)};
@@ -508,25 +531,23 @@ __global__ __launch_bounds__(64 * attn_waves(D, MT)) void attn_part(AttnArgs a) 
   const int u = turn / RB * XCDS + blockIdx.x % XCDS;
   const int h = u % a.c.kv_heads, item = u / a.c.kv_heads;
   if (item >= a.plan.items) return;
-  int run;
+  Cut cut;
   Set set;
   if (a.plan.whole) {
-    set = SEL ? listed_set(a, item, a.n_sel << (a.c.shift - TILE_SHIFT), lane) : seq_set(a.b, item);
-    run = set.tiles;
+    set = SEL ? listed_set(a, item, 0, lane) : seq_set(a.b, item);
+    cut = Cut{set.tiles, true};
   } else {
-    set = find_set<SEL>(a, item, 0, lane, &run);
+    set = find_set<SEL>(a, item, 0, lane, &cut);
   }
-  const int begin = a.plan.whole ? set.first : item * run;
+  const int begin = a.plan.whole ? 0 : item * cut.run;
   const size_t slots = (size_t)a.c.kv_heads * RB * a.plan.items * 2;
   const size_t slot = ((size_t)h * RB + rb) * a.plan.items * 2;
-  while (set.tiles > 0 && set.first < begin + run) {
-    if (set.b >= 0) {
-      const int lo = max(begin - set.first, 0), hi = min(begin + run - set.first, set.tiles);
-      const Out out{a, lo == 0 && hi == set.tiles, slot + part_slot(item, run, set.first), slots};
-      attn_run<D, MT, SEL, ONCE>(a, set, h, rb, lo, hi, out, lds);
-    }
-    if (set.first + set.tiles >= begin + run) break;
-    set = next_set<SEL>(a, set, lane);
+  while (set.b >= 0) {
+    const int lo = max(begin - set.first, 0), hi = min(begin + cut.run - set.first, set.tiles);
+    const Out out{a, lo == 0 && hi == set.tiles, slot + part_slot(item, cut.run, set.first), slots};
+    attn_run<D, MT, SEL, ONCE>(a, set, h, rb, lo, hi, out, lds);
+    if (SEL || cut.apart || set.first + set.tiles >= begin + cut.run) break;
+    set = next_seq(a, set);
     __syncthreads();  // the LDS of the set before is free
   }
 }
@@ -539,10 +560,10 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
   const int GROUPS = blockDim.x / LANES;
   const int l = threadIdx.x % LANES, grp = threadIdx.x / LANES, lane = threadIdx.x & 63;
   const int hq = blockIdx.x % a.heads, row = blockIdx.x / a.heads;
-  int run;
-  const Set set = find_set<SEL>(a, -1, row, lane, &run);
+  Cut cut;
+  const Set set = find_set<SEL>(a, -1, row, lane, &cut);
   if (set.b < 0) return;
-  const int n = run_parts(set.first, set.tiles, run);
+  const int run = cut.run, n = run_parts(set.first, set.tiles, run);
   if (n == 1) return;  // the row is out already
   const int h = hq / a.group, g0 = hq % a.group;
   const int r = SEL ? g0 : (row - set.seq.row) * a.group + g0;  // of the set's rows

@@ -177,29 +177,39 @@ AttnPlan attn_plan(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel)
   const int row_tiles = ceil_div(rows, 16 * p.q_tiles);
   p.row_blocks = ceil_div(row_tiles, wide ? 4 : 8);
   p.row_waves = ceil_div(row_tiles, p.row_blocks);
-  const int most_waves = attn_waves(c.head_dim, p.q_tiles);
   const bool alone = wide && p.row_waves > 1;  // row waves fill a work-group
+  // waves of a work-group: 8, more where many row waves of D = 64 leave room, 4 of two wide row tiles
+  const int room = attn_waves(c.head_dim, p.q_tiles);
+  const int waves = room > 8 && p.row_waves <= 4 ? 8 : room;
+  const int most_groups = alone ? 1 : waves / p.row_waves;
 
   const int tiles = n_sel ? n_sel << (c.shift - TILE_SHIFT) : ceil_div(b.max_ctx, TILE);
   const int units = c.kv_heads * p.row_blocks;
   const long long sets = n_sel ? b.n_tokens : b.n_seqs;
   const long long full = sets * units;  // work-groups of whole sets
-  p.whole = full < CUS              ? tiles <= (!wide ? 24 : rows > 16 ? 6 : 12)
+  p.whole = full < CUS              ? tiles <= (wide ? (rows > 16 ? 6 : 12) : 3 * most_groups)
             : n_sel                 ? 1  // lists are alike
             : alone                 ? tiles <= 32
             : full < 2 * CUS        ? tiles <= 64
                                     : tiles <= 128;
   const bool few = p.whole ? full >= 2 * CUS && tiles <= 16 : !n_sel && tiles <= 64;
-  const int waves = few || most_waves == 4 ? 4 : 8;
-  p.groups = alone || p.row_waves > waves ? 1 : waves / p.row_waves;
-  if (p.groups > tiles) p.groups = tiles > 0 ? tiles : 1;
+  p.groups = few && p.row_waves <= 4 && most_groups > 4 / p.row_waves ? 4 / p.row_waves : most_groups;
+  if (p.groups > tiles) p.groups = tiles;
+  if (p.groups < 1) p.groups = 1;
 
-  p.least = p.groups;
-  const long long most = (sets * (tiles > 0 ? tiles : 1) + p.least - 1) / p.least;
-  const int fill = most_waves == 4 ? CUS : alone ? CUS * (8 / p.row_waves) : CUS * (8 / waves);
+  // a part of so many rows is written and read again: a run has a sixteenth as many tiles at least
+  const int part_rows = rows < attn_rows(p) ? rows : attn_rows(p);
+  p.least = p.groups > part_rows / 16 ? p.groups : part_rows / 16;
+  const int held = (room < 8 ? room : 8) / (p.row_waves * p.groups);  // work-groups of a CU
+  const int fill = CUS * (held > 1 ? held : 1);
+  const long long runs = ceil_div(tiles > 0 ? tiles : 1, p.least);  // of a set at most
   long long items = fill / units;
-  if (n_sel) items = items > sets ? items / sets * sets : sets;  // lists cut alike
-  if (items > most) items = most;
+  if (n_sel) {
+    items /= sets;
+    items = (items > runs ? runs : items > 1 ? items : 1) * sets;
+  } else if (items > runs * sets) {
+    items = runs * sets;
+  }
   p.items = p.whole ? (int)sets : items > 1 ? (int)items : 1;
   return p;
 }

@@ -81,9 +81,11 @@ constexpr int TILE_SHIFT = 5;
 constexpr int attn_waves(int D, int q_tiles) { return D == 64 ? 16 : D == 256 && q_tiles > 1 ? 4 : 8; }
 
 // How a call is cut.  Its sets of rows (a sequence's window; one token for listed pages) have their tiles one set
-// behind the other, and the work-groups of a kv head and row block take equal runs of them, whatever set they belong
-// to: as many work-groups as the chip holds at once, none with more to do than another, however unlike the lengths
-// are and however far below the bounds.  The host fixes the number of work-groups, the device the run's length.
+// behind the other, and the work-groups of a kv head and row block take equal runs of them: as many work-groups as
+// the chip holds at once, none with much more to do than another, however unlike the lengths are and however far
+// below the bounds.  The host fixes the number of work-groups, the device the run's length.  Where the work-groups
+// suffice, every set begins a run of its own (a second set costs a work-group the wait for its first loads again);
+// else a run goes on from one set to the next.
 struct AttnPlan {
   int q_tiles;     // 16-row tiles a wave holds
   int row_waves;   // waves of a work-group over the rows
@@ -97,6 +99,19 @@ HCR_HD int attn_rows(const AttnPlan& p) { return p.row_waves * p.q_tiles * 16; }
 // Tiles of one run, from those of all sets (every set has one at least: a set without positions writes its zeros).
 HCR_HD int run_tiles(const AttnPlan& p, int tiles_of_all) {
   const int even = ceil_div(tiles_of_all, p.items);
+  return even > p.least ? even : p.least;
+}
+// The same with each of `sets` sets beginning a run: at most so many runs more; 0 where that makes them longer by
+// more than a sixteenth.
+HCR_HD int run_tiles_apart(const AttnPlan& p, int tiles_of_all, int sets) {
+  if (sets >= p.items) return 0;
+  const int even = ceil_div(tiles_of_all, p.items - sets);
+  const int run = even > p.least ? even : p.least;
+  return 16ll * run <= 17ll * run_tiles(p, tiles_of_all) ? run : 0;
+}
+// Listed pages: every token's list in as many runs.
+HCR_HD int run_tiles_listed(const AttnPlan& p, int list_tiles, int n_tokens) {
+  const int even = ceil_div(list_tiles, p.items / n_tokens);
   return even > p.least ? even : p.least;
 }
 // The runs that a set's tiles [first, first + tiles) lie in: a row's parts, to be joined where there are several.

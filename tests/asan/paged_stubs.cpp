@@ -105,19 +105,29 @@ static const char* check_plans() {
                       if (x < 1) x = 1;
                       all += x;
                     }
-                    const int run = run_tiles(p, all);
+                    int run = run_tiles(p, all), runs = 0;
                     CHECK(run >= 1 && (long long)run * p.items >= all);
+                    for (int x : t) runs += ceil_div(x, run);
+                    bool apart = sets <= 64 && runs <= p.items;
+                    if (n_sel) {
+                      CHECK(p.items % sets == 0);
+                      run = run_tiles_listed(p, most, sets);
+                      apart = true;
+                    } else if (sets <= 64 && !apart && run_tiles_apart(p, all, sets) > 0) {
+                      run = run_tiles_apart(p, all, sets);
+                      apart = true;
+                    }
                     std::vector<char> used(2 * p.items);
                     int first = 0;
                     for (int x : t) {  // every part of every set has a place of its own
                       const int n = run_parts(first, x, run);
-                      CHECK(n >= 1 && (n == 1 || attn_joins(p)));
-                      for (int k = 0; k < n && n > 1; ++k) {
+                      CHECK(n >= 1 && (n == 1 || attn_joins(p)) && (!apart || n == ceil_div(x, run)));
+                      for (int k = 0; k < n && (n > 1 || apart); ++k) {
                         const int slot = part_slot(first / run + k, run, first);
                         CHECK(slot >= 0 && slot < 2 * p.items && !used[slot]);
                         used[slot] = 1;
                       }
-                      first += x;
+                      first += apart ? n * run : x;
                     }
                   }
                 }
