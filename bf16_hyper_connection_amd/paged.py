@@ -22,7 +22,7 @@ HCR_ROPE_HALVES, HCR_ROPE_PAIRS = 0, 1
 _TYPES = {torch.float32: HCR_F32, torch.bfloat16: HCR_BF16}
 
 _vp, _ip, _sz, _ll, _fl, _db = (ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong, ctypes.c_float,
-                                       ctypes.c_double)
+                                     ctypes.c_double)
 
 
 class hcr_batch(ctypes.Structure):
@@ -77,6 +77,7 @@ class Batch:
     device tensors that the kernels read when they run (a captured graph reads what they hold at its replay);
     ``max_tokens`` and ``max_ctx`` are host bounds of the new tokens and of the length of any sequence.  Rows
     of q, k, v and outputs are numbered by ``q_start``; sequence b's last new token sits at ctx_len[b] - 1.
+    Tensors and bounds are fixed (their contents are not): for others make another batch.
     """
 
     def __init__(self, q_start, ctx_len, block_table, max_tokens, max_ctx):
@@ -94,6 +95,11 @@ class Batch:
         self.device, self.n_seqs = ctx_len.device, n
         self.max_tokens, self.max_ctx = int(max_tokens), int(max_ctx)
         self._by_rows = {}
+
+    def __setattr__(self, name, value):
+        if "_by_rows" in self.__dict__:
+            raise AttributeError(f"{name}: a batch's tensors and bounds are fixed")
+        super().__setattr__(name, value)
 
     def _of(self, n_tokens):
         """The C struct for calls of n_tokens rows (kept: a decode loop calls with the same number again)."""
@@ -186,7 +192,7 @@ class PagedCache:
         by_token, by_head, by_value = x.stride()
         if by_value != 1:
             raise ValueError(f"{name}: the values of a head side by side")
-        return hcr_rows(x.data_ptr(), by_token, by_head)
+        return hcr_rows(x.data_ptr(), by_token if shape[0] > 1 else 0, by_head if shape[1] > 1 else 0)
 
     def append(self, batch, q, k, v, q_norm=None, k_norm=None, eps=1e-6, rope=None, interleaved=False, q_out=None,
                stream=None):
