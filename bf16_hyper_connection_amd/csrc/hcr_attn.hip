@@ -27,6 +27,8 @@
 // of which the first loads' way, the parts' (9 MB written and read) and the second launch take about 15.
 
 #include <float.h>
+#include <limits.h>
+#include <math.h>
 #include <hip/hip_runtime.h>
 
 #include "hcr_paged_device.h"
@@ -186,12 +188,18 @@ __device__ __forceinline__ Set find_set(const AttnArgs& a, int x, int row, int l
   if (row >= a.b.n_tokens) return Set{Seq{0, 0, 0}, -1, 0, 0, 0};
   return listed_set(a, row, row * runs * cut->run, lane);
 }
-// The sequence with new tokens behind this one, its tiles next (tiles 0: none).
-__device__ __forceinline__ Set next_seq(const AttnArgs& a, const Set& s) {
+// The sequence with new tokens behind this one, its tiles next (tiles 0: none); 64 looked at together, since a padded
+// batch may hold many without.
+__device__ __forceinline__ Set next_seq(const AttnArgs& a, const Set& s, int lane) {
   const int first = s.first + s.tiles;
-  for (int b = s.b + 1; b < a.b.n_seqs; ++b) {
-    const Seq q = seq_of(a.b, a.b.q_start[b], a.b.q_start[b + 1], a.b.ctx_len[b]);
-    if (q.tokens) return Set{q, b, 0, first, tiles_of(q)};
+  for (int b = s.b + 1; b < a.b.n_seqs; b += 64) {
+    const Seq q = lane_seq(a.b, b, lane);
+    const unsigned long long at = __ballot(q.tokens > 0);
+    if (at) {
+      const int l = __ffsll(at) - 1;
+      const Seq found = of_lane(q, l);
+      return Set{found, b + l, 0, first, tiles_of(found)};
+    }
   }
   return Set{Seq{0, 0, 0}, -1, 0, first, 0};
 }
@@ -268,6 +276,42 @@ __device__ __forceinline__ uint4 visible8(const uint4& v, int p, int len) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) w[e] = p + 2 * e + 1 < len ? w[e] : p + 2 * e < len ? w[e] & 0xFFFFu : 0u;
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Whether one of the wave's values is infinite or NaN.
+template <int N>
+__device__ __forceinline__ bool any_odd(const uint4 (&v)[N]) {
+  typedef __attribute__((ext_vector_type(2))) uint16_t u16x2;
+  u16x2 top = {0, 0};
+#pragma unroll
+  for (int d = 0; d < N; ++d) {
+    const uint32_t w[4] = {v[d].x, v[d].y, v[d].z, v[d].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, w[e] & 0x7FFF7FFFu));
+  }
+  return __any(top[0] >= 0x7F80 || top[1] >= 0x7F80);
+}
+
+// The values from position `from` on that are no numbers become zeros; the first one's position.  p: the lane's first.
+template <int N>
+__device__ __forceinline__ int drop_odd(uint4 (&v)[N], int p, int from) {
+  int first = INT_MAX;
+#pragma unroll
+  for (int d = 0; d < N; ++d) {
+    uint32_t w[4] = {v[d].x, v[d].y, v[d].z, v[d].w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t half = e & 1 ? 0x7F800000u : 0x7F80u;
+      if ((w[e >> 1] & half) == half && p + e >= from) {
+        w[e >> 1] &= e & 1 ? 0xFFFFu : 0xFFFF0000u;
+        first = min(first, p + e);
+      }
+    }
+    v[d] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  for (int o = 32; o; o >>= 1) first = min(first, __shfl_xor(first, o));
+  return __builtin_amdgcn_readfirstlane(first);
 }
 
 // The lane's 8 products s of one row as probabilities against the row's running maximum; its sum and values follow
@@ -435,6 +479,10 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
 #pragma unroll
       for (int d = 0; d < DT; ++d) vf[d] = visible8(vf[d], now + 8 * lg, rows.len_max);
     }
+    // A value that is no number and that only later tokens see: zero times it would reach the earlier ones' rows.  It
+    // leaves the product, and the rows that see it become NaN.
+    int odd = INT_MAX;
+    if (!SEL && !whole && rows.len_min < rows.len_max && any_odd(vf)) odd = drop_odd(vf, now + 8 * lg, rows.len_min);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       float p[8];
@@ -449,6 +497,11 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
         const uint4 pr = split_rest(p, ph, pl);
 #pragma unroll
         for (int d = 0; d < DT; ++d) acc[m][d] = mfma(vf[d], pr, acc[m][d]);
+      }
+      if (!SEL && odd < INT_MAX) {
+        const float none = len[m] > odd ? NAN : 0.f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) acc[m][d] += f32x4{none, none, none, none};
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -547,7 +600,7 @@ __global__ __launch_bounds__(64 * attn_waves(D, MT)) void attn_part(AttnArgs a) 
     const Out out{a, lo == 0 && hi == set.tiles, slot + part_slot(item, cut.run, set.first), slots};
     attn_run<D, MT, SEL, ONCE>(a, set, h, rb, lo, hi, out, lds);
     if (SEL || cut.apart || set.first + set.tiles >= begin + cut.run) break;
-    set = next_seq(a, set);
+    set = next_seq(a, set, lane);
     __syncthreads();  // the LDS of the set before is free
   }
 }

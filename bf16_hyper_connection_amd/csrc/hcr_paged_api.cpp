@@ -1,6 +1,7 @@
 // C ABI of the paged cache: argument checks, the handle and the plan of an attention call.  Every check runs on
 // the host before any HIP call.
 
+#include <math.h>
 #include <stdint.h>
 #include <stdlib.h>
 
@@ -86,8 +87,9 @@ int check_arrays(const BatchArgs& b) {
 int check_rows(const hcr_rows* r, int type, int n_tokens, int heads, int head_dim, Span* s) {
   if (!r || !r->data) return HCR_EINVAL;
   const long long unit = type == HCR_F32 ? 4 : 8, size = type == HCR_F32 ? 4 : 2;
-  const long long most = 1ll << 40;
-  if (r->token_stride < 0 || r->head_stride < 0 || r->token_stride > most || r->head_stride > most) return HCR_EINVAL;
+  const long long most = 1ll << 48;  // elements on the way to the last row
+  if (r->token_stride < 0 || r->head_stride < 0 || r->token_stride > most / n_tokens || r->head_stride > most / heads)
+    return HCR_EINVAL;
   if (!aligned(r->data, 16) || r->token_stride % unit || r->head_stride % unit) return HCR_EALIGN;
   const long long last = (n_tokens - 1) * r->token_stride + (heads - 1) * r->head_stride + head_dim;
   *s = span(r->data, (size_t)last * size);
@@ -139,7 +141,9 @@ int attn(hcr_cache_t h, const hcr_batch* batch, int heads, double scale, const v
   a.group = heads / c.kv_heads;
   a.out_type = out_type;
   const double log2e = scale * 1.4426950408889634;
+  // both parts of one sign, neither zero: a product of -inf stays -inf and weighs nothing
   a.scale_hi = (float)log2e;
+  if (fabs(a.scale_hi) >= fabs(log2e)) a.scale_hi = nextafterf(a.scale_hi, 0.f);
   a.scale_lo = (float)(log2e - a.scale_hi);
   a.out = out;
   a.part = static_cast<float*>(scratch);

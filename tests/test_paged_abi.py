@@ -168,6 +168,8 @@ def append(lib, h, b, heads=32, type_=0, q=(Q, 6144, 128), k=(Q + 16384, 6144, 1
 @pytest.mark.parametrize("kw,rc", [
     (dict(heads=4), hcr.HCR_EINVAL), (dict(type_=3), hcr.HCR_EINVAL), (dict(q=None), hcr.HCR_EINVAL),
     (dict(k=(None, 6144, 128)), hcr.HCR_EINVAL), (dict(v=(Q, -6144, 128)), hcr.HCR_EINVAL),
+    (dict(q=(Q, 1 << 47, 128)), hcr.HCR_EINVAL), (dict(k=(Q, 6144, 1 << 50)), hcr.HCR_EINVAL),
+    (dict(v=(Q, (1 << 63) - 16, 128)), hcr.HCR_EINVAL), (dict(q=(Q, 6144, 1 << 46)), hcr.HCR_EINVAL),
     (dict(eps=-1.0), hcr.HCR_EINVAL), (dict(eps=float("nan")), hcr.HCR_EINVAL), (dict(eps=float("inf")), hcr.HCR_EINVAL),
     (dict(rope=None), hcr.HCR_EINVAL), (dict(dim=136), hcr.HCR_EINVAL), (dict(dim=24), hcr.HCR_EINVAL),
     (dict(dim=-8), hcr.HCR_EINVAL), (dict(rows=4999), hcr.HCR_EINVAL), (dict(style=2), hcr.HCR_EINVAL),

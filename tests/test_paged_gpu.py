@@ -124,6 +124,63 @@ def test_lengths_and_rows_beyond_the_bounds_are_cut():
     assert torch.all(again == 3.0)
 
 
+@pytest.mark.parametrize("head_dim,kv,group,T", [(128, 2, 4, 5), (256, 1, 6, 7), (64, 1, 8, 20), (128, 1, 12, 3),
+                                                 (256, 2, 10, 3), (256, 1, 16, 9)])
+@pytest.mark.parametrize("odd", [np.inf, -np.inf, np.nan])
+def test_attend_rows_do_not_depend_on_later_tokens(head_dim, kv, group, T, odd):
+    """A window's last tokens have keys and values that are no numbers: the rows before them are as ever, their own
+    are no numbers either."""
+    windows = [(T, 300), (T, 64), (T, T), (T, 5003)]
+    s = pu.scene(15, kv, head_dim, 64, windows)
+    heads = kv * group
+    q = pu.queries(15, s.n_tokens, heads, head_dim)
+    keys, values = pu.decoded(s)
+    qf = oracle.bf16_bits_to_f64(q)
+    want = oracle.paged.attend(s.batch, keys, values, qf, 0.1)
+    tol = pu.rows_tolerance(qf, float(np.sqrt(np.nansum(keys ** 2, axis=-1)).max()), 0.1, 5003, False)
+    bits = pu.bf16([odd])[0]
+    for b, (_, ctx) in enumerate(windows):
+        for at, store in ((ctx - 2, s.v_bits), (ctx - 1, s.k_bits)):
+            page = s.table[b, at // 64]
+            if store is s.v_bits:
+                store[page, :, at % 64 // 8, ::3, at % 8] = bits
+            else:
+                store[page, :, :, at % 64, 0] = bits
+    out = pu.dev_cache(s).attend(pu.dev_batch(s), pu.dev_bits(q), scale=0.1)
+    early = {n: w for n, w in want.items() if n % T < T - 2}
+    pu.check_rows(out, early, tol, "early")
+    finite = torch.isfinite(out).all(-1)
+    late = torch.arange(s.n_tokens, device="cuda") % T >= T - 2
+    assert finite[~late].all() and not finite[late].any()
+
+
+@pytest.mark.parametrize("scale", [0.1, 0.125, 0.3, -0.1, -0.7])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_a_product_of_minus_infinity_weighs_nothing(scale, out_dtype):
+    s = pu.scene(16, 1, 64, 32, [(2, 70), (1, 33)])
+    q = pu.queries(16, s.n_tokens, 4, 64)
+    q[..., 0] = pu.bf16([2.0])[0]
+    low = np.float32(-np.inf if scale > 0 else np.inf)
+    for b, at in ((0, 5), (0, 66), (1, 0)):
+        s.k_bits[s.table[b, at // 32], 0, 0, at % 32, 0] = pu.bf16([low])[0]
+    keys, values = pu.decoded(s)
+    keys = np.where(np.isinf(keys), np.sign(low) * 1e30, keys)  # far enough
+    qf = oracle.bf16_bits_to_f64(q)
+    want = oracle.paged.attend(s.batch, keys, values, qf, scale)
+    out = pu.dev_cache(s).attend(pu.dev_batch(s), pu.dev_bits(q), scale=scale, out_dtype=out_dtype)
+    pu.check_rows(out, want, pu.rows_tolerance(qf, 20.0, scale, 70, out_dtype == torch.bfloat16), "infinite")
+
+
+def test_attend_of_a_padded_batch():
+    """A few sequences far apart among many without new tokens, some of those with a length."""
+    windows = [(0, 0 if i % 3 else 90) for i in range(260)]
+    for i, w in ((3, (1, 1500)), (70, (2, 40)), (71, (1, 900)), (190, (2, 1300)), (259, (1, 33))):
+        windows[i] = w
+    s = pu.scene(17, 1, 128, 64, windows)
+    out, want, tol = _attend(s, 4)
+    pu.check_rows(out, want, tol, "padded")
+
+
 def test_attend_with_loose_bounds():
     """Bounds above what the sequences have (as a captured graph keeps them), rows behind the last sequence's."""
     s = pu.scene(5, 2, 128, 64, [(2, 100), (1, 700)], table_extra=40)
@@ -555,3 +612,25 @@ def test_two_streams_with_their_own_scratch():
     torch.cuda.synchronize()
     for o, w in zip(outs, want):
         assert torch.equal(o, w)
+
+
+def test_append_of_one_token_takes_any_stride():
+    """A single row's token stride is never used (torch leaves it as it comes), nor a single head's."""
+    s = pu.scene(45, 1, 64, 32, [(1, 20)], visible=[19])
+    y = torch.randn(6 * 64 + 3, device="cuda")
+    odd = [y.as_strided((1, n, 64), (387, 64 if n > 1 else 5, 1), at * 64) for n, at in ((4, 0), (1, 4), (1, 5))]
+    even = [y[at * 64:(at + n) * 64].clone().view(1, n, 64) for n, at in ((4, 0), (1, 4), (1, 5))]
+    assert odd[0].stride(0) == 387 and odd[1].stride(1) == 5
+    caches = [pu.dev_cache(s) for _ in range(2)]
+    got = [c.append(pu.dev_batch(s), *p) for c, p in zip(caches, (odd, even))]
+    assert torch.equal(got[0], got[1])
+    for a, b in ((caches[0].k_pages, caches[1].k_pages), (caches[0].v_pages, caches[1].v_pages)):
+        assert np.array_equal(pu.host_bits(a), pu.host_bits(b))
+
+
+def test_a_batch_keeps_its_tensors_and_bounds():
+    s = pu.scene(46, 1, 64, 32, [(1, 20)])
+    batch = pu.dev_batch(s)
+    for name, value in (("max_ctx", 30), ("max_tokens", 2), ("ctx_len", batch.ctx_len.clone()), ("n_seqs", 0)):
+        with pytest.raises(AttributeError):
+            setattr(batch, name, value)
