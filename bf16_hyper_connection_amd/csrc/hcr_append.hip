@@ -237,7 +237,7 @@ __global__ __launch_bounds__(APPEND_THREADS) void append(AppendArgs a, int kv_gr
     const int h = g % a.c.kv_heads;
     g /= a.c.kv_heads;
     const int b = g / pages;
-    const Seq seq = seq_of(a.b, a.b.q_start[b], a.b.q_start[b + 1], a.b.ctx_len[b]);
+    const Seq seq = wave_seq(a.b, b);
     const int pg = (max(seq.first, 0) >> a.c.shift) + g % pages;
     if (seq.tokens > 0) append_page<D, F32>(a, seq, b, pg, h, key);
     return;
@@ -247,7 +247,7 @@ __global__ __launch_bounds__(APPEND_THREADS) void append(AppendArgs a, int kv_gr
   g /= passes;
   const int parts = ceil_div(a.b.max_tokens, EACH);
   const int b = g / parts;
-  const Seq seq = seq_of(a.b, a.b.q_start[b], a.b.q_start[b + 1], a.b.ctx_len[b]);
+  const Seq seq = wave_seq(a.b, b);
   const int l = threadIdx.x % LANES, head = pass * PER + threadIdx.x / LANES;
   const int hh = min(head, a.heads - 1);
   const int t0 = g % parts * EACH;

@@ -169,25 +169,20 @@ __device__ __forceinline__ Set find_seq(const BatchArgs& b, int x, int row, int 
 }
 // A sequence's set where no other is counted.
 __device__ __forceinline__ Set seq_set(const BatchArgs& b, int i) {
-  const Seq q = seq_of(b, b.q_start[i], b.q_start[i + 1], b.ctx_len[i]);
+  const Seq q = wave_seq(b, i);
   return Set{q, q.tokens ? i : -1, 0, 0, tiles_of(q)};
 }
-// A token's set for listed pages: its list begins at tile `first`.
-__device__ __forceinline__ Set listed_set(const AttnArgs& a, int row, int first, int lane) {
-  const RowOf r = seq_of_row(a.b, row, lane);
-  return Set{r.seq, r.b, r.token, first, a.n_sel << (a.c.shift - TILE_SHIFT)};
-}
-// The set that run x begins in, or (x < 0) row `row`'s.
-template <bool SEL>
-__device__ __forceinline__ Set find_set(const AttnArgs& a, int x, int row, int lane, Cut* cut) {
-  if (!SEL) return find_seq(a.b, x, row, lane, a.plan, cut);
-  const int tiles = a.n_sel << (a.c.shift - TILE_SHIFT);
-  *cut = Cut{run_tiles_listed(a.plan, tiles, a.b.n_tokens), true};
-  const int runs = ceil_div(tiles, cut->run);
-  if (x >= 0) row = x / runs;
-  if (row >= a.b.n_tokens) return Set{Seq{0, 0, 0}, -1, 0, 0, 0};
-  return listed_set(a, row, row * runs * cut->run, lane);
-}
+// Listed pages: every token's list in `runs` runs of `run` tiles, whole ones as one.
+struct Lists {
+  int tiles, run, runs;
+  __device__ __forceinline__ explicit Lists(const AttnArgs& a)
+      : tiles(a.n_sel << (a.c.shift - TILE_SHIFT)),
+        run(a.plan.whole ? tiles : run_tiles_listed(a.plan, tiles, a.b.n_tokens)), runs(ceil_div(tiles, run)) {}
+  __device__ __forceinline__ Set set(const AttnArgs& a, int row, int lane) const {
+    const RowOf r = seq_of_row(a.b, row, lane);
+    return Set{r.seq, r.b, r.token, row * runs * run, tiles};
+  }
+};
 // The sequence with new tokens behind this one, its tiles next (tiles 0: none); 64 looked at together, since a padded
 // batch may hold many without.
 __device__ __forceinline__ Set next_seq(const AttnArgs& a, const Set& s, int lane) {
@@ -217,8 +212,13 @@ struct Rows {
   }
 };
 
+// Entry idx of a row's list of pages (behind its end the last one, which no tile takes).
+__device__ __forceinline__ int listed(const AttnArgs& a, int row, int h, int idx) {
+  return a.sel[((size_t)row * a.c.kv_heads + h) * a.n_sel + min(idx, a.n_sel - 1)];
+}
+
 // The tiles of a set from `tile` to `hi`, every `step`-th, those without a visible position left out.  Lane l holds
-// entry `from` + l of the page list, as the page's number (-1: none) and its index in the sequence.
+// entry `from` + l of the page list, as the page's number (any: the table's) and its index in the sequence.
 template <int D, bool SEL>
 struct Tiles {
   const AttnArgs& a;
@@ -228,36 +228,35 @@ struct Tiles {
   int p0;               // of the tile found: its first position,
   const char *kp, *vp;  // its keys and values (the same for the whole wave)
   __device__ __forceinline__ Tiles(const AttnArgs& a_, const Set& set_, int h_, int len, int lane_, int lo, int hi_,
-                                   int skip, int step_)
+                                   int skip, int step_, int entry)
       : a(a_), set(set_), h(h_), len_max(len), lane(lane_), psh(a_.c.shift - TILE_SHIFT), hi(hi_), step(step_),
         tile(lo + skip), from(lo >> psh), number(-1), index(-1), p0(0), kp(nullptr), vp(nullptr) {
-    list();
+    list(entry);
   }
-  __device__ __forceinline__ void list() {
-    const int idx = from + lane;
+  // Raw entries, not looked at before find(): the query rows' loads go out behind these without a wait.  entry: of a
+  // list of pages, loaded before.
+  __device__ __forceinline__ void list(int entry) {
+    if (len_max <= 0) return;  // nothing to see; the table may have no columns
     const int* table = a.b.table + (size_t)set.b * a.b.table_stride;
-    number = -1;
-    index = idx;
     if (SEL) {
-      index = idx < a.n_sel ? a.sel[((size_t)(set.seq.row + set.token) * a.c.kv_heads + h) * a.n_sel + idx] : -1;
-      if (index >= 0 && len_max > 0 && index <= (len_max - 1) >> a.c.shift)
-        number = page_or_none(table[index], a.c.n_pages);
-      else
-        index = 0;  // not used
-    } else if (idx << a.c.shift < len_max) {
-      number = page_or_none(table[idx], a.c.n_pages);
+      const bool in = entry >= 0 && entry <= (len_max - 1) >> a.c.shift;
+      number = table[in ? entry : 0];
+      index = in ? entry : 1 << 30 >> a.c.shift;  // at positions that no row sees
+    } else {
+      number = table[min(from + lane, a.b.table_stride - 1)];
     }
   }
   __device__ __forceinline__ bool find() {
     for (; tile < hi; tile += step) {
       if ((tile >> psh) - from >= 64) {
         from = tile >> psh;
-        list();
+        list(SEL ? listed(a, set.seq.row + set.token, h, from + lane) : 0);
+        asm volatile("" : "+v"(number), "+v"(index));  // waited for here, not by every tile behind the branch
       }
       const int at = (tile >> psh) - from;
-      const int pn = __builtin_amdgcn_readlane(number, at);
+      const int pn = page_or_none(__builtin_amdgcn_readlane(number, at), a.c.n_pages);
       const int off = (tile << TILE_SHIFT) & ((1 << a.c.shift) - 1);
-      p0 = (__builtin_amdgcn_readlane(index, at) << a.c.shift) + off;
+      p0 = SEL ? (__builtin_amdgcn_readlane(index, at) << a.c.shift) + off : tile << TILE_SHIFT;
       if (pn < 0 || p0 >= len_max) continue;
       const size_t base = head_base(a.c, pn, h);
       kp = reinterpret_cast<const char*>(a.c.k + base + off * 8);
@@ -373,7 +372,7 @@ struct Out {
 // A set's tiles [lo, hi) (counted from its own first) in one work-group: its rows' part of the softmax.
 template <int D, int MT, bool SEL, bool ONCE>
 __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int h, int rb, int lo, int hi,
-                                         const Out& out, uint4* lds) {
+                                         int entry, const Out& out, uint4* lds) {
   constexpr int KS = D / 32, DT = D / 16;
   const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -385,7 +384,7 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
   // a wave behind the last row takes the last row again, and stores nothing
   const int r0 = rows.first + rt * 16 * MT;
   const bool idle = r0 >= rows.count;
-  Tiles<D, SEL> tiles(a, set, h, rows.len_max, lane, lo, hi, tg, TG);
+  Tiles<D, SEL> tiles(a, set, h, rows.len_max, lane, lo, hi, tg, TG, entry);
 
   // Keys of the next tile are loaded behind their last use in this one, values likewise, so that one of the two is
   // always on its way while the other is worked on; the first ones go out ahead of the query rows' way through LDS.
@@ -427,19 +426,14 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
   // row waves alone keep step, so that the first one's misses are the others' hits in L1 (36 rows of D = 256: 314
   // against 342 us; all of them find the same tiles)
   const bool together = TG == 1 && RT > 1;
-  bool more = tiles.find();
-  if (more && !idle) {
-    load_keys();
-    load_values();
-  }
-  if (tg == 0) {
+  auto store_rows = [&]() {
+    if (tg != 0) return;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
       for (int k = 0; k < KS; ++k) lds_q[(m * KS + k) * 64] = qf[m][k];
     }
-  }
-  lds_barrier();
+  };
   f32x4 acc[MT][DT];
   float mx[MT], sum[MT];
 #pragma unroll
@@ -449,6 +443,14 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
 #pragma unroll
     for (int d = 0; d < DT; ++d) acc[m][d] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
+
+  bool more = tiles.find();
+  store_rows();
+  if (more && !idle) {
+    load_keys();
+    load_values();
+  }
+  lds_barrier();
 
   while (more) {
     if (idle) {
@@ -586,19 +588,30 @@ __global__ __launch_bounds__(64 * attn_waves(D, MT)) void attn_part(AttnArgs a) 
   if (item >= a.plan.items) return;
   Cut cut;
   Set set;
-  if (a.plan.whole) {
-    set = SEL ? listed_set(a, item, 0, lane) : seq_set(a.b, item);
+  int entry = 0, begin = 0;
+  if (SEL) {
+    const Lists lists(a);
+    const int row = item / lists.runs;
+    if (row >= a.b.n_tokens) return;
+    begin = item * lists.run;
+    cut = Cut{lists.run, true};
+    // the list's load goes out beside the sequence's, one wait less (4 tokens, 64 pages
+    // of 64, D = 256: 28.7 against 29.7 us)
+    entry = listed(a, row, h, ((begin - row * lists.runs * lists.run) >> (a.c.shift - TILE_SHIFT)) + lane);
+    set = lists.set(a, row, lane);
+  } else if (a.plan.whole) {
+    set = seq_set(a.b, item);
     cut = Cut{set.tiles, true};
   } else {
-    set = find_set<SEL>(a, item, 0, lane, &cut);
+    set = find_seq(a.b, item, 0, lane, a.plan, &cut);
+    begin = item * cut.run;
   }
-  const int begin = a.plan.whole ? 0 : item * cut.run;
   const size_t slots = (size_t)a.c.kv_heads * RB * a.plan.items * 2;
   const size_t slot = ((size_t)h * RB + rb) * a.plan.items * 2;
   while (set.b >= 0) {
     const int lo = max(begin - set.first, 0), hi = min(begin + cut.run - set.first, set.tiles);
     const Out out{a, lo == 0 && hi == set.tiles, slot + part_slot(item, cut.run, set.first), slots};
-    attn_run<D, MT, SEL, ONCE>(a, set, h, rb, lo, hi, out, lds);
+    attn_run<D, MT, SEL, ONCE>(a, set, h, rb, lo, hi, entry, out, lds);
     if (SEL || cut.apart || set.first + set.tiles >= begin + cut.run) break;
     set = next_seq(a, set, lane);
     __syncthreads();  // the LDS of the set before is free
@@ -614,9 +627,9 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
   const int l = threadIdx.x % LANES, grp = threadIdx.x / LANES, lane = threadIdx.x & 63;
   const int hq = blockIdx.x % a.heads, row = blockIdx.x / a.heads;
   Cut cut;
-  const Set set = find_set<SEL>(a, -1, row, lane, &cut);
+  const Set set = SEL ? Lists(a).set(a, row, lane) : find_seq(a.b, -1, row, lane, a.plan, &cut);
   if (set.b < 0) return;
-  const int run = cut.run, n = run_parts(set.first, set.tiles, run);
+  const int run = SEL ? Lists(a).run : cut.run, n = run_parts(set.first, set.tiles, run);
   if (n == 1) return;  // the row is out already
   const int h = hq / a.group, g0 = hq % a.group;
   const int r = SEL ? g0 : (row - set.seq.row) * a.group + g0;  // of the set's rows

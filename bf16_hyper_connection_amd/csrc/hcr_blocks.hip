@@ -42,7 +42,7 @@ __global__ __launch_bounds__(64 * SCORE_WAVES) void block_scores(ScoreArgs a, in
 #pragma unroll
   for (int p = 0; p < TILES; ++p)
     number[p] = a.b.table[(size_t)b * a.b.table_stride + min(j0 + 16 * p + li, a.b.table_stride - 1)];
-  const Seq seq = seq_of(a.b, a.b.q_start[b], a.b.q_start[b + 1], a.b.ctx_len[b]);
+  const Seq seq = wave_seq(a.b, b);
   if (seq.tokens == 0) return;
   const int before = max(seq.first + seq.tokens - 1, 0) >> a.c.shift;  // pages that the last token scores
   if (j0 >= before) return;
