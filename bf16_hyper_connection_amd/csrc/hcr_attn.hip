@@ -19,12 +19,15 @@
 // chip holds at once (AttnPlan), so that unlike lengths and loose bounds cost nothing; a run goes from one sequence
 // on to the next.  The waves of a work-group take its tiles in turn and join in LDS; sequences that lie in several
 // runs are joined by a second launch; each join is (m, l, O) -> (max, sum of l 2^(m - max), sum of O 2^(m - max)),
-// in a fixed order.
+// in a fixed order.  Where the chip is full of sequences or they are short, a work-group takes a whole one instead and
+// nothing is left to join (there a long one among short ones, or a bound far above them, does cost: the plan's rule
+// keeps that to sequences of 4,096).
 //
 // Bound by the bytes of keys and values.  Measured on MI355X (graphs of calls, inputs rotated): one sequence of
-// 420,000 positions, 48 heads of 256 over 8, 2 tokens: 528 us, 6.5 TB/s (a 4 GiB device copy moves 4.8); 64 sequences
-// of 1,000 to 8,192, 32 heads of 128 over 8: 193 us, 6.3 TB/s.  36 rows of 4 sequences of up to 9,001: 51 us, 3.3 TB/s,
-// of which the first loads' way, the parts' (9 MB written and read) and the second launch take about 15.
+// 420,000 positions, 48 heads of 256 over 8, 2 tokens: 530 us, 6.5 TB/s (a 4 GiB device copy moves 4.8); 64 sequences
+// of 1,000 to 8,192, 32 heads of 128 over 8: 195 us, 6.2 TB/s.  36 rows of 4 sequences of up to 9,001: 51 us, 3.3 TB/s:
+// a work-group has 10 tiles behind 6 us of first loads, three row waves share each of them, so that a CU has 64 KB on
+// their way where it has 256 KB with one row wave, and the second launch takes 7.
 
 #include <float.h>
 #include <limits.h>

@@ -167,7 +167,12 @@ int attn(hcr_cache_t h, const hcr_batch* batch, int heads, double scale, const v
 //              bytes: a CU alone takes about 35 GB/s).  36 rows of D = 256: 700 63 against 74, 2,000 158 against
 //              153.  Beyond 4,096 the runs stay, although lengths as even as these would still gain 5 % (8,192: 184
 //              against 194): one long sequence among short ones would hold a single CU for the whole call
-//   waves      8 a work-group, one work-group a CU, for long sequences (D = 256, one sequence of 420,000: 568
+//   apart      every set begins a run of its own where runs get no more than a sixteenth longer by it (run_tiles_apart;
+//              a quarter was slower for a few long sequences), and a run is worth the part that it leaves, which is
+//              written and read again (least).  Together: 12 single tokens over up to 3,127 positions 19.0 against 22.9,
+//              37 windows of 224 rows of D = 256 over up to 249 24.4 against 34.6
+//   waves      16 for D = 64 with more than 64 rows (42 windows of 192 rows over up to 913 positions: 23 against 32
+//              with 8).  Else 8 a work-group, one work-group a CU, for long sequences (D = 256, one of 420,000: 568
 //              against 575 with 4); 4, two work-groups a CU, for runs where no sequence is longer than 2,048 (one of
 //              2,000, D = 256: 13.4 against 14.5) and for many sets of up to 512 (300: 14 against 17), since a short
 //              one is mostly the wait for its first loads

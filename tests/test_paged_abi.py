@@ -103,7 +103,8 @@ BAD_BATCHES = [
     (dict(n_seqs=-1), hcr.HCR_EINVAL), (dict(n_tokens=-1), hcr.HCR_EINVAL), (dict(max_tokens=-2), hcr.HCR_EINVAL),
     (dict(max_ctx=-1), hcr.HCR_EINVAL), (dict(table_stride=-1), hcr.HCR_EINVAL),
     (dict(max_ctx=6401), hcr.HCR_EINVAL),           # more positions than the table's 100 pages of 64
-    (dict(q_start=None), hcr.HCR_EINVAL), (dict(ctx_len=None), hcr.HCR_EINVAL), (dict(block_table=None), hcr.HCR_EINVAL),
+    (dict(q_start=None), hcr.HCR_EINVAL), (dict(ctx_len=None), hcr.HCR_EINVAL),
+    (dict(block_table=None), hcr.HCR_EINVAL),
     (dict(q_start=STARTS + 2), hcr.HCR_EALIGN), (dict(ctx_len=LENS + 1), hcr.HCR_EALIGN),
     (dict(block_table=TABLE + 3), hcr.HCR_EALIGN),
     (dict(n_tokens=1 << 30), hcr.HCR_EINVAL),       # more rows than 32 bits hold

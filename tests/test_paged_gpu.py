@@ -99,7 +99,8 @@ def test_attend_runs_over_many_short_sequences(head_dim, kv, group, T):
     pu.check_rows(out, want, tol, "runs")
 
 
-@pytest.mark.parametrize("head_dim,kv,group,most", [(128, 2, 2, 500), (64, 2, 1, 2000), (256, 2, 1, 300), (128, 2, 9, 400)])
+@pytest.mark.parametrize("head_dim,kv,group,most", [(128, 2, 2, 500), (64, 2, 1, 2000), (256, 2, 1, 300),
+                                                    (128, 2, 9, 400)])
 def test_attend_many_sequences(head_dim, kv, group, most):
     """A work-group a sequence, more of them than the chip holds at once."""
     g = gen.rng(100, head_dim)
