@@ -8,6 +8,15 @@ current stream of the cache's device or on ``stream`` (a raw hipStream_t).  Ther
 
 Outputs and scratch allocated here belong to torch's current stream: with another ``stream``, pass them in (or
 record them on that stream) so that torch does not reuse their memory before the kernels have run.
+
+A decode step (``y``: the projections' output, [tokens][heads + 2 kv_heads][head_dim])::
+
+    from bf16_hyper_connection_amd.paged import Batch, PagedCache
+    cache = PagedCache.allocate(n_pages=4096, kv_heads=8, head_dim=128, page=64)
+    batch = Batch(q_start, ctx_len, block_table, max_tokens=4, max_ctx=32768)   # int32 device tensors, host bounds
+    q = cache.append(batch, y[:, :32], y[:, 32:40], y[:, 40:], q_norm=wq, k_norm=wk, rope=angles)
+    out = cache.attend(batch, q)                                                # or, over the best 32 pages a token:
+    out = cache.attend_blocks(batch, q, cache.block_topk(batch, cache.block_scores(batch, q), 32))
 """
 
 import ctypes

@@ -4,6 +4,8 @@ and over listed pages, page scores, page selection, and a window's run of them t
 Cells that no visible position owns hold NaN, so a read behind a sequence shows.  Tolerances: see
 ``paged_util.rows_tolerance`` (attention); BF16 outputs half a step (2^-8 of the value) and FP32's share."""
 
+import textwrap
+
 import numpy as np
 import pytest
 import torch
@@ -635,3 +637,32 @@ def test_a_batch_keeps_its_tensors_and_bounds():
     for name, value in (("max_ctx", 30), ("max_tokens", 2), ("ctx_len", batch.ctx_len.clone()), ("n_seqs", 0)):
         with pytest.raises(AttributeError):
             setattr(batch, name, value)
+
+
+def test_the_decode_step_of_the_documentation():
+    """The binding's example as it stands, over a few sequences."""
+    code = textwrap.dedent(paged.__doc__.split("::\n\n")[1])
+    starts = torch.tensor([0, 1, 4, 8], dtype=torch.int32, device="cuda")
+    lengths = torch.tensor([1, 300, 32768], dtype=torch.int32, device="cuda")
+    table = torch.arange(3 * 512, dtype=torch.int32, device="cuda").view(3, 512)
+    angles = torch.randn(32768, 64, device="cuda")
+    names = dict(q_start=starts, ctx_len=lengths, block_table=table, y=torch.randn(8, 48, 128, device="cuda"),
+                 wq=torch.ones(128, device="cuda"), wk=torch.ones(128, device="cuda"), angles=angles)
+    allocate = paged.PagedCache.allocate
+
+    def zeroed(**kw):
+        cache = allocate(**kw)
+        for t in (cache.k_pages, cache.v_pages, cache.k_means):
+            t.zero_()
+        return cache
+    paged.PagedCache.allocate = zeroed
+    try:
+        exec(code, names)
+    finally:
+        paged.PagedCache.allocate = allocate
+    out = names["out"]
+    assert out.shape == (8, 32, 128) and torch.isfinite(out).all()
+    # the first token's only position: its value times p and 1 / p, p near 1.  Three roundings of the parts' sums, two
+    # of the reciprocal and one of the product, half a step (2^-24) each
+    value = names["y"][0, 40:].bfloat16().float().repeat_interleave(4, 0)
+    assert torch.all((out[0] - value).abs() <= 6 * 2.0 ** -24 * value.abs())
