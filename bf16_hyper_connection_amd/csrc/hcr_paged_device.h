@@ -32,16 +32,20 @@ struct RowOf {
   int b, token;
 };
 __device__ __forceinline__ RowOf seq_of_row(const BatchArgs& b, int row, int lane) {
-  for (int i = 0; i < b.n_seqs; i += 64) {
-    const Seq s = lane_seq(b, i, lane);
-    const unsigned long long at = __ballot(row >= s.row && row < s.row + s.tokens);
-    if (at) {
-      const int l = __ffsll(at) - 1;
-      const Seq q = of_lane(s, l);
-      return RowOf{q, i + l, row - q.row};
-    }
+  // 64 first rows at a time, of every 4,096th sequence, then of every 64th: they ascend
+  int i = 0, step = 1;
+  while ((long long)step * 64 < b.n_seqs) step *= 64;
+  for (; step > 1; step /= 64) {
+    const long long at = i + (long long)lane * step;
+    const unsigned long long upto = __ballot(at < b.n_seqs && b.q_start[min(at, (long long)b.n_seqs - 1)] <= row);
+    if (upto) i += (63 - __clzll(upto)) * step;
   }
-  return RowOf{Seq{0, 0, 0}, -1, 0};
+  const Seq s = lane_seq(b, i, lane);
+  const unsigned long long at = __ballot(row >= s.row && row < s.row + s.tokens);
+  if (!at) return RowOf{Seq{0, 0, 0}, -1, 0};
+  const int l = __ffsll(at) - 1;
+  const Seq q = of_lane(s, l);
+  return RowOf{q, i + l, row - q.row};
 }
 
 }  // namespace hcr

@@ -440,6 +440,28 @@ def test_block_topk_of_ragged_windows():
     assert all(np.array_equal(got[r], w) for r, w in want.items()) and np.all(got[n:] == 77)
 
 
+@pytest.mark.parametrize("n_seqs", [63, 64, 65, 128, 4096, 4097, 9000])
+def test_rows_of_many_sequences(n_seqs):
+    """Every row finds its sequence, runs of sequences without new tokens among them; rows behind the last."""
+    g = gen.rng(103, n_seqs)
+    page, kv = 32, 1
+    tokens = g.integers(0, 3, n_seqs) * (g.random(n_seqs // 50 + 1).repeat(50)[:n_seqs] < 0.6)
+    tokens[-1] = 1
+    starts = np.concatenate([[0], np.cumsum(tokens)]).astype(np.int32)
+    lens = (tokens + g.integers(0, 500, n_seqs)).astype(np.int32)
+    n = int(starts[-1])
+    scores = g.standard_normal((n + 2, kv, 16)).astype(np.float32)
+    table = np.zeros((n_seqs, 16), np.int32)
+    want = oracle.paged.block_topk((starts, lens, table), page, scores, 4, 1, 1)
+    cache = paged.PagedCache.allocate(1, kv, 64, page)
+    batch = paged.Batch(torch.from_numpy(starts).cuda(), torch.from_numpy(lens).cuda(),
+                        torch.from_numpy(table).cuda(), 2, 512)
+    sel = torch.full((n + 2, kv, 4), 77, dtype=torch.int32, device="cuda")
+    cache.block_topk(batch, torch.from_numpy(scores).cuda(), 4, n_first=1, n_last=1, sel=sel)
+    got = sel.cpu().numpy()
+    assert len(want) == n and all(np.array_equal(got[r], w) for r, w in want.items()) and np.all(got[n:] == 77)
+
+
 @pytest.mark.parametrize("kind", ["normal", "level", "few", "odd"])
 @pytest.mark.parametrize("ctx", [1, 33, 700, 20000, 300000])
 @pytest.mark.parametrize("n_sel,n_first,n_last", [(16, 1, 2), (3, 1, 2), (1, 0, 1), (100, 0, 3)])
@@ -666,3 +688,81 @@ def test_the_decode_step_of_the_documentation():
     # of the reciprocal and one of the product, half a step (2^-24) each
     value = names["y"][0, 40:].bfloat16().float().repeat_interleave(4, 0)
     assert torch.all((out[0] - value).abs() <= 6 * 2.0 ** -24 * value.abs())
+
+
+@pytest.mark.parametrize("max_ctx,columns", [(0, 0), (0, 3), (90, 3)])
+def test_a_batch_of_empty_sequences(max_ctx, columns):
+    """Padded sequences alone, lengths of zero and below, a table without columns: zeros, -1 and untouched pages."""
+    kv, D, page, n = 2, 128, 32, 5
+    cache = paged.PagedCache.allocate(4, kv, D, page)
+    before = [t.view(torch.int16).clone() for t in (cache.k_pages, cache.v_pages, cache.k_means)]
+    batch = paged.Batch(torch.tensor([0, 1, 3, 5], dtype=torch.int32, device="cuda"),
+                        torch.tensor([0, -7, 0], dtype=torch.int32, device="cuda"),
+                        torch.zeros(3, columns, dtype=torch.int32, device="cuda"), 2, max_ctx)
+    y = torch.randn(n, 8 + 2 * kv, D, device="cuda")
+    rope = torch.randn(max(max_ctx, 1), 64, device="cuda")
+    q = cache.append(batch, y[:, :8], y[:, 8:8 + kv], y[:, 8 + kv:], rope=rope)
+    assert torch.all(q == 0)
+    q = y[:, :8].bfloat16()
+    assert torch.all(cache.attend(batch, q) == 0)
+    sel = torch.zeros(n, kv, 3, dtype=torch.int32, device="cuda")
+    assert torch.all(cache.attend_blocks(batch, q, sel, out_dtype=torch.bfloat16) == 0)
+    scores = cache.block_scores(batch, q)
+    assert torch.all(scores == -torch.inf)
+    assert torch.all(cache.block_topk(batch, scores, 3) == -1)
+    for t, b in zip((cache.k_pages, cache.v_pages, cache.k_means), before):
+        assert torch.equal(t.view(torch.int16), b)
+
+
+def test_the_binding_refuses():
+    """Shapes, types, strides and devices that do not fit, before any pointer is taken; the library's own codes."""
+    s = pu.scene(47, 2, 64, 32, [(2, 3000), (1, 20)])
+    cache, batch = pu.dev_cache(s), pu.dev_batch(s)
+    q = pu.dev_bits(pu.queries(47, 3, 4, 64))
+    f = torch.zeros(3, 8, 64, device="cuda")
+    sel = torch.zeros(3, 2, 4, dtype=torch.int32, device="cuda")
+    scores = torch.zeros(3, 2, 94, device="cuda")
+    refused = [
+        lambda: cache.attend(batch, q.float()),
+        lambda: cache.attend(batch, q.half()),
+        lambda: cache.attend(batch, q[..., :32]),
+        lambda: cache.attend(batch, q.transpose(0, 1)),
+        lambda: cache.attend(batch, q.cpu()),
+        lambda: cache.attend(batch, q, out=torch.zeros(3, 4, 64, device="cuda", dtype=torch.float16)),
+        lambda: cache.attend(batch, q, out=torch.zeros(2, 4, 64, device="cuda")),
+        lambda: cache.attend(batch, q, out_dtype=torch.float64),
+        lambda: cache.attend(batch, q, scratch=torch.zeros(8)),
+        lambda: cache.attend_blocks(batch, q, sel.long()),
+        lambda: cache.attend_blocks(batch, q, sel[:2]),
+        lambda: cache.attend_blocks(batch, q, sel[:, :1]),
+        lambda: cache.append(batch, f[:, :4].half(), f[:, 4:6].half(), f[:, 6:].half()),
+        lambda: cache.append(batch, f[:, :4], f[:, 4:6].bfloat16(), f[:, 6:]),
+        lambda: cache.append(batch, f[:, :4], f[:, 4:7], f[:, 6:]),
+        lambda: cache.append(batch, f[:, :4], f[:, 4:6], f.permute(0, 2, 1)[:, :2]),
+        lambda: cache.append(batch, f[:, :4], f[:, 4:6], f[:, 6:], q_norm=torch.ones(32, device="cuda")),
+        lambda: cache.append(batch, f[:, :4], f[:, 4:6], f[:, 6:], rope=torch.ones(64, device="cuda")),
+        lambda: cache.block_scores(batch, q, scores=scores.double()),
+        lambda: cache.block_topk(batch, scores[:, :1], 4),
+        lambda: cache.block_topk(batch, scores, 4, sel=sel[:, :, :2]),
+    ]
+    for call in refused:
+        with pytest.raises(ValueError):
+            call()
+    coded = [
+        (lambda: cache.attend(batch, q, scratch=torch.zeros(16, dtype=torch.uint8, device="cuda")), hcr.HCR_ESCRATCH),
+        (lambda: cache.attend(batch, q, scale=float("nan")), hcr.HCR_EINVAL),
+        (lambda: cache.attend(batch, q, out=q), hcr.HCR_EALIAS),
+        (lambda: cache.attend(batch, pu.dev_bits(pu.queries(47, 3, 5, 64))), hcr.HCR_EINVAL),
+        (lambda: cache.attend_blocks(batch, q, sel[:, :, :0].contiguous()), hcr.HCR_EINVAL),
+        (lambda: cache.append(batch, f[:, :4], f[:, 4:6], f[:, 6:], rope=torch.ones(600, 32, device="cuda")),
+         hcr.HCR_EINVAL),
+        (lambda: cache.append(batch, f[:, :4], f[:, 4:6], f[:, 6:], eps=-1.0), hcr.HCR_EINVAL),
+        (lambda: cache.block_scores(batch, q, scores=scores[:, :, :20].contiguous()), hcr.HCR_EINVAL),
+        (lambda: cache.block_topk(batch, scores, 2), hcr.HCR_EINVAL),
+        (lambda: cache.block_topk(batch, scores, 0), hcr.HCR_EINVAL),
+        (lambda: pu.dev_cache(s, means=False).block_scores(batch, q), hcr.HCR_EINVAL),
+    ]
+    for call, code in coded:
+        with pytest.raises(hcr.HCRError) as e:
+            call()
+        assert e.value.rc == code
