@@ -168,9 +168,13 @@ int attn(hcr_cache_t h, const hcr_batch* batch, int heads, double scale, const v
 //              153.  Beyond 4,096 the runs stay, although lengths as even as these would still gain 5 % (8,192: 184
 //              against 194): one long sequence among short ones would hold a single CU for the whole call
 //   apart      every set begins a run of its own where runs get no more than a sixteenth longer by it (run_tiles_apart;
-//              a quarter was slower for a few long sequences), and a run is worth the part that it leaves, which is
-//              written and read again (least).  Together: 12 single tokens over up to 3,127 positions 19.0 against 22.9,
-//              37 windows of 224 rows of D = 256 over up to 249 24.4 against 34.6
+//              a quarter was slower for a few long sequences): 12 single tokens over up to 3,127 positions 19.0 against
+//              22.9
+//   least      a run has a tile for each of its waves, and a sixteenth as many tiles as rows, whose part is written and
+//              read again (37 windows of 224 rows of D = 256 over up to 249: 24.4 against 34.6 with a tile a run); but
+//              fewer, down to a tile (two for up to 16 rows), where that leaves no more runs than CUs: 56 rows of 2
+//              sequences of 483 12.1 against 15.4, 128 rows of 328 18.3 against 20.5, 2 single tokens over 4,988
+//              (D = 128) 11.1 against 12.5; without that bound 40 single tokens over up to 2,050 19.3 against 15.9
 //   waves      16 for D = 64 with more than 64 rows (42 windows of 192 rows over up to 913 positions: 23 against 32
 //              with 8).  Else 8 a work-group, one work-group a CU, for long sequences (D = 256, one of 420,000: 568
 //              against 575 with 4); 4, two work-groups a CU, for runs where no sequence is longer than 2,048 (one of
@@ -206,9 +210,12 @@ AttnPlan attn_plan(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel)
   if (p.groups > tiles) p.groups = tiles;
   if (p.groups < 1) p.groups = 1;
 
-  // a part of so many rows is written and read again: a run has a sixteenth as many tiles at least
+  // tiles that are worth a work-group, fewer where there are work-groups to spare
   const int part_rows = rows < attn_rows(p) ? rows : attn_rows(p);
-  p.least = p.groups > part_rows / 16 ? p.groups : part_rows / 16;
+  const int worth = p.groups > part_rows / 16 ? p.groups : part_rows / 16;
+  const long long even = (sets * units * tiles + CUS - 1) / CUS;
+  p.least = even < worth ? (int)even : worth;
+  if (p.least < (rows > 16 ? 1 : 2)) p.least = rows > 16 || worth == 1 ? 1 : 2;
   const int held = (room < 8 ? room : 8) / (p.row_waves * p.groups);  // work-groups of a CU
   const int fill = CUS * (held > 1 ? held : 1);
   const long long runs = ceil_div(tiles > 0 ? tiles : 1, p.least);  // of a set at most
