@@ -156,7 +156,9 @@ int attn(hcr_cache_t h, const hcr_batch* batch, int heads, double scale, const v
 // longest up to it:
 //   row tiles  two 16-row tiles a wave from 17 rows on.  D = 128: 24 rows 154 against 160, 64 rows 161 against 185.
 //              D = 256 up to 32 rows, a wave a SIMD: 24 rows of 4 sequences of 90,010 260 against 302, of 64 of
-//              4,000 197 against 257.  Not D = 64 (92 against 90), nor three for D = 256 (36 rows 283 against 303,
+//              4,000 197 against 257.  49 to 64 rows too, in two row waves, where there are tiles for them: 64 rows of
+//              16,400 50 against 58, 4 sequences of 60,000 233 against 258, but 32 of 700 71 against 61, one of 9,001 36
+//              against 35 (36 rows level, 54 against 52 at 9,001).  Not D = 64 (92 against 90), nor three for D = 256 (36 rows 283 against 303,
 //              but 57 against 51 at 9,001: the accumulators no longer fit beside the operands)
 //   rows       several row waves, D = 256: one group, as many work-groups as fit a CU (36 rows: 314 against 432
 //              with two groups), four row waves at most (96 rows: 484 against 544 with six in one work-group)
@@ -186,7 +188,10 @@ AttnPlan attn_plan(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel)
   const int group = heads / c.kv_heads;
   const int rows = n_sel ? group : b.max_tokens * group;
   const bool wide = c.head_dim == 256;
-  p.q_tiles = rows > 16 && (c.head_dim == 128 || (wide && rows <= 32)) ? 2 : 1;
+  const int tiles = n_sel ? n_sel << (c.shift - TILE_SHIFT) : ceil_div(b.max_ctx, TILE);
+  const long long sets = n_sel ? b.n_tokens : b.n_seqs;
+  const bool lengthy = rows > 48 && rows <= 64 && tiles >= 256 && sets * tiles >= 512;
+  p.q_tiles = rows > 16 && (c.head_dim == 128 || (wide && (rows <= 32 || lengthy))) ? 2 : 1;
   const int row_tiles = ceil_div(rows, 16 * p.q_tiles);
   p.row_blocks = ceil_div(row_tiles, wide ? 4 : 8);
   p.row_waves = ceil_div(row_tiles, p.row_blocks);
@@ -196,9 +201,7 @@ AttnPlan attn_plan(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel)
   const int waves = room > 8 && p.row_waves <= 4 ? 8 : room;
   const int most_groups = alone ? 1 : waves / p.row_waves;
 
-  const int tiles = n_sel ? n_sel << (c.shift - TILE_SHIFT) : ceil_div(b.max_ctx, TILE);
   const int units = c.kv_heads * p.row_blocks;
-  const long long sets = n_sel ? b.n_tokens : b.n_seqs;
   const long long full = sets * units;  // work-groups of whole sets
   p.whole = full < CUS              ? tiles <= (wide ? (rows > 16 ? 6 : 12) : 3 * most_groups)
             : n_sel                 ? 1  // lists are alike

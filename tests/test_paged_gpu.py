@@ -80,7 +80,7 @@ def test_attend_many_rows(head_dim, kv, group, T):
 
 
 @pytest.mark.parametrize("head_dim,page,kv,group,T", [(128, 64, 1, 4, 1), (256, 64, 2, 6, 2), (64, 32, 1, 8, 4),
-                                                      (128, 256, 1, 16, 5)])
+                                                      (128, 256, 1, 16, 5), (256, 64, 1, 8, 8)])
 def test_attend_split_lengths(head_dim, page, kv, group, T):
     """Long and short sequences in one call: splits that only some sequences reach, joined."""
     s = pu.scene(4, kv, head_dim, page, [(T, 20011), (1, 5), (T, 4097), (1, 8192), (1, 0)])
