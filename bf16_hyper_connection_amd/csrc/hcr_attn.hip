@@ -389,8 +389,10 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
   const bool idle = r0 >= rows.count;
   Tiles<D, SEL> tiles(a, set, h, rows.len_max, lane, lo, hi, tg, TG, entry);
 
-  // Keys of the next tile are loaded behind their last use in this one, values likewise, so that one of the two is
-  // always on its way while the other is worked on; the first ones go out ahead of the query rows' way through LDS.
+  // Keys of the next tile are loaded behind their last use in this one, values likewise.  (The compiler's wait for the
+  // keys covers the values too, since loads behind a branch leave it no count.  Loads without the branch, one address
+  // for every lane past the last tile: 64 rows of D = 256 over 60,010 positions 219 against 236 us, 60 of D = 64 over
+  // 50,000 78 against 88, but 96 of D = 256 over 60,001 362 against 339, one row over 700 9.6 against 9.1.)
   const uint32_t k_lane = ((uint32_t)(lg << a.c.shift) + 8 * (li >> 2) + (li & 3)) * 16;  // key tile 0's row li
   const uint32_t v_lane = (uint32_t)(lg * D + li) * 16;
   const uint32_t k_step = 4u << a.c.shift << 4;  // 32 dimensions on
@@ -429,14 +431,6 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
   // row waves alone keep step, so that the first one's misses are the others' hits in L1 (36 rows of D = 256: 314
   // against 342 us; all of them find the same tiles)
   const bool together = TG == 1 && RT > 1;
-  auto store_rows = [&]() {
-    if (tg != 0) return;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-      for (int k = 0; k < KS; ++k) lds_q[(m * KS + k) * 64] = qf[m][k];
-    }
-  };
   f32x4 acc[MT][DT];
   float mx[MT], sum[MT];
 #pragma unroll
@@ -448,7 +442,13 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
   }
 
   bool more = tiles.find();
-  store_rows();
+  if (tg == 0) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int k = 0; k < KS; ++k) lds_q[(m * KS + k) * 64] = qf[m][k];
+    }
+  }
   if (more && !idle) {
     load_keys();
     load_values();
