@@ -389,25 +389,30 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
   const bool idle = r0 >= rows.count;
   Tiles<D, SEL> tiles(a, set, h, rows.len_max, lane, lo, hi, tg, TG, entry);
 
-  // Keys of the next tile are loaded behind their last use in this one, values likewise.  (The compiler's wait for the
-  // keys covers the values too, since loads behind a branch leave it no count.  Loads without the branch, one address
-  // for every lane past the last tile: 64 rows of D = 256 over 60,010 positions 219 against 236 us, 60 of D = 64 over
-  // 50,000 78 against 88, but 96 of D = 256 over 60,001 362 against 339, one row over 700 9.6 against 9.1.)
+  // Keys of the next tile are loaded behind their last use in this one, values likewise.  Loads return in order and a
+  // wait counts the loads issued behind the one it is for: behind a branch there is no count, and the wait for the keys
+  // covers the values too.  BLIND: no branch, past the last tile every lane asks for the tile's first 16 bytes again.
+  // Taken where several row waves of D = 64, or of two tiles of D = 256, share the tiles: 60 rows of D = 64 over 50,000
+  // 69 against 81 us, over 20,000 39 against 43, 64 of D = 256 over 16,400 49 against 51 (1,000 and 300 positions, 256
+  // rows of D = 64: 1 % slower).  Not elsewhere, where the loads for nothing cost as much as they gain: 60 rows of
+  // D = 128 110 against 107, 96 of D = 256 362 against 339, one row over 700 9.6 against 9.1, over 420,000 536 against
+  // 529; for 36 rows of D = 256 49.7 against 50.7.
+  constexpr bool BLIND = !ONCE && !SEL && (D == 64 || (D == 256 && MT == 2));
   const uint32_t k_lane = ((uint32_t)(lg << a.c.shift) + 8 * (li >> 2) + (li & 3)) * 16;  // key tile 0's row li
   const uint32_t v_lane = (uint32_t)(lg * D + li) * 16;
   const uint32_t k_step = 4u << a.c.shift << 4;  // 32 dimensions on
   uint4 kf[2][KS], vf[DT];
-  auto load_keys = [&]() {
+  auto load_keys = [&](uint32_t on) {
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
-      const char* at = tiles.kp + k * k_step;
-      kf[0][k] = ld_kv<ONCE>(at + k_lane);
-      kf[1][k] = ld_kv<ONCE>(at + k_lane + 4 * 16);
+      const char* at = tiles.kp + (k * k_step & on);
+      kf[0][k] = ld_kv<ONCE>(at + (k_lane & on));
+      kf[1][k] = ld_kv<ONCE>(at + (k_lane & on) + (4 * 16 & on));
     }
   };
-  auto load_values = [&]() {
+  auto load_values = [&](uint32_t on) {
 #pragma unroll
-    for (int d = 0; d < DT; ++d) vf[d] = ld_kv<ONCE>(tiles.vp + v_lane + 16 * 16 * d);
+    for (int d = 0; d < DT; ++d) vf[d] = ld_kv<ONCE>(tiles.vp + (v_lane & on) + (16 * 16 * d & on));
   };
   // the lane's query row of each 16-row tile and its length; the rows as operands in LDS, one copy for all groups
   // (in registers they would push the loop's operands out)
@@ -449,14 +454,22 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
       for (int k = 0; k < KS; ++k) lds_q[(m * KS + k) * 64] = qf[m][k];
     }
   }
-  if (more && !idle) {
-    load_keys();
-    load_values();
+  if (BLIND && (idle || !more)) {
+    lds_barrier();
+    while (more) {
+      more = tiles.find();
+      if (together) __builtin_amdgcn_s_barrier();
+    }
+  } else {
+    if (BLIND || (more && !idle)) {
+      load_keys(~0u);
+      load_values(~0u);
+    }
+    lds_barrier();
   }
-  lds_barrier();
 
   while (more) {
-    if (idle) {
+    if (!BLIND && idle) {
       more = tiles.find();
       if (together) __builtin_amdgcn_s_barrier();
       continue;
@@ -477,7 +490,8 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
     __builtin_amdgcn_sched_barrier(0);
     more = tiles.find();
     if (together) __builtin_amdgcn_s_barrier();
-    if (more) load_keys();
+    const uint32_t on = !BLIND || more ? ~0u : 0u;
+    if (BLIND || more) load_keys(on);
     __builtin_amdgcn_sched_barrier(0);
 
     if (!whole) {
@@ -510,7 +524,7 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    if (more) load_values();
+    if (BLIND || more) load_values(on);
     __builtin_amdgcn_sched_barrier(0);
   }
 #pragma unroll
