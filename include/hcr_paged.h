@@ -117,8 +117,8 @@ size_t hcr_attn_scratch_bytes(hcr_cache_t c, const hcr_batch* batch, int heads, 
 /* Attention of a window over its sequences' pages: the window's own keys and values
  * are in the cache already (hcr_cache_append), token n sees positions 0..p.
  *   q    BF16 [n_tokens][heads][D]       out  float or BF16 (out_type) [n_tokens][heads][D]
- *   scratch  hcr_attn_scratch_bytes, 256-byte aligned; calls that share one must be
- *            ordered on one stream.  NULL where 0 bytes are needed
+ *   scratch  hcr_attn_scratch_bytes, 256-byte aligned; calls that share one, replays of
+ *            graphs among them, must be ordered on one stream.  NULL where 0 bytes are needed
  * Products of BF16 values in FP32 on the matrix cores; probabilities in two BF16 parts
  * (2^-17), in three for a float `out`.  A row that sees no position is zeros.  |scale|
  * < 1e30.
