@@ -338,11 +338,12 @@ __device__ __forceinline__ void probabilities(const AttnArgs& a, const f32x4 (&s
 #pragma unroll
     for (int d = 0; d < DT; ++d) acc[d] *= f;
   }
-  // exponents with the scale in two parts: one rounding, of the difference from the maximum
+  // exponents with the scale in two parts, the small one's product added to the difference from the maximum: both sums
+  // round at the difference's size (the other way round the first would round at the maximum's)
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float v = s[i >> 2][i & 3];
-    p[i] = exp2_of(__builtin_fmaf(v, a.scale_hi, __builtin_fmaf(v, a.scale_lo, -mx)));
+    p[i] = exp2_of(__builtin_fmaf(v, a.scale_lo, __builtin_fmaf(v, a.scale_hi, -mx)));
   }
   if (!whole) {
 #pragma unroll

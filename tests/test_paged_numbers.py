@@ -1,0 +1,120 @@
+"""Numbers of the paged cache's kernels at their edges: bounds close enough that a rounding at the wrong place shows,
+values that are no numbers, rows that must not feel their neighbours.
+
+The close bounds use keys and queries whose products are whole numbers below 2^24, which FP32 sums hold exactly in any
+order, so that the softmax and the second product alone are off.  In half steps (2^-24 of a value), for n positions
+whose exponents of two lie within E of the row's maximum:
+
+  exponent   two fused products, each rounded once, of size E + 1 at most: 2 (E + 1) ln 2 of a probability
+  power      one step: 2
+  sum        a chain of at most n additions, 16 more over lanes, waves and parts
+  product    three parts a probability (their sum is all of its 24 bits), each added with at most one whole step: 6 n,
+             16 more over waves and parts
+  quotient   reciprocal and product: 3
+
+Exponents and powers stand in the sum and in the product, so each counts twice."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from bf16_hyper_connection_amd import inputs as gen
+from tests import paged_util as pu
+from tests.libhcr_util import ensure_built
+
+HALF = 2.0 ** -24
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lib():
+    ensure_built()
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+
+
+def room(n, E):
+    return (4 * np.log(2) * (E + 1) + 4 + (n + 16) + (6 * n + 16) + 3) * HALF
+
+
+def _set_keys(s, keys):
+    """Visible keys (the others stay NaN) [pages][kv heads][page][D]."""
+    old = oracle.paged.decode_keys(s.k_bits)
+    s.k_bits = pu.store_keys(np.where(np.isnan(old), np.uint16(pu.NAN_BITS), pu.bf16(keys)))
+
+
+def _large_scores(seed, D, group, windows, around):
+    """Products within 24 of ``around`` (under 2^21): whole numbers."""
+    g = gen.rng(110, seed)
+    s = pu.scene(seed, 1, D, 32, windows)
+    keys = np.full((s.k_bits.shape[0], 1, 32, D), 128, np.float32)
+    keys[..., :8] = g.integers(0, 4, keys[..., :8].shape)
+    keys[..., 8] = 1
+    _set_keys(s, keys)
+    q = np.zeros((s.n_tokens, group, D), np.float32)
+    q[..., :8] = g.integers(1, 3, q[..., :8].shape)
+    base = around - 24
+    q[..., 8] = base % 128
+    share = base // 128
+    for d in range(9, D):
+        q[..., d] = share // (D - d)
+        share -= share // (D - d)
+    assert share == 0 and q.max() <= 256
+    return s, q
+
+
+def _close(out, s, q, scale, E, label):
+    keys, values = pu.decoded(s)
+    want = oracle.paged.attend(s.batch, keys, values, q, scale)
+    size = oracle.paged.attend(s.batch, keys, np.abs(values), q, scale)  # probabilities times magnitudes
+    got = out.double().cpu().numpy()
+    for n, b, p in oracle.paged.tokens(s.q_start, s.ctx_len):
+        off = np.abs(got[n] - want[n]) - room(p + 1, E) * size[n]
+        assert np.all(off <= 0), f"{label}: row {n} of sequence {b}, {off.max():.2e} too much"
+
+
+# the first four: scores at which v times the scale's small part crosses half a step of the maximum (or one and a half)
+LARGE = [(128, 128 ** -0.5, 852189), (128, 0.1, 495313), (64, 0.3, 330209), (256, -0.2, 990626),
+         (128, 128 ** -0.5, 12288), (64, 0.125, 500000), (256, 0.0625, 1000000), (128, 0.3, 300001)]
+
+
+@gpu
+@pytest.mark.parametrize("D,scale,around", LARGE)
+def test_large_scores_keep_their_differences(lib, D, scale, around):
+    """Scores of up to 10^5 that differ by a few: exponents rounded at the scores' size would be off by 2^-6."""
+    s, q = _large_scores(1, D, 6, [(3, 40), (1, 290), (2, 2), (1, 9)], around)
+    out = pu.dev_cache(s).attend(pu.dev_batch(s), pu.dev_bits(pu.bf16(q)), scale=scale)
+    _close(out, s, q, scale, 48 * abs(scale) * np.log2(np.e) + 8, f"D {D} scale {scale}")
+
+
+def _fma(a, b, c):
+    """FP32, rounded once (the product of two FP32 values is exact in 64 bits; of the sum's two roundings the first is
+    2^-29 of the second)."""
+    return (np.float64(a) * np.float64(b) + np.float64(c)).astype(np.float32)
+
+
+def _parts(scale):
+    log2e = scale * 1.4426950408889634
+    hi = np.float32(log2e)
+    if abs(float(hi)) >= abs(log2e):
+        hi = np.nextafter(hi, np.float32(0))
+    return hi, np.float32(log2e - float(hi))
+
+
+@pytest.mark.parametrize("D,scale,around", LARGE[:4])
+def test_a_maximum_subtracted_from_the_small_part_fails_the_bound(D, scale, around):
+    """The bound sees the difference between v hi - max + v lo and v lo - max + v hi."""
+    s, q = _large_scores(1, D, 6, [(1, 290)], around)
+    keys, values = pu.decoded(s)
+    k = np.concatenate([keys[j, 0] for j in s.table[0] if j >= 0])[:290]
+    v = np.concatenate([values[j, 0] for j in s.table[0] if j >= 0])[:290]
+    hi, lo = _parts(scale)
+    x = (q[0] @ k.T).astype(np.float32)
+    w = np.exp(scale * (x.astype(np.float64) - x.max(-1, keepdims=True)))
+    w /= w.sum(-1, keepdims=True)
+    top = (x * hi).max(-1, keepdims=True)
+    bound = room(290, 48 * abs(scale) * np.log2(np.e) + 8)
+    for order, fits in ((_fma(x, lo, _fma(x, hi, -top)), True), (_fma(x, hi, _fma(x, lo, -top)), False)):
+        p = np.exp2(order.astype(np.float64))
+        off = np.abs((p / p.sum(-1, keepdims=True)) @ v - w @ v)
+        assert np.all(off <= bound * (w @ np.abs(v))) == fits
