@@ -19,11 +19,13 @@ typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 // 8 heads of 256, 4 tokens in 11.1 us.
 constexpr int SCORE_WAVES = 4;
 
+// The larger one, NaN where one is NaN (one instruction, v_maximum3_f32; fmaxf would drop a head that is no number).
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 __device__ __forceinline__ float max_dpp(float v, int width) {  // over aligned runs of `width` lanes of a row
-  if (width >= 2) v = fmaxf(v, dpp<0xB1>(v));
-  if (width >= 4) v = fmaxf(v, dpp<0x4E>(v));
-  if (width >= 8) v = fmaxf(v, dpp<0x141>(v));
-  if (width >= 16) v = fmaxf(v, dpp<0x140>(v));
+  if (width >= 2) v = larger(v, dpp<0xB1>(v));
+  if (width >= 4) v = larger(v, dpp<0x4E>(v));
+  if (width >= 8) v = larger(v, dpp<0x141>(v));
+  if (width >= 16) v = larger(v, dpp<0x140>(v));
   return v;
 }
 
@@ -93,7 +95,7 @@ __global__ __launch_bounds__(64 * SCORE_WAVES) void block_scores(ScoreArgs a, in
 #pragma unroll
     for (int p = 0; p < TILES; ++p)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) best[p][i] = fmaxf(best[p][i], c[p][i]);
+      for (int i = 0; i < 4; ++i) best[p][i] = larger(best[p][i], c[p][i]);
     if ((tile + 1) % tiles_per_token) continue;
     const int t = tile / tiles_per_token * tokens_per_tile + li / width;
     const int last = max(seq.first + t, 0) >> a.c.shift;  // this token scores the pages before it

@@ -118,3 +118,36 @@ def test_a_maximum_subtracted_from_the_small_part_fails_the_bound(D, scale, arou
         p = np.exp2(order.astype(np.float64))
         off = np.abs((p / p.sum(-1, keepdims=True)) @ v - w @ v)
         assert np.all(off <= bound * (w @ np.abs(v))) == fits
+
+
+@gpu
+@pytest.mark.parametrize("head_dim,page,kv,group", [(128, 64, 2, 4), (64, 32, 1, 24), (256, 64, 1, 6), (128, 32, 2, 1),
+                                                    (64, 64, 2, 16)])
+@pytest.mark.parametrize("odd", [np.nan, np.inf, -np.inf])
+def test_scores_of_what_is_no_number(lib, head_dim, page, kv, group, odd):
+    """One head's query, one page's mean: the scores that they enter are the definition's, NaN or infinite; no other."""
+    s = pu.scene(6, kv, head_dim, page, [(4, 40 * page + 3), (2, 9 * page), (1, 2 * page + 1)])
+    s.table[1, 2] = -1
+    q = pu.queries(6, s.n_tokens, kv * group, head_dim)
+    bits = pu.bf16([odd])[0]
+    q[1, group // 2, 7] = bits
+    q[5, -1, 1] = bits
+    s.means[s.table[0, 11], 0, 5] = bits
+    s.means[s.table[1, 4], -1, head_dim - 1] = bits
+    means, qf = oracle.bf16_bits_to_f64(s.means), oracle.bf16_bits_to_f64(q)
+    with np.errstate(invalid="ignore"):
+        want = oracle.paged.block_scores(s.batch, means, page, qf)
+    scores = torch.zeros(s.n_tokens, kv, 41, device="cuda")
+    pu.dev_cache(s).block_scores(pu.dev_batch(s), pu.dev_bits(q), scores=scores)
+    got = scores.double().cpu().numpy()
+    fine_q, fine_m = (np.where(np.isfinite(x), x, 0) for x in (qf, means))
+    room = head_dim * HALF * float(np.abs(fine_q).sum(-1).max() * np.abs(fine_m).max())
+    odd_ones = 0
+    for n, w in want.items():
+        g = got[n, :, :w.shape[1]]
+        assert np.array_equal(np.isnan(w), np.isnan(g)) and np.array_equal(np.isinf(w), np.isinf(g)), f"row {n}"
+        assert np.array_equal(w[np.isinf(w)], g[np.isinf(w)])
+        fine = np.isfinite(w)
+        odd_ones += (~fine).sum()
+        assert np.all(np.abs(g[fine] - w[fine]) <= room), f"row {n}"
+    assert odd_ones > 20
