@@ -30,7 +30,6 @@
 // their way where it has 256 KB with one row wave, and the second launch takes 7.
 
 #include <float.h>
-#include <limits.h>
 #include <math.h>
 #include <hip/hip_runtime.h>
 
@@ -295,25 +294,24 @@ __device__ __forceinline__ bool any_odd(const uint4 (&v)[N]) {
   return __any(top[0] >= 0x7F80 || top[1] >= 0x7F80);
 }
 
-// The values from position `from` on that are no numbers become zeros; the first one's position.  p: the lane's first.
-template <int N>
-__device__ __forceinline__ int drop_odd(uint4 (&v)[N], int p, int from) {
-  int first = INT_MAX;
+// The values from position `from` on that are no numbers become zeros; in their place, ones where they were and zeros
+// elsewhere.  p: the position of the first of 8.
+__device__ __forceinline__ uint4 drop_odd(uint4& v, int p, int from) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w}, at[4] = {0, 0, 0, 0};
 #pragma unroll
-  for (int d = 0; d < N; ++d) {
-    uint32_t w[4] = {v[d].x, v[d].y, v[d].z, v[d].w};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t half = e & 1 ? 0x7F800000u : 0x7F80u;
-      if ((w[e >> 1] & half) == half && p + e >= from) {
-        w[e >> 1] &= e & 1 ? 0xFFFFu : 0xFFFF0000u;
-        first = min(first, p + e);
-      }
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t half = e & 1 ? 0x7F800000u : 0x7F80u;
+    if ((w[e >> 1] & half) == half && p + e >= from) {
+      w[e >> 1] &= e & 1 ? 0xFFFFu : 0xFFFF0000u;
+      at[e >> 1] |= e & 1 ? 0x3F800000u : 0x3F80u;
     }
-    v[d] = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  for (int o = 32; o; o >>= 1) first = min(first, __shfl_xor(first, o));
-  return __builtin_amdgcn_readfirstlane(first);
+  v = make_uint4(w[0], w[1], w[2], w[3]);
+  return make_uint4(at[0], at[1], at[2], at[3]);
+}
+// Ones at the positions, of 8 from p on, that a row of length len sees.
+__device__ __forceinline__ uint4 seen8(int p, int len) {
+  return visible8(make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u), p, len);
 }
 
 // The lane's 8 products s of one row as probabilities against the row's running maximum; its sum and values follow
@@ -500,9 +498,20 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
       for (int d = 0; d < DT; ++d) vf[d] = visible8(vf[d], now + 8 * lg, rows.len_max);
     }
     // A value that is no number and that only later tokens see: zero times it would reach the earlier ones' rows.  It
-    // leaves the product, and the rows that see it become NaN.
-    int odd = INT_MAX;
-    if (!SEL && !whole && rows.len_min < rows.len_max && any_odd(vf)) odd = drop_odd(vf, now + 8 * lg, rows.len_min);
+    // leaves the product, and its dimension of the rows that see it becomes NaN: those where a product of such places
+    // with the rows' visible ones is not zero.
+    if (!SEL && !whole && rows.len_min < rows.len_max && any_odd(vf)) {
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        const uint4 at = drop_odd(vf[d], now + 8 * lg, rows.len_min);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const f32x4 met = mfma(at, seen8(now + 8 * lg, len[m]), f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[m][d][i] = met[i] > 0.f ? NAN : acc[m][d][i];
+        }
+      }
+    }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       float p[8];
@@ -517,11 +526,6 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
         const uint4 pr = split_rest(p, ph, pl);
 #pragma unroll
         for (int d = 0; d < DT; ++d) acc[m][d] = mfma(vf[d], pr, acc[m][d]);
-      }
-      if (!SEL && odd < INT_MAX) {
-        const float none = len[m] > odd ? NAN : 0.f;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) acc[m][d] += f32x4{none, none, none, none};
       }
     }
     __builtin_amdgcn_sched_barrier(0);

@@ -32,9 +32,10 @@
  * 0..n_tokens-1.  A token at a negative position (a padded sequence of length 0)
  * appends nothing and its row of every output is zeros (scores: nothing; topk:
  * -1).  Rows behind the last sequence's (from q_start[n_seqs]) are left as they
- * were.  A row whose q, keys or values are not finite is not either; no other row
- * depends on them, nor on what else lies in a page (behind the last position, NaN
- * included), with one exception: a key whose product with q is -inf weighs nothing.
+ * were.  A row whose q or keys are not finite is not either; a value that is not
+ * finite makes its own dimension of the rows that see it so.  No other row depends on
+ * them, nor on what else lies in a page (behind the last position, NaN included), with
+ * one exception: a key whose product with q is -inf weighs nothing.
  *
  * Every call is asynchronous on `stream`, makes no allocation, synchronisation or
  * memset and can be captured into a HIP graph; its lengths and pages are read when

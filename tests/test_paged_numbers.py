@@ -151,3 +151,33 @@ def test_scores_of_what_is_no_number(lib, head_dim, page, kv, group, odd):
         odd_ones += (~fine).sum()
         assert np.all(np.abs(g[fine] - w[fine]) <= room), f"row {n}"
     assert odd_ones > 20
+
+
+SHAPES = [(128, 2, 4, 5), (256, 1, 6, 7), (64, 1, 8, 20), (128, 1, 12, 3), (256, 2, 10, 3), (256, 1, 16, 9)]
+
+
+@gpu
+@pytest.mark.parametrize("D,kv,group,T", SHAPES)
+@pytest.mark.parametrize("odd", [np.inf, -np.inf, np.nan])
+def test_a_value_that_is_no_number_reaches_its_own_dimension(lib, D, kv, group, T, odd):
+    """Wherever in its tile, whichever rows see it: a product's other dimensions are as ever."""
+    windows = [(T, 300), (T, 64), (T, T), (T, 5003), (T, 160 + T // 2)]
+    s = pu.scene(3, kv, D, 64, windows)
+    q = pu.queries(3, s.n_tokens, kv * group, D)
+    qf = oracle.bf16_bits_to_f64(q)
+    keys, values = pu.decoded(s)
+    want = oracle.paged.attend(s.batch, keys, values, qf, 0.1)
+    tol = pu.rows_tolerance(qf, float(np.sqrt(np.nansum(keys ** 2, axis=-1)).max()), 0.1, 5003, False)
+    bits = pu.bf16([odd])[0]
+    # dimension 3 mod 16 of every sequence's last but one position, dimension 5 of its window's first
+    hit = np.zeros((s.n_tokens, D), bool)
+    for b, (_, c) in enumerate(windows):
+        for at, dim in ((c - 2, 3), (c - T, 5)):
+            s.v_bits[s.table[b, at // 64], :, at % 64 // 8, dim::16, at % 8] = bits
+            hit[s.q_start[b] + at - (c - T):s.q_start[b + 1], dim::16] = True
+    out = pu.dev_cache(s).attend(pu.dev_batch(s), pu.dev_bits(q), scale=0.1)
+    got = out.double().cpu().numpy()
+    for n, w in want.items():
+        assert not np.isfinite(got[n][:, hit[n]]).any(), f"row {n}"
+        off = np.linalg.norm((got[n] - w)[:, ~hit[n]], axis=1)
+        assert np.all(off <= tol * np.linalg.norm(w, axis=1)), f"row {n}"
