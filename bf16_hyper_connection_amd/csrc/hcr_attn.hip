@@ -329,7 +329,7 @@ __device__ __forceinline__ void probabilities(const AttnArgs& a, const f32x4 (&s
   float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
   top = rows_max(top);
   if (__any(top > mx + 8.f)) {
-    const float high = fmaxf(mx, top);
+    const float high = top > mx + 8.f ? top : mx;  // a row's own: no row feels another's
     const float f = exp2_of(mx - high);
     mx = high;
     sum *= f;

@@ -181,3 +181,27 @@ def test_a_value_that_is_no_number_reaches_its_own_dimension(lib, D, kv, group, 
         assert not np.isfinite(got[n][:, hit[n]]).any(), f"row {n}"
         off = np.linalg.norm((got[n] - w)[:, ~hit[n]], axis=1)
         assert np.all(off <= tol * np.linalg.norm(w, axis=1)), f"row {n}"
+
+
+@gpu
+@pytest.mark.parametrize("D,kv,group,T", SHAPES + [(128, 1, 1, 16), (64, 1, 1, 31)])
+@pytest.mark.parametrize("later", ["large", np.inf, np.nan])
+def test_rows_do_not_feel_later_tokens(lib, D, kv, group, T, later):
+    """Bit for bit: the last token's query, key and value are others, the rows before it the same."""
+    windows = [(T, 290 + T), (T, 2 * T), (T, T), (T, 3000 + T)]
+    a, b = (pu.scene(4, kv, D, 64, windows) for _ in range(2))
+    q = pu.queries(4, a.n_tokens, kv * group, D)
+    first = pu.dev_cache(a).attend(pu.dev_batch(a), pu.dev_bits(q), scale=0.05)
+    last = np.arange(a.n_tokens) % T == T - 1
+    for i, (_, c) in enumerate(windows):
+        page, slot = b.table[i, (c - 1) // 64], (c - 1) % 64
+        if later == "large":
+            b.k_bits[page, :, :, slot] ^= 0x8000
+            b.v_bits[page, :, slot // 8, :, slot % 8] ^= 0x8000
+        else:
+            b.k_bits[page, :, 0, slot, 0] = pu.bf16([later])[0]
+            b.v_bits[page, :, slot // 8, 1, slot % 8] = pu.bf16([later])[0]
+    q[last] = pu.bf16(oracle.bf16_bits_to_f64(q[last]) * 16)
+    again = pu.dev_cache(b).attend(pu.dev_batch(b), pu.dev_bits(q), scale=0.05)
+    keep = torch.from_numpy(~last).cuda()
+    assert torch.isfinite(first).all() and torch.equal(first[keep], again[keep])
