@@ -1,6 +1,7 @@
 // C ABI of the paged cache: argument checks, the handle and the plan of an attention call.  Every check runs on
 // the host before any HIP call.
 
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 #include <stdlib.h>
@@ -141,10 +142,16 @@ int attn(hcr_cache_t h, const hcr_batch* batch, int heads, double scale, const v
   a.group = heads / c.kv_heads;
   a.out_type = out_type;
   const double log2e = scale * 1.4426950408889634;
-  // both parts of one sign, neither zero: a product of -inf stays -inf and weighs nothing
+  // both parts of one sign, neither zero (the least FP32 value if need be): a product of -inf stays -inf and weighs
+  // nothing
   a.scale_hi = (float)log2e;
   if (fabs(a.scale_hi) >= fabs(log2e)) a.scale_hi = nextafterf(a.scale_hi, 0.f);
   a.scale_lo = (float)(log2e - a.scale_hi);
+  if (scale != 0) {
+    const float least = copysignf(FLT_TRUE_MIN, (float)scale);
+    if (a.scale_hi == 0.f) a.scale_hi = least;
+    if (a.scale_lo == 0.f) a.scale_lo = least;
+  }
   a.out = out;
   a.part = static_cast<float*>(scratch);
   return launch_attn(a, stream);

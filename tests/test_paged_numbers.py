@@ -205,3 +205,18 @@ def test_rows_do_not_feel_later_tokens(lib, D, kv, group, T, later):
     again = pu.dev_cache(b).attend(pu.dev_batch(b), pu.dev_bits(q), scale=0.05)
     keep = torch.from_numpy(~last).cuda()
     assert torch.isfinite(first).all() and torch.equal(first[keep], again[keep])
+
+
+@gpu
+@pytest.mark.parametrize("scale", [1e-30, -3e-38, 1e-42, -1e-45, 1e-300])
+def test_a_product_of_minus_infinity_weighs_nothing_at_any_scale(lib, scale):
+    s = pu.scene(5, 1, 64, 32, [(2, 70), (1, 33)])
+    q = pu.queries(5, s.n_tokens, 4, 64)
+    q[..., 0] = pu.bf16([2.0])[0]
+    for b, at in ((0, 5), (0, 66), (1, 0)):
+        s.k_bits[s.table[b, at // 32], 0, 0, at % 32, 0] = pu.bf16([-np.inf if scale > 0 else np.inf])[0]
+    keys, values = pu.decoded(s)
+    qf = oracle.bf16_bits_to_f64(q)
+    want = oracle.paged.attend(s.batch, keys, values, qf, scale)
+    out = pu.dev_cache(s).attend(pu.dev_batch(s), pu.dev_bits(q), scale=scale)
+    pu.check_rows(out, want, pu.rows_tolerance(qf, 20.0, scale, 70, False), "small scale")
