@@ -181,6 +181,21 @@ class PagedCache:
         if rc != HCR_OK:
             raise HCRError(rc, fn.__name__)
 
+    def _new(self, stream, shape, dtype, fill=None):
+        """A new tensor of a call, filled, on the stream that the call runs on: behind that stream's earlier steps and
+        ahead of the call's kernels.  Torch's current stream, on which the caller takes it, is noted, so that its
+        memory is not used again before that stream is done with it."""
+        if stream is None or stream == torch._C._cuda_getCurrentRawStream(self.device.index):
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+            return t if fill is None else t.fill_(fill)
+        own = torch.cuda.ExternalStream(stream, device=self.device) if stream else torch.cuda.default_stream(self.device)
+        with torch.cuda.stream(own):
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+            if fill is not None:
+                t.fill_(fill)
+        t.record_stream(torch.cuda.current_stream(self.device))
+        return t
+
     # The checks below run at every call, ahead of kernels of a few microseconds: each reads a property once.
 
     def _heads_of(self, q):
@@ -290,8 +305,8 @@ class PagedCache:
         """
         n, heads = self._heads_of(q)
         if scores is None:
-            scores = torch.full((n, self.kv_heads, max(-(-batch.max_ctx // self.page), 1)), float("-inf"),
-                                device=self.device)
+            scores = self._new(stream, (n, self.kv_heads, max(-(-batch.max_ctx // self.page), 1)), torch.float32,
+                               float("-inf"))
         else:
             if scores.dim() != 3:
                 raise ValueError(f"scores: float32 [{n}][{self.kv_heads}][pages]")

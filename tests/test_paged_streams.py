@@ -1,0 +1,143 @@
+"""The paged cache's calls on another stream than torch's current one: what they make belongs to the stream they run on.
+
+On the CPU the binding runs against stand-ins for torch's streams and allocations and for the library, which note on
+which stream each step is queued; on the GPU the other stream is held up and must neither meet nor miss anything."""
+
+import contextlib
+import types
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from bf16_hyper_connection_amd import paged
+from tests import paged_util as pu
+from tests.libhcr_util import ensure_built
+
+MAIN, OTHER = 11, 22  # raw streams of the stand-ins
+
+
+class Noted(torch.Tensor):
+    """A host tensor that notes on which stream it is filled, and the streams it is recorded on."""
+
+    def record_stream(self, stream):
+        self.log.append(("record", stream, self.data_ptr()))
+
+    def fill_(self, value):
+        self.log.append(("fill", self.streams[-1], self.data_ptr()))
+        return super().fill_(value)
+
+    def zero_(self):
+        return self.fill_(0)
+
+
+class StandIn:
+    """torch, with streams that are numbers and allocations that are noted."""
+
+    def __init__(self):
+        self.log, self.streams = [], [MAIN]
+        self.cuda = types.SimpleNamespace(
+            stream=self._stream, ExternalStream=lambda s, device=None: s, current_stream=lambda d=None: self.streams[-1],
+            default_stream=lambda d=None: 0, device=lambda d: contextlib.nullcontext())
+        self._C = types.SimpleNamespace(_cuda_getCurrentRawStream=lambda i: self.streams[-1],
+                                        _cuda_getDevice=lambda: None)
+
+    def __getattr__(self, name):
+        return getattr(torch, name)
+
+    @contextlib.contextmanager
+    def _stream(self, s):
+        self.streams.append(s)
+        yield
+        self.streams.pop()
+
+    def _noted(self, t):
+        t = t.as_subclass(Noted)
+        t.log, t.streams = self.log, self.streams
+        return t
+
+    def empty(self, *shape, **kw):
+        t = self._noted(torch.empty(*shape, **kw))
+        self.log.append(("make", self.streams[-1], t.data_ptr()))
+        return t
+
+    def full(self, shape, value, **kw):
+        return self.empty(shape, **{"dtype": torch.float32, **kw}).fill_(value)
+
+
+class Library:
+    """Entry points that note their stream (the last argument)."""
+
+    def __init__(self, log):
+        self.log = log
+
+    def hcr_attn_scratch_bytes(self, *args):
+        return 4096
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.log.append((name, args[-1], args))
+            return 0
+        call.__name__ = name
+        return call
+
+
+@pytest.fixture()
+def stand_in(monkeypatch):
+    fake = StandIn()
+    monkeypatch.setattr(paged, "torch", fake)
+    cache = object.__new__(paged.PagedCache)
+    cpu = torch.device("cpu")
+    cache.__dict__.update(kv_heads=2, head_dim=64, page=32, n_pages=4, device=cpu, handle=None, _L=Library(fake.log))
+    batch = types.SimpleNamespace(device=cpu, max_ctx=100, _of=lambda n: None)
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    return types.SimpleNamespace(fake=fake, cache=cache, batch=batch, q=q)
+
+
+def _all_on(log, stream, entry):
+    """Every allocation and fill of the call on its stream, before it is used there."""
+    steps = [kind for kind, _, _ in log]
+    assert steps.count(entry) == 1
+    assert [s for kind, s, _ in log if kind in ("make", "fill", entry)].count(stream) == sum(
+        kind in ("make", "fill", entry) for kind in steps), log
+    assert max([i for i, k in enumerate(steps) if k in ("make", "fill")], default=-1) < steps.index(entry)
+
+
+@pytest.mark.parametrize("stream", [None, MAIN, OTHER, 0])
+def test_scores_are_filled_on_the_stream_of_the_call(stand_in, stream):
+    s = stand_in
+    scores = s.cache.block_scores(s.batch, s.q, stream=stream)
+    assert scores.shape == (3, 2, 4) and torch.all(scores.as_subclass(torch.Tensor) == -torch.inf)
+    _all_on(s.fake.log, MAIN if stream is None else stream, "hcr_block_scores")
+    other = stream in (OTHER, 0)
+    assert [x for x in s.fake.log if x[0] == "record"] == [("record", MAIN, scores.data_ptr())] * other
+
+
+@pytest.fixture(scope="module")
+def lib():
+    ensure_built()
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+
+
+def _held_up():
+    """Work of about a tenth of a second."""
+    torch.cuda._sleep(200_000_000)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("default", [False, True])
+def test_scores_made_while_the_current_stream_is_busy(lib, default):
+    s = pu.scene(60, 2, 128, 32, [(3, 2000), (1, 900)])
+    q = pu.queries(60, 4, 8, 128)
+    cache, batch, qd = pu.dev_cache(s), pu.dev_batch(s), pu.dev_bits(q)
+    want = cache.block_scores(batch, qd)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side) if default else contextlib.nullcontext():
+        _held_up()
+        got = cache.block_scores(batch, qd, stream=0 if default else side.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.isfinite(want[0, :, :62]).all() and torch.equal(got, want)
+    ref = oracle.paged.block_scores(s.batch, oracle.bf16_bits_to_f64(s.means), 32, oracle.bf16_bits_to_f64(q))
+    assert all(np.allclose(got[n, :, :w.shape[1]].cpu(), w, atol=1e-3) for n, w in ref.items())
