@@ -6,8 +6,10 @@ and at long contexts ``block_scores``, ``block_topk`` and ``attend_blocks`` atte
 scores alone.  Argument marshalling only, as in ``hcr.py``: every step runs in the library's kernels, on torch's
 current stream of the cache's device or on ``stream`` (a raw hipStream_t).  There is no fallback.
 
-Outputs and scratch allocated here belong to torch's current stream: with another ``stream``, pass them in (or
-record them on that stream) so that torch does not reuse their memory before the kernels have run.
+Outputs and scratch made here are made on the stream of the call; with another ``stream`` than torch's current one,
+outputs are noted on that one too (``Tensor.record_stream``), so that the caller takes them there, once it has waited
+for ``stream``, as any tensor of its own.  The inputs' memory is the caller's: a tensor that may be freed before the
+kernels have run is recorded on ``stream``, as for any call of torch's.
 
 A decode step (``y``: the projections' output, [tokens][heads + 2 kv_heads][head_dim])::
 
@@ -181,10 +183,10 @@ class PagedCache:
         if rc != HCR_OK:
             raise HCRError(rc, fn.__name__)
 
-    def _new(self, stream, shape, dtype, fill=None):
+    def _new(self, stream, shape, dtype, fill=None, returned=True):
         """A new tensor of a call, filled, on the stream that the call runs on: behind that stream's earlier steps and
-        ahead of the call's kernels.  Torch's current stream, on which the caller takes it, is noted, so that its
-        memory is not used again before that stream is done with it."""
+        ahead of the call's kernels.  Torch's current stream, on which the caller takes what is returned, is noted, so
+        that the memory is not used again before that stream is done with it."""
         if stream is None or stream == torch._C._cuda_getCurrentRawStream(self.device.index):
             t = torch.empty(shape, dtype=dtype, device=self.device)
             return t if fill is None else t.fill_(fill)
@@ -193,7 +195,8 @@ class PagedCache:
             t = torch.empty(shape, dtype=dtype, device=self.device)
             if fill is not None:
                 t.fill_(fill)
-        t.record_stream(torch.cuda.current_stream(self.device))
+        if returned:
+            t.record_stream(torch.cuda.current_stream(self.device))
         return t
 
     # The checks below run at every call, ahead of kernels of a few microseconds: each reads a property once.
@@ -246,7 +249,7 @@ class PagedCache:
             rope_rows, rope_dim = rope.shape
             self._given("rope", rope, (rope_rows, rope_dim), torch.float32)
         if q_out is None:
-            q_out = torch.empty((n, heads, D), dtype=torch.bfloat16, device=self.device)
+            q_out = self._new(stream, (n, heads, D), torch.bfloat16)
         else:
             self._given("q_out", q_out, (n, heads, D), torch.bfloat16)
         self._call(self._L.hcr_cache_append, batch, stream, batch._of(n), heads, _TYPES[dtype], rq, rk, rv,
@@ -258,7 +261,7 @@ class PagedCache:
     def _attend(self, fn, batch, q, sel, scale, out, out_dtype, scratch, stream):
         n, heads = self._heads_of(q)
         if out is None:
-            out = torch.empty((n, heads, self.head_dim), dtype=out_dtype, device=self.device)
+            out = self._new(stream, (n, heads, self.head_dim), out_dtype)
         else:
             self._given("out", out, (n, heads, self.head_dim), out.dtype)
         if out.dtype not in _TYPES:
@@ -267,7 +270,7 @@ class PagedCache:
         c_batch = batch._of(n)
         need = self._L.hcr_attn_scratch_bytes(self.handle, c_batch, heads, n_sel)
         if scratch is None:
-            scratch = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
+            scratch = self._new(stream, need, torch.uint8, returned=False) if need else None
         elif not scratch.is_cuda or scratch.device != self.device or not scratch.is_contiguous():
             raise ValueError(f"scratch: a contiguous tensor on {self.device}")
         room = 0 if scratch is None else scratch.numel() * scratch.element_size()
@@ -326,7 +329,7 @@ class PagedCache:
         n = scores.shape[0]
         self._given("scores", scores, (n, self.kv_heads, scores.shape[2]), torch.float32)
         if sel is None:
-            sel = torch.empty((n, self.kv_heads, max(n_sel, 0)), dtype=torch.int32, device=self.device)
+            sel = self._new(stream, (n, self.kv_heads, max(n_sel, 0)), torch.int32)
         else:
             self._given("sel", sel, (n, self.kv_heads, n_sel), torch.int32)
         self._call(self._L.hcr_block_topk, batch, stream, batch._of(n), scores.data_ptr(), scores.shape[2],

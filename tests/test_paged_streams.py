@@ -114,6 +114,27 @@ def test_scores_are_filled_on_the_stream_of_the_call(stand_in, stream):
     assert [x for x in s.fake.log if x[0] == "record"] == [("record", MAIN, scores.data_ptr())] * other
 
 
+CALLS = {
+    "hcr_attn": lambda s, stream: s.cache.attend(s.batch, s.q, stream=stream),
+    "hcr_attn_blocks": lambda s, stream: s.cache.attend_blocks(s.batch, s.q, torch.zeros(3, 2, 4, dtype=torch.int32),
+                                                               out_dtype=torch.bfloat16, stream=stream),
+    "hcr_block_topk": lambda s, stream: s.cache.block_topk(s.batch, torch.zeros(3, 2, 4), 3, stream=stream),
+    "hcr_cache_append": lambda s, stream: s.cache.append(s.batch, s.q, s.q[:, :2], s.q[:, 2:], stream=stream),
+}
+
+
+@pytest.mark.parametrize("entry", sorted(CALLS))
+@pytest.mark.parametrize("stream", [None, MAIN, OTHER, 0])
+def test_outputs_and_scratch_belong_to_the_stream_of_the_call(stand_in, entry, stream):
+    """Scratch is let go when the call returns: its memory is the call's stream's, behind the kernels there."""
+    s = stand_in
+    out = CALLS[entry](s, stream)
+    _all_on(s.fake.log, MAIN if stream is None else stream, entry)
+    made = [at for kind, _, at in s.fake.log if kind == "make"]
+    assert len(made) == (2 if "attn" in entry else 1) and out.data_ptr() in made
+    assert [x for x in s.fake.log if x[0] == "record"] == [("record", MAIN, out.data_ptr())] * (stream in (OTHER, 0))
+
+
 @pytest.fixture(scope="module")
 def lib():
     ensure_built()
@@ -141,3 +162,48 @@ def test_scores_made_while_the_current_stream_is_busy(lib, default):
     assert torch.isfinite(want[0, :, :62]).all() and torch.equal(got, want)
     ref = oracle.paged.block_scores(s.batch, oracle.bf16_bits_to_f64(s.means), 32, oracle.bf16_bits_to_f64(q))
     assert all(np.allclose(got[n, :, :w.shape[1]].cpu(), w, atol=1e-3) for n, w in ref.items())
+
+
+@pytest.mark.gpu
+def test_scratch_let_go_by_a_call_on_another_stream(lib):
+    """The call's stream is held up; the current one makes and fills tensors of the scratch's size meanwhile."""
+    s = pu.scene(61, 2, 256, 64, [(2, 9000)])
+    cache, batch, q = pu.dev_cache(s), pu.dev_batch(s), pu.dev_bits(pu.queries(61, 2, 12, 256))
+    want = cache.attend(batch, q)
+    need = cache.scratch_bytes(batch, 2, 12)
+    assert need > 0
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            _held_up()
+        got = cache.attend(batch, q, stream=side.cuda_stream)
+        others = [torch.full((need,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(got, want)
+        del others
+
+
+@pytest.mark.gpu
+def test_outputs_of_another_stream_are_taken_on_the_current_one(lib):
+    """A window's calls on another stream, their outputs let go while the current stream still reads them."""
+    s = pu.scene(62, 2, 128, 32, [(2, 900), (1, 300)])
+    cache, batch, q = pu.dev_cache(s), pu.dev_batch(s), pu.dev_bits(pu.queries(62, 3, 8, 128))
+    want = cache.attend_blocks(batch, q, cache.block_topk(batch, cache.block_scores(batch, q), 9))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    st = side.cuda_stream
+    kept = []
+    for _ in range(3):
+        side.wait_stream(torch.cuda.current_stream())
+        sel = cache.block_topk(batch, cache.block_scores(batch, q, stream=st), 9, stream=st)
+        got = cache.attend_blocks(batch, q, sel, stream=st)
+        torch.cuda.current_stream().wait_stream(side)
+        _held_up()
+        kept.append(got.clone())  # behind the work above
+        del got, sel
+        with torch.cuda.stream(side):
+            torch.full_like(kept[0], 7.0)  # of the size that was let go
+    torch.cuda.synchronize()
+    for k in kept:
+        assert torch.equal(k, want)
