@@ -264,8 +264,9 @@ __global__ __launch_bounds__(APPEND_THREADS) void append(AppendArgs a, int kv_gr
     const int t = t0 + i;
     if (t >= seq.tokens) break;
     const int pos = seq.first + t;
-    Values x = norm_rotate<D>(values<F32>(raw[i]), a.q_norm, a, l, max(pos, 0));
-    if (pos < 0) x = Values{};
+    // a token of a padded sequence has no position: zeros, and no row of the table is read (one token a work-group's
+    // pass, so nothing diverges)
+    const Values x = pos < 0 ? Values{} : norm_rotate<D>(values<F32>(raw[i]), a.q_norm, a, l, pos);
     if (head < a.heads)
       *reinterpret_cast<uint4*>(a.q_out + ((size_t)(seq.row + t) * a.heads + head) * D + 8 * l) = round8(x);
   }

@@ -766,3 +766,22 @@ def test_the_binding_refuses():
         with pytest.raises(hcr.HCRError) as e:
             call()
         assert e.value.rc == code
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("pairs", [0, 1])
+def test_append_reads_no_row_of_a_table_without_rows(dtype, pairs):
+    """Bounds of zero positions allow a table of none: padded tokens alone, zeros (through C; the address is not read)."""
+    kv, D, page, n = 2, 128, 32, 40
+    cache = paged.PagedCache.allocate(4, kv, D, page)
+    batch = paged.Batch(torch.tensor([0, 1, 39, 40], dtype=torch.int32, device="cuda"),
+                        torch.zeros(3, dtype=torch.int32, device="cuda"),
+                        torch.zeros(3, 0, dtype=torch.int32, device="cuda"), n, 0)
+    y = torch.randn(n, 8 + 2 * kv, D, device="cuda").to(dtype)
+    table = torch.full((1, D), float("nan"), device="cuda")
+    q_out = torch.full((n, 8, D), 5.0, dtype=torch.bfloat16, device="cuda")
+    rows = [paged.hcr_rows(y[:, h:].data_ptr(), y.stride(0), D) for h in (0, 8, 8 + kv)]
+    rc = paged.lib().hcr_cache_append(cache.handle, batch._of(n), 8, paged._TYPES[dtype], *rows, None, None, 1e-6,
+                                      table.data_ptr(), 0, D, pairs, q_out.data_ptr(),
+                                      torch.cuda.current_stream().cuda_stream)
+    assert rc == hcr.HCR_OK and torch.all(q_out == 0)
