@@ -382,7 +382,9 @@ int hcr_block_topk(hcr_cache_t h, const hcr_batch* batch, const float* scores, i
   const size_t rows = (size_t)a.b.n_tokens * c.kv_heads;
   if (rows * 1024 > (size_t)THREADS_MAX) return HCR_EINVAL;
   const Span so = span(sel, rows * n_sel * 4);
-  if (overlap(so, span(scores, rows * scores_stride * 4)) || overlap_any(so, batch_spans(a.b))) return HCR_EALIAS;
+  if (overlap(so, span(scores, rows * scores_stride * 4)) || overlap_any(so, cache_spans(c)) ||
+      overlap_any(so, batch_spans(a.b)))
+    return HCR_EALIAS;
   a.scores = scores;
   a.stride = scores_stride;
   a.kv_heads = c.kv_heads;

@@ -227,6 +227,11 @@ def test_topk_rejects(lib, cache, kw, rc):
     assert topk(lib, cache, batch(), **kw) == rc
 
 
+@pytest.mark.parametrize("sel", [K, V + 4096, M + 64, K - 4, M + 1000 * 8 * 128 * 2 - 4])
+def test_topk_rejects_a_list_inside_the_cache(lib, cache, sel):
+    assert topk(lib, cache, batch(), sel=sel) == hcr.HCR_EALIAS
+
+
 def test_empty_calls_do_nothing(lib, cache):
     for kw in (dict(n_seqs=0), dict(n_tokens=0), dict(max_tokens=0)):
         b = batch(q_start=None, ctx_len=None, block_table=None, **kw)
