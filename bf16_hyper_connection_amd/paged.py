@@ -127,7 +127,8 @@ class PagedCache:
 
     ``k_pages`` BF16 [n_pages][kv_heads][head_dim / 8][page][8], ``v_pages`` BF16
     [n_pages][kv_heads][page / 8][head_dim][8], ``k_means`` BF16 [n_pages][kv_heads][head_dim] or None (no block
-    scores).  head_dim is 64, 128 or 256, page 32, 64, 128 or 256.
+    scores).  head_dim is 64, 128 or 256, page 32, 64, 128 or 256.  The pages are fixed (their contents are not): for
+    others make another cache.
     """
 
     def __init__(self, k_pages, v_pages, k_means=None):
@@ -152,7 +153,7 @@ class PagedCache:
                                         None if k_means is None else k_means.data_ptr(), n, heads, self.head_dim,
                                         page, ctypes.byref(h)), "hcr_cache_create")
         self.handle = h.value
-        self._destroy_fn, self._vp = self._L.hcr_cache_destroy, _vp
+        self._vp, self._destroy_fn = _vp, self._L.hcr_cache_destroy
 
     @classmethod
     def allocate(cls, n_pages, kv_heads, head_dim, page=64, device="cuda", means=True):
@@ -166,8 +167,16 @@ class PagedCache:
         # references bound at creation: at interpreter exit this module's globals may already be gone
         h, fn, vp = getattr(self, "handle", None), getattr(self, "_destroy_fn", None), getattr(self, "_vp", None)
         if h and fn is not None and vp is not None:
+            self.__dict__["handle"] = None
             fn(vp(h))
-            self.handle = None
+
+    def __setattr__(self, name, value):
+        if "_destroy_fn" in self.__dict__:
+            raise AttributeError(f"{name}: a cache's pages and geometry are fixed")
+        super().__setattr__(name, value)
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{name}: a cache's pages and geometry are fixed")
 
     def _call(self, fn, batch, stream, *args):
         """The entry point on the cache's device, its stream last."""

@@ -11,6 +11,7 @@ import re
 import shutil
 import subprocess
 import sys
+import types
 
 import pytest
 import torch
@@ -264,6 +265,27 @@ def test_binding_rejects_what_it_can_see():
         paged.Batch(i, i, i, 1, 1)
     with pytest.raises(ValueError):
         paged.Batch(i.long(), i, i, 1, 1)
+
+
+def _binding_tensor(at, *shape, dtype=torch.bfloat16):
+    """What the binding asks of a device tensor; the address is made up."""
+    return types.SimpleNamespace(dtype=dtype, shape=torch.Size(shape), is_cuda=True, device=torch.device("cuda:0"),
+                                 is_contiguous=lambda: True, dim=lambda: len(shape), data_ptr=lambda: at)
+
+
+def test_a_binding_cache_keeps_its_pages():
+    """The handle holds the pages' addresses: another tensor in their place would leave it with memory let go."""
+    ensure_built()
+    k = _binding_tensor(K, 10, 2, 8, 32, 8)
+    cache = paged.PagedCache(k, _binding_tensor(V, 10, 2, 4, 64, 8), _binding_tensor(M, 10, 2, 64))
+    handle = cache.handle
+    for name in ("k_pages", "v_pages", "k_means", "handle", "page", "device", "more"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, None)
+    for name in ("k_pages", "v_pages", "k_means", "handle"):
+        with pytest.raises(AttributeError):
+            delattr(cache, name)
+    assert cache.k_pages is k and cache.handle == handle
 
 
 @pytest.fixture(scope="module")
