@@ -112,6 +112,9 @@ class Batch:
             raise AttributeError(f"{name}: a batch's tensors and bounds are fixed")
         super().__setattr__(name, value)
 
+    def __delattr__(self, name):
+        raise AttributeError(f"{name}: a batch's tensors and bounds are fixed")
+
     def _of(self, n_tokens):
         """The C struct for calls of n_tokens rows (kept: a decode loop calls with the same number again)."""
         s = self._by_rows.get(n_tokens)

@@ -288,6 +288,23 @@ def test_a_binding_cache_keeps_its_pages():
     assert cache.k_pages is k and cache.handle == handle
 
 
+def _binding_batch(**bounds):
+    i32 = torch.int32
+    return paged.Batch(_binding_tensor(STARTS, 5, dtype=i32), _binding_tensor(LENS, 4, dtype=i32),
+                       _binding_tensor(TABLE, 4, 100, dtype=i32), **{"max_tokens": 3, "max_ctx": 5000, **bounds})
+
+
+def test_a_binding_batch_keeps_its_tensors():
+    """Calls keep the addresses: a tensor deleted from the batch would be let go under them."""
+    b = _binding_batch()
+    b._of(8)
+    for name in ("q_start", "ctx_len", "block_table", "max_ctx", "_by_rows"):
+        with pytest.raises(AttributeError):
+            delattr(b, name)
+    with pytest.raises(AttributeError):
+        b.max_ctx = 7
+
+
 @pytest.fixture(scope="module")
 def sanitized(tmp_path_factory):
     cxx = next((c for c in ("g++", "c++") if shutil.which(c)), None)
