@@ -100,8 +100,8 @@ class Batch:
             raise ValueError(f"q_start [{n + 1}] and block_table [{n}][entries] for ctx_len [{n}]")
         if q_start.device != ctx_len.device or block_table.device != ctx_len.device:
             raise ValueError("q_start, ctx_len and block_table on one device")
-        if max_tokens < 0 or max_ctx < 0:
-            raise ValueError("max_tokens and max_ctx: not negative")
+        if not 0 <= max_tokens < 1 << 31 or not 0 <= max_ctx < 1 << 31:  # ctypes would cut them to 32 bits
+            raise ValueError("max_tokens and max_ctx: not negative, under 2^31")
         self.q_start, self.ctx_len, self.block_table = q_start, ctx_len, block_table
         self.device, self.n_seqs = ctx_len.device, n
         self.max_tokens, self.max_ctx = int(max_tokens), int(max_ctx)
@@ -338,6 +338,8 @@ class PagedCache:
         """
         if scores.dim() != 3:
             raise ValueError(f"scores: float32 [n_tokens][{self.kv_heads}][pages]")
+        if not -1 << 31 <= min(n_sel, n_first, n_last) <= max(n_sel, n_first, n_last) < 1 << 31:  # as a batch's bounds
+            raise ValueError("n_sel, n_first and n_last: whole numbers of 32 bits")
         n = scores.shape[0]
         self._given("scores", scores, (n, self.kv_heads, scores.shape[2]), torch.float32)
         if sel is None:

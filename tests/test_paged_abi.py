@@ -305,6 +305,26 @@ def test_a_binding_batch_keeps_its_tensors():
         b.max_ctx = 7
 
 
+@pytest.mark.parametrize("bounds", [dict(max_ctx=2 ** 31), dict(max_ctx=2 ** 32 + 5000), dict(max_tokens=2 ** 32 + 3),
+                                    dict(max_tokens=2 ** 63), dict(max_ctx=-1)])
+def test_a_binding_batch_refuses_bounds_past_32_bits(bounds):
+    """ctypes would cut them: 2^32 + 5,000 positions to 5,000."""
+    with pytest.raises(ValueError):
+        _binding_batch(**bounds)
+    assert _binding_batch(max_ctx=2 ** 31 - 1).max_ctx == 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("counts", [dict(n_first=2 ** 32 + 1), dict(n_last=2 ** 32 + 2), dict(n_first=-2 ** 32),
+                                    dict(n_last=2 ** 31)])
+def test_binding_topk_refuses_counts_past_32_bits(counts):
+    ensure_built()
+    cache = paged.PagedCache(_binding_tensor(K, 10, 2, 8, 32, 8), _binding_tensor(V, 10, 2, 4, 64, 8))
+    scores = _binding_tensor(S, 8, 2, 200, dtype=torch.float32)
+    sel = _binding_tensor(SEL, 8, 2, 9, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        cache.block_topk(_binding_batch(), scores, 9, **counts, sel=sel)
+
+
 @pytest.fixture(scope="module")
 def sanitized(tmp_path_factory):
     cxx = next((c for c in ("g++", "c++") if shutil.which(c)), None)
