@@ -120,6 +120,60 @@ def test_a_maximum_subtracted_from_the_small_part_fails_the_bound(D, scale, arou
         assert np.all(off <= bound * (w @ np.abs(v))) == fits
 
 
+def _pairs(seed, D, group, count):
+    """``count`` sequences of two positions, the first one's value zero: each row's output is the second's value times
+    its probability, one in a row's sum of two.  Products are eighths, within 16 of each other."""
+    g = gen.rng(111, seed)
+    s = pu.scene(seed, 1, D, 32, [(1, 2)] * count)
+    keys = np.broadcast_to(g.integers(-9, 10, D), (s.k_bits.shape[0], 1, 32, D)).astype(np.float32).copy()
+    keys[:, :, 1, :8] = keys[:, :, 0, :8] + 1
+    _set_keys(s, keys)
+    s.v_bits[:, :, 0, :, 0] = 0
+    q = g.integers(-16, 17, (count, group, D)).astype(np.float32) / 8
+    return s, q
+
+
+def _pair_room(scale):
+    # sum: one addition; product: two of three parts added to the first, one whole step each
+    return (4 * np.log(2) * (16 * abs(scale) * np.log2(np.e) + 1) + 4 + 1 + 4 + 3) * HALF
+
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("group", [1, 16, 64])
+def test_float_outputs_take_whole_probabilities(lib, D, group):
+    """Closer than two BF16 parts of a probability come (2^-18)."""
+    scale = 0.0931
+    s, q = _pairs(2, D, group, 40)
+    keys, values = pu.decoded(s)
+    want = oracle.paged.attend(s.batch, keys, values, q, scale)
+    out = pu.dev_cache(s).attend(pu.dev_batch(s), pu.dev_bits(pu.bf16(q)), scale=scale).double().cpu().numpy()
+    for n, w in want.items():
+        assert np.all(np.abs(out[n] - w) <= _pair_room(scale) * np.abs(w)), f"row {n}"
+
+
+def test_two_parts_of_a_probability_fail_the_bound():
+    scale = 0.0931
+    s, q = _pairs(2, 128, 64, 40)
+    keys, _ = pu.decoded(s)
+    hi, lo = _parts(scale)
+    x = np.stack([q[b] @ keys[s.table[b, 0], 0, :2].T for b in range(40)]).astype(np.float32)  # [40][64][2]
+    top = (x * hi).max(-1, keepdims=True)
+    p = np.exp2(_fma(x, lo, _fma(x, hi, -top)).astype(np.float64)).astype(np.float32)
+    want = 1 / (1 + np.exp(scale * (x[..., 0] - x[..., 1]).astype(np.float64)))
+
+    def bf16(a):
+        return oracle.bf16_bits_to_f64(pu.bf16(a)).astype(np.float32)
+    first = bf16(p)
+    second = bf16(p - first)
+    third = bf16(p - first - second)
+    assert np.array_equal(first.astype(np.float64) + second + third, p)
+    total = p.sum(-1, dtype=np.float64)
+    for parts, fits in ((first.astype(np.float64) + second + third, True), (first.astype(np.float64) + second, False)):
+        off = np.abs(parts[..., 1] / total - want)
+        assert np.all(off <= _pair_room(scale) * want) == fits
+
+
 @gpu
 @pytest.mark.parametrize("head_dim,page,kv,group", [(128, 64, 2, 4), (64, 32, 1, 24), (256, 64, 1, 6), (128, 32, 2, 1),
                                                     (64, 64, 2, 16)])
