@@ -140,3 +140,16 @@ extern "C" const char* paged_index_checks(void) {
   if (const char* e = check_plans()) return e;
   return "ok";
 }
+
+// Pages (entries of a table's row, or of a list) that the longest run of an attention call spans: `all` tiles of the
+// sequences together, `longest` of one (dense calls).
+extern "C" int paged_run_pages(int D, int kv, int page, int heads, int n_seqs, int n_tokens, int max_tokens, int max_ctx,
+                               int n_sel, int all, int longest) {
+  const CacheArgs c{nullptr, nullptr, nullptr, 10, kv, D, log2_of(page)};
+  const BatchArgs b{nullptr, nullptr, nullptr, ceil_div(max_ctx, page), n_seqs, n_tokens, max_tokens, max_ctx};
+  const AttnPlan p = attn_plan(c, b, heads, n_sel);
+  const int tiles = n_sel ? n_sel << (c.shift - TILE_SHIFT) : longest;
+  int run = p.whole ? tiles : n_sel ? run_tiles_listed(p, tiles, n_tokens) : run_tiles(p, all);
+  if (run > tiles) run = tiles;
+  return run >> (c.shift - TILE_SHIFT);
+}

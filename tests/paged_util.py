@@ -127,3 +127,13 @@ def check_rows(out, want, tol, label):
             norm = float(np.linalg.norm(w[hd]))
             off = float(np.linalg.norm(got[n, hd] - w[hd]))
             assert off <= tol * norm, f"{label}: row {n} head {hd}: off by {off:.3e}, allowed {tol * norm:.3e}"
+
+
+# Attention whose work-groups walk more pages than a wave has lanes (they load 64 entries of a table's row or a list at
+# a time): name -> (kv heads, heads, head_dim, page, windows, entries of a list or 0)
+LONG_RUNS = {
+    "a sequence whole": (8, 16, 64, 32, [(1, 4000)] + [(1, 7 + 31 * (i % 9)) for i in range(63)], 0),
+    "a sequence cut": (16, 16, 64, 32, [(1, 70), (1, 40000)], 0),
+    "lists whole": (8, 8, 64, 32, [(4, 4190 + 3 * i) for i in range(8)], 130),
+    "lists cut": (16, 16, 64, 32, [(1, 40000)], 1200),
+}

@@ -366,3 +366,18 @@ def test_index_arithmetic_stays_in_bounds(sanitized):
                                         "L.paged_index_checks.restype = ctypes.c_char_p\n"
                                         "print(L.paged_index_checks().decode())"])
     assert out.strip().endswith("ok"), out
+
+
+@pytest.mark.skipif(bool(SANITIZED), reason="the parent's")
+def test_index_long_runs_pass_a_waves_lanes(sanitized):
+    """The GPU tests' scenes of long runs do what they are for under the present plan."""
+    from tests import paged_util as pu
+    calls = []
+    for name, (kv, heads, D, page, windows, n_sel) in sorted(pu.LONG_RUNS.items()):
+        tiles = [max(-(-c // 32), 1) for _, c in windows]
+        calls.append((D, kv, page, heads, len(windows), sum(t for t, _ in windows), max(t for t, _ in windows),
+                      max(c for _, c in windows), n_sel, sum(tiles), max(tiles)))
+    out = _under_asan(sanitized, ["-c", "import ctypes, os; L = ctypes.CDLL(os.environ['PAGED_ABI_LIB'])\n"
+                                        f"print([L.paged_run_pages(*c) for c in {calls}])"])
+    runs = [int(x) for x in out.strip().strip("[]").split(",")]
+    assert len(runs) == len(calls) and all(r > 64 for r in runs), runs
