@@ -1,5 +1,5 @@
 """The paged cache on the GPU at sizes that take its kernels' longer ways: runs over more pages than a wave holds
-entries of, page scores two tiles of pages a wave."""
+entries of, page scores two tiles of pages a wave, prompts of hundreds of tokens."""
 
 import numpy as np
 import pytest
@@ -88,3 +88,12 @@ def test_block_scores_of_many_pages(head_dim, group):
         assert np.all(np.abs(got[r, :, :m][fine] - w[fine]) <= room), f"row {r}"
         assert np.all(got[r, :, m:] == 9.0), f"row {r}: entries from the token's own page on"
     assert np.all(got[n] == 9.0)
+
+
+@pytest.mark.parametrize("head_dim,kv,group,windows", [
+    (128, 1, 4, [(700, 1033)]), (256, 1, 3, [(260, 260), (1, 77), (130, 900)]), (64, 2, 5, [(515, 600), (33, 33)]),
+    (128, 2, 1, [(1025, 1500)]), (256, 1, 16, [(97, 300)])])
+def test_attend_over_prompts(head_dim, kv, group, windows):
+    """Windows of hundreds of tokens, behind earlier ones or from the first position on."""
+    s = pu.scene(72, kv, head_dim, 64, windows)
+    _attend(s, kv * group, 72)
