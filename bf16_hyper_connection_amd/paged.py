@@ -115,6 +115,9 @@ class Batch:
     def __delattr__(self, name):
         raise AttributeError(f"{name}: a batch's tensors and bounds are fixed")
 
+    def __reduce__(self):  # a copy keeps structs of its own tensors
+        return type(self), (self.q_start, self.ctx_len, self.block_table, self.max_tokens, self.max_ctx)
+
     def _of(self, n_tokens):
         """The C struct for calls of n_tokens rows (kept: a decode loop calls with the same number again)."""
         s = self._by_rows.get(n_tokens)
@@ -180,6 +183,9 @@ class PagedCache:
 
     def __delattr__(self, name):
         raise AttributeError(f"{name}: a cache's pages and geometry are fixed")
+
+    def __reduce__(self):  # a copy makes a handle of its own
+        return type(self), (self.k_pages, self.v_pages, self.k_means)
 
     def _call(self, fn, batch, stream, *args):
         """The entry point on the cache's device, its stream last."""

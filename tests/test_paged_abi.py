@@ -325,6 +325,23 @@ def test_binding_topk_refuses_counts_past_32_bits(counts):
         cache.block_topk(_binding_batch(), scores, 9, **counts, sel=sel)
 
 
+def test_a_binding_copy_has_a_handle_of_its_own():
+    """Two caches that destroy one handle would free it twice; a batch's copy holds its own tensors' addresses."""
+    ensure_built()
+    code = ("import copy, sys\nimport torch\nsys.path.insert(0, '.')\nfrom bf16_hyper_connection_amd import paged\n"
+            "from tests.test_paged_abi import K, M, V, _binding_batch, _binding_tensor\n"
+            "c = paged.PagedCache(_binding_tensor(K, 10, 2, 8, 32, 8), _binding_tensor(V, 10, 2, 4, 64, 8),\n"
+            "                     _binding_tensor(M, 10, 2, 64))\n"
+            "d = copy.copy(c)\n"
+            "assert d.handle != c.handle and d.k_pages is c.k_pages and d.k_means is c.k_means and d.page == 32\n"
+            "del c, d\n"
+            "b = _binding_batch()\nb._of(8)\nx = copy.copy(b)\n"
+            "assert x.q_start is b.q_start and x.max_ctx == b.max_ctx and not x._by_rows\n"
+            "print('fine', flush=True)\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
 @pytest.fixture(scope="module")
 def sanitized(tmp_path_factory):
     cxx = next((c for c in ("g++", "c++") if shutil.which(c)), None)
