@@ -205,10 +205,15 @@ class PagedCache:
         """A new tensor of a call, filled, on the stream that the call runs on: behind that stream's earlier steps and
         ahead of the call's kernels.  Torch's current stream, on which the caller takes what is returned, is noted, so
         that the memory is not used again before that stream is done with it."""
-        if stream is None or stream == torch._C._cuda_getCurrentRawStream(self.device.index):
+        own = None
+        if stream is not None:
+            raw = getattr(stream, "value", stream) or 0  # as a number, or as ctypes holds it
+            if raw != torch._C._cuda_getCurrentRawStream(self.device.index):
+                own = torch.cuda.ExternalStream(raw, device=self.device) if raw else \
+                    torch.cuda.default_stream(self.device)
+        if own is None:
             t = torch.empty(shape, dtype=dtype, device=self.device)
             return t if fill is None else t.fill_(fill)
-        own = torch.cuda.ExternalStream(stream, device=self.device) if stream else torch.cuda.default_stream(self.device)
         with torch.cuda.stream(own):
             t = torch.empty(shape, dtype=dtype, device=self.device)
             if fill is not None:

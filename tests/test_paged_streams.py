@@ -4,6 +4,7 @@ On the CPU the binding runs against stand-ins for torch's streams and allocation
 which stream each step is queued; on the GPU the other stream is held up and must neither meet nor miss anything."""
 
 import contextlib
+import ctypes
 import types
 
 import numpy as np
@@ -135,6 +136,16 @@ def test_outputs_and_scratch_belong_to_the_stream_of_the_call(stand_in, entry, s
     assert [x for x in s.fake.log if x[0] == "record"] == [("record", MAIN, out.data_ptr())] * (stream in (OTHER, 0))
 
 
+@pytest.mark.parametrize("stream", [MAIN, OTHER, 0])
+def test_a_stream_as_ctypes_holds_it(stand_in, stream):
+    s = stand_in
+    held = ctypes.c_void_p(stream)
+    out = s.cache.attend(s.batch, s.q, stream=held)
+    assert [x[1] for x in s.fake.log if x[0] == "make"] == [stream, stream]
+    assert [x for x in s.fake.log if x[0] == "hcr_attn"][0][1] is held
+    assert ("record", MAIN, out.data_ptr()) in s.fake.log or stream == MAIN
+
+
 @pytest.fixture(scope="module")
 def lib():
     ensure_built()
@@ -207,3 +218,32 @@ def test_outputs_of_another_stream_are_taken_on_the_current_one(lib):
     torch.cuda.synchronize()
     for k in kept:
         assert torch.equal(k, want)
+
+
+@pytest.mark.gpu
+def test_a_captured_fork_onto_another_stream(lib):
+    """Calls on a stream that a capture forked to, their outputs and scratch made there: replays equal eager calls."""
+    s = pu.scene(63, 2, 128, 32, [(2, 5000), (1, 300)])
+    cache, batch = pu.dev_cache(s), pu.dev_batch(s)
+    q = pu.dev_bits(pu.queries(63, 3, 8, 128))
+    assert cache.scratch_bytes(batch, 3, 8) > 0
+    main, fork = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def step(stream):
+        sel = cache.block_topk(batch, cache.block_scores(batch, q, stream=stream), 9, stream=stream)
+        return cache.attend(batch, q, stream=stream), cache.attend_blocks(batch, q, sel, stream=stream)
+    graph = torch.cuda.CUDAGraph()
+    main.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(main), torch.cuda.graph(graph, stream=main):
+        fork.wait_stream(main)
+        dense = cache.attend(batch, q)
+        outs = step(fork.cuda_stream)
+        main.wait_stream(fork)
+    torch.cuda.current_stream().wait_stream(main)
+    for i in range(4):
+        q.copy_(pu.dev_bits(pu.queries(64 + i, 3, 8, 128)))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step(None)
+        torch.cuda.synchronize()
+        assert torch.equal(dense, want[0]) and all(torch.equal(a, b) for a, b in zip(outs, want)), f"replay {i}"
