@@ -3,7 +3,7 @@
 // for every page of a sequence, or for the pages listed per token and kv head.
 //
 // A unit is one kv head of one sequence: its rows are the T x G (tokens x heads of the group) query rows, which
-// all read the same keys and values.  A wave takes tiles of 32 positions and holds 16, 32 or 64 of the rows:
+// all read the same keys and values.  A wave takes tiles of 32 positions and holds 16 or 32 of the rows:
 //   S^T = K Q^T : A = 16 keys (two row tiles per 32 positions), B = 16 query rows; S^T arrives with one query row
 //                 per lane column, so a row's maximum and sum run over a lane's 8 values and the 4 lane rows.
 //   O^T += V^T P^T : the K index of this product is a position.  Row r of key tile t is position
@@ -12,8 +12,8 @@
 //                 bytes, its A operand as loaded.  Nothing goes through LDS inside the loop.
 // Probabilities are powers of two against a running maximum that moves only when a tile passes it by 2^8 (sums
 // and products are FP32, so the offset costs no precision), split into BF16 parts: two (2^-17) for BF16 outputs,
-// three (the whole FP32 value) for float ones, where two would be the largest error of all (1.1e-6 of the result's
-// norm instead of 1.5e-7; the third costs matrix products that the loop has time for).
+// three (the whole FP32 value) for float ones, where two would be the largest error of all (2^-18 of a probability, up
+// to 3.8e-6; the third costs matrix products that the loop has time for).
 //
 // Work: the tiles of all sequences, one behind the other, are cut into equal runs, one for each work-group that the
 // chip holds at once (AttnPlan), so that unlike lengths and loose bounds cost nothing; a run goes from one sequence
@@ -24,8 +24,8 @@
 // keeps that to sequences of 4,096).
 //
 // Bound by the bytes of keys and values.  Measured on MI355X (graphs of calls, inputs rotated): one sequence of
-// 420,000 positions, 48 heads of 256 over 8, 2 tokens: 530 us, 6.5 TB/s (a 4 GiB device copy moves 4.8); 64 sequences
-// of 1,000 to 8,192, 32 heads of 128 over 8: 195 us, 6.2 TB/s.  36 rows of 4 sequences of up to 9,001: 51 us, 3.3 TB/s:
+// 420,000 positions, 48 heads of 256 over 8, 2 tokens: 505 us, 6.8 TB/s (a 4 GiB device copy moves 4.8); 64 sequences
+// of 1,000 to 8,192, 32 heads of 128 over 8: 194 us, 6.2 TB/s.  36 rows of 4 sequences of up to 9,001: 51 us, 3.3 TB/s:
 // a work-group has 10 tiles behind 6 us of first loads, three row waves share each of them, so that a CU has 64 KB on
 // their way where it has 256 KB with one row wave, and the second launch takes 7.
 

@@ -76,8 +76,8 @@ HCR_HD int ceil_div(int a, int b) { return (a + b - 1) / b; }
 // pages), tiles of 32 positions, and splits of the length into chunks of tiles
 constexpr int TILE = 32;
 constexpr int TILE_SHIFT = 5;
-// Waves of a work-group at most: what its registers leave room for on a CU (one 16-row tile of D = 256 takes 247
-// of 512 registers of a lane, two 328; of D = 128 151 and 202; of D = 64 104).
+// Waves of a work-group at most: what its registers leave room for on a CU (one 16-row tile of D = 256 takes 249
+// of 512 registers of a lane, two 334; of D = 128 153 and 207; of D = 64 105).
 constexpr int attn_waves(int D, int q_tiles) { return D == 64 ? 16 : D == 256 && q_tiles > 1 ? 4 : 8; }
 
 // How a call is cut.  Its sets of rows (a sequence's window; one token for listed pages) have their tiles one set

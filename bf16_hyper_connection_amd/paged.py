@@ -327,7 +327,8 @@ class PagedCache:
     def block_scores(self, batch, q, scores=None, stream=None):
         """Scores of the complete pages before each token's own: float32 [n_tokens][kv_heads][pages].
 
-        Entries from the token's own page on are left as they were (in a new tensor: -inf).
+        Entries from the token's own page on are left as they were (in a new tensor: -inf).  ``scores`` begins at a
+        whole 16 bytes.
         """
         n, heads = self._heads_of(q)
         if scores is None:

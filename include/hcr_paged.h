@@ -135,9 +135,9 @@ int hcr_attn_blocks(hcr_cache_t c, const hcr_batch* batch, int heads, double sca
                     int n_sel, int out_type, void* out, void* scratch, size_t scratch_bytes, void* stream);
 
 /* Scores of the complete pages before each token's own (j < p / page) from their mean
- * keys: scores[n][h][j], float [n_tokens][kv_heads][scores_stride], scores_stride >=
- * (max_ctx - 1) / page; the other entries are left as they were.  A score is NaN where
- * one of its products is, -inf where the page is none.
+ * keys: scores[n][h][j], float [n_tokens][kv_heads][scores_stride], 16-byte aligned,
+ * scores_stride >= (max_ctx - 1) / page; the other entries are left as they were.  A
+ * score is NaN where one of its products is, -inf where the page is none.
  * Errors: HCR_EINVAL (a cache without means too), HCR_EALIGN, HCR_EALIAS, HCR_EHIP. */
 int hcr_block_scores(hcr_cache_t c, const hcr_batch* batch, int heads, const void* q, float* scores, int scores_stride,
                      void* stream);
