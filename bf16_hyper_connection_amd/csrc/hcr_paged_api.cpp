@@ -373,7 +373,9 @@ int hcr_block_topk(hcr_cache_t h, const hcr_batch* batch, const float* scores, i
   const int rc = check_bounds(c, batch, c.kv_heads, &a.b);
   if (rc < 0) return rc;
   const int pages = a.b.max_ctx > 0 ? (a.b.max_ctx - 1) >> c.shift : 0;
-  if (n_sel < 1 || n_first < 0 || n_last < 1 || n_first > n_sel || n_last > n_sel - n_first) return HCR_EINVAL;
+  // n_sel: the kernel's lanes step through a list in 32 bits
+  if (n_sel < 1 || n_sel > ROWS_MAX || n_first < 0 || n_last < 1 || n_first > n_sel || n_last > n_sel - n_first)
+    return HCR_EINVAL;
   if (scores_stride < 0 || scores_stride < pages) return HCR_EINVAL;
   if (rc == 1) return HCR_OK;
   if (!sel || (!scores && pages)) return HCR_EINVAL;

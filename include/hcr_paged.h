@@ -146,7 +146,8 @@ int hcr_block_scores(hcr_cache_t c, const hcr_batch* batch, int heads, const voi
  * last n_last (the token's own among them) and, up to n_sel in all, those of the
  * highest scores between (level scores: the lowest index first; NaN ranks as -inf), as
  * ascending indices in sel [n_tokens][kv_heads][n_sel], -1 behind them.  n_first >= 0,
- * n_last >= 1, n_first + n_last <= n_sel.  scores as hcr_block_scores leaves them.
+ * n_last >= 1, n_first + n_last <= n_sel <= 2^30.  scores as hcr_block_scores leaves
+ * them.
  * Errors: HCR_EINVAL, HCR_EALIGN, HCR_EALIAS, HCR_EHIP. */
 int hcr_block_topk(hcr_cache_t c, const hcr_batch* batch, const float* scores, int scores_stride, int n_sel,
                    int n_first, int n_last, int* sel, void* stream);

@@ -233,6 +233,16 @@ def test_topk_rejects_a_list_inside_the_cache(lib, cache, sel):
     assert topk(lib, cache, batch(), sel=sel) == hcr.HCR_EALIAS
 
 
+@pytest.mark.parametrize("n_sel", [(1 << 30) + 1, (1 << 31) - 1024, (1 << 31) - 1])
+def test_topk_rejects_lists_past_its_counters(lib, n_sel):
+    """A lane steps through a list in 32 bits, 1,024 entries at a time."""
+    rc, h = create(lib, kv=1)
+    b = batch(n_seqs=1, n_tokens=1, max_tokens=1)
+    assert rc == hcr.HCR_OK
+    assert topk(lib, h, b, n_sel=n_sel, sel=200 * GB) == hcr.HCR_EINVAL
+    lib.hcr_cache_destroy(h)
+
+
 def test_empty_calls_do_nothing(lib, cache):
     for kw in (dict(n_seqs=0), dict(n_tokens=0), dict(max_tokens=0)):
         b = batch(q_start=None, ctx_len=None, block_table=None, **kw)
