@@ -176,13 +176,19 @@ class PagedCache:
             self.__dict__["handle"] = None
             fn(vp(h))
 
+    # what the handle was made of, and what it is destroyed with
+    _FIXED = frozenset(("k_pages", "v_pages", "k_means", "n_pages", "kv_heads", "page", "head_dim", "device", "handle",
+                        "_L", "_vp", "_destroy_fn"))
+
     def __setattr__(self, name, value):
-        if "_destroy_fn" in self.__dict__:
+        if name in self._FIXED and "_destroy_fn" in self.__dict__:
             raise AttributeError(f"{name}: a cache's pages and geometry are fixed")
         super().__setattr__(name, value)
 
     def __delattr__(self, name):
-        raise AttributeError(f"{name}: a cache's pages and geometry are fixed")
+        if name in self._FIXED:
+            raise AttributeError(f"{name}: a cache's pages and geometry are fixed")
+        super().__delattr__(name)
 
     def __reduce__(self):  # a copy makes a handle of its own
         return type(self), (self.k_pages, self.v_pages, self.k_means)

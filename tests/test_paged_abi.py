@@ -289,9 +289,11 @@ def test_a_binding_cache_keeps_its_pages():
     k = _binding_tensor(K, 10, 2, 8, 32, 8)
     cache = paged.PagedCache(k, _binding_tensor(V, 10, 2, 4, 64, 8), _binding_tensor(M, 10, 2, 64))
     handle = cache.handle
-    for name in ("k_pages", "v_pages", "k_means", "handle", "page", "device", "more"):
+    for name in ("k_pages", "v_pages", "k_means", "handle", "page", "device", "kv_heads", "head_dim", "n_pages"):
         with pytest.raises(AttributeError):
             setattr(cache, name, None)
+    cache.layer = 3  # an attribute of the caller's own
+    del cache.layer
     for name in ("k_pages", "v_pages", "k_means", "handle"):
         with pytest.raises(AttributeError):
             delattr(cache, name)
@@ -350,6 +352,17 @@ def test_a_binding_copy_has_a_handle_of_its_own():
             "print('fine', flush=True)\n")
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
+def test_a_binding_cache_may_be_derived_from():
+    ensure_built()
+
+    class Layer(paged.PagedCache):
+        def __init__(self, number, *pages):
+            super().__init__(*pages)
+            self.number = number
+    layer = Layer(7, _binding_tensor(K, 10, 2, 8, 32, 8), _binding_tensor(V, 10, 2, 4, 64, 8))
+    assert layer.number == 7 and layer.k_means is None
 
 
 @pytest.fixture(scope="module")
