@@ -8,9 +8,9 @@
 // are staged in LDS, 64 slots at a time, and written in the page's order, so that a prompt's pages go out as whole
 // lines (a lane writes 8 dimensions of a slot, or 8 slots of a dimension).  The others take query heads.  Loads of
 // several tokens go out together.  Nothing bounds it but the bytes of the rows, and for a few tokens the launch
-// itself.  Measured on MI355X (graphs of calls, inputs rotated): 4,352 tokens of 32 + 16 heads of 128, BF16, 26.1 us,
-// 4.2 TB/s (by a first measurement 27.4, 28.5 with loads that stay in the caches; 40.7 with 4 dimensions a lane and one token's load at a time);
-// one token of 48 + 16 heads of 256 3.8 us.
+// itself.  Measured on MI355X: 4,352 tokens of 32 + 16 heads of 128, BF16, 26.1 us, 4.2 TB/s (in graphs of calls, inputs
+// rotated, 27.4 against 28.5 with loads that stay in the caches, 28.3 against 40.7 with 4 dimensions a lane and one
+// token's load at a time); one token of 48 + 16 heads of 256 3.8 us.
 
 #include <hip/hip_runtime.h>
 

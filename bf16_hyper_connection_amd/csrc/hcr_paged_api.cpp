@@ -165,8 +165,8 @@ int attn(hcr_cache_t h, const hcr_batch* batch, int heads, double scale, const v
 //              D = 256 up to 32 rows, a wave a SIMD: 24 rows of 4 sequences of 90,010 260 against 302, of 64 of
 //              4,000 197 against 257.  49 to 64 rows too, in two row waves, where there are tiles for them: 64 rows of
 //              16,400 50 against 58, 4 sequences of 60,000 233 against 258, but 32 of 700 71 against 61, one of 9,001 36
-//              against 35 (36 rows level, 54 against 52 at 9,001).  Not D = 64 (92 against 90), nor three for D = 256 (36 rows 283 against 303,
-//              but 57 against 51 at 9,001: the accumulators no longer fit beside the operands)
+//              against 35 (36 rows level, 54 against 52 at 9,001).  Not D = 64 (92 against 90), nor three for D = 256
+//              (36 rows 283 against 303, but 57 against 51 at 9,001: the accumulators no longer fit beside the operands)
 //   rows       several row waves, D = 256: one group, as many work-groups as fit a CU (36 rows: 314 against 432
 //              with two groups), four row waves at most (96 rows: 484 against 544 with six in one work-group)
 //   whole      a work-group a set and no join, where the chip is full of them or they end soon.  512 work-groups,
