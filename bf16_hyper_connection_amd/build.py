@@ -1,11 +1,13 @@
 """Build libhcr.so (the HIP kernels and the C ABI) in-tree for gfx950 with hipcc, and the plain C
 caller of the ABI that the tests run (tests/c_caller/hcr_read_file, built with the host C compiler)."""
 
+import concurrent.futures
 import hashlib
 import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,9 +21,12 @@ C_FLAGS = ["-std=c11", "-O2", "-Wall", "-Wextra", "-Wpedantic", "-Werror",
            "-D__HIP_PLATFORM_AMD__"]  # selects the AMD half of the HIP runtime header
 
 SOURCES = ["hcr_kernels.hip", "hcr_matvec.hip", "hcr_api.cpp"]
-# the paged cache (include/hcr_paged.h), in the same library
-PAGED_SOURCES = ["hcr_append.hip", "hcr_attn.hip", "hcr_blocks.hip", "hcr_paged_api.cpp"]
-PAGED_HEADERS = ["hcr_paged_device.h", "hcr_paged_layout.h"]
+# the paged cache (include/hcr_paged.h, hcr_paged_q8.h), in the same library
+PAGED_SOURCES = ["hcr_attn_int8.hip", "hcr_attn_e4m3.hip", "hcr_attn.hip", "hcr_attn_window.hip", "hcr_append.hip",
+                 "hcr_append_q8.hip", "hcr_cache_read.hip", "hcr_blocks.hip", "hcr_paged_api.cpp",
+                 "hcr_paged_q8_api.cpp"]
+PAGED_HEADERS = ["hcr_paged_device.h", "hcr_paged_layout.h", "hcr_attn_device.h", "hcr_append_device.h",
+                 "hcr_paged_check.h"]
 # the calibration kernels (include/hcr_calib.h): a library of their own, measurement only
 CALIB_LIB = os.path.join(PKG, "libhcr_calib.so")
 CALIB_SOURCES = ["hcr_calib.hip"]
@@ -113,26 +118,39 @@ def build_c_caller(verbose=False):
     return C_CALLER
 
 
-def _hipcc_shared(path, sources, verbose):
-    tmp = path + ".tmp%d" % os.getpid()
-    cmd = [hipcc()] + HIPCC_FLAGS + ["-I", os.path.join(ROOT, "include"), "-I", CSRC, "-o", tmp] + \
-          [os.path.join(CSRC, s) for s in sources]
+def _run_hipcc(args, verbose):
+    cmd = [hipcc()] + args
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     out = "\n".join(line for line in (res.stdout + res.stderr).splitlines()
-                    if "packed-fp32-ops" not in line)
+                    if "packed-fp32-ops" not in line and "argument unused during compilation: '-shared'" not in line)
     if res.returncode != 0:
         raise RuntimeError("hipcc failed:\n" + out)
     if verbose and out.strip():
         print(out, flush=True)
+
+
+def _hipcc_shared(path, sources, verbose):
+    """Compile every source to an object, a few at a time, and link them."""
+    tmp = path + ".tmp%d" % os.getpid()
+    with tempfile.TemporaryDirectory() as d:
+        objects = [os.path.join(d, s + ".o") for s in sources]
+
+        def compile_one(source, obj):
+            _run_hipcc(HIPCC_FLAGS + ["-I", os.path.join(ROOT, "include"), "-I", CSRC, "-c",
+                                      os.path.join(CSRC, source), "-o", obj], verbose)
+
+        with concurrent.futures.ThreadPoolExecutor(min(8, len(sources), os.cpu_count() or 1)) as pool:
+            list(pool.map(compile_one, sources, objects))
+        _run_hipcc(["--offload-arch=gfx950", "-fPIC", "-shared", "-o", tmp] + objects, verbose)
     os.replace(tmp, path)
 
 
 def build(verbose=False):
     """Compile every source into libhcr.so and the calibration kernels into libhcr_calib.so, then the
     C caller (always recompiles); returns the library path."""
-    _hipcc_shared(LIB, SOURCES + PAGED_SOURCES, verbose)
+    _hipcc_shared(LIB, PAGED_SOURCES + SOURCES, verbose)
     _hipcc_shared(CALIB_LIB, CALIB_SOURCES, verbose)
     build_c_caller(verbose)
     return LIB

@@ -6,96 +6,11 @@
 #include <stdint.h>
 #include <stdlib.h>
 
-#include "hcr_paged_layout.h"
-
-struct hcr_cache {
-  hcr::CacheArgs args;
-};
+#include "hcr_paged_check.h"
 
 namespace hcr {
 
 namespace {
-
-struct Span {
-  uintptr_t lo, hi;  // [lo, hi); lo == hi: absent
-};
-Span span(const void* p, size_t bytes) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return p ? Span{a, a + bytes} : Span{0, 0};
-}
-bool overlap(Span a, Span b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-constexpr long long ROWS_MAX = 1ll << 30;  // rows of heads of a call, positions, tiles: 32 bits hold them
-constexpr long long THREADS_MAX = (1ll << 32) - 1;  // of a launch
-
-size_t pages_elements(const CacheArgs& c) {
-  return ((size_t)c.n_pages * c.kv_heads * c.head_dim) << c.shift;
-}
-size_t means_elements(const CacheArgs& c) { return (size_t)c.n_pages * c.kv_heads * c.head_dim; }
-
-// The device arrays of a batch, which no output may overlap.
-struct BatchSpans {
-  Span s[3];
-};
-BatchSpans batch_spans(const BatchArgs& b) {
-  return BatchSpans{{span(b.q_start, ((size_t)b.n_seqs + 1) * 4), span(b.ctx_len, (size_t)b.n_seqs * 4),
-                     span(b.table, (size_t)b.n_seqs * b.table_stride * 4)}};
-}
-struct CacheSpans {
-  Span s[3];
-};
-CacheSpans cache_spans(const CacheArgs& c) {
-  return CacheSpans{{span(c.k, pages_elements(c) * 2), span(c.v, pages_elements(c) * 2),
-                     span(c.means, means_elements(c) * 2)}};
-}
-template <typename T>
-bool overlap_any(Span o, const T& t) {
-  for (const Span& s : t.s)
-    if (overlap(o, s)) return true;
-  return false;
-}
-
-// The ints of a batch against a cache and a number of heads; *b takes them.  1: nothing to do.
-int check_bounds(const CacheArgs& c, const hcr_batch* in, int heads, BatchArgs* b) {
-  if (!in) return HCR_EINVAL;
-  if (heads < 1 || heads % c.kv_heads || heads / c.kv_heads > GROUP_MAX) return HCR_EINVAL;
-  if (in->n_seqs < 0 || in->n_tokens < 0 || in->max_tokens < 0 || in->max_ctx < 0 || in->table_stride < 0)
-    return HCR_EINVAL;
-  if ((long long)in->table_stride << c.shift < in->max_ctx || in->max_ctx > 1 << 30) return HCR_EINVAL;
-  *b = BatchArgs{in->q_start, in->ctx_len,  in->block_table, in->table_stride,
-                 in->n_seqs,  in->n_tokens, in->max_tokens,  in->max_ctx};
-  if (b->max_tokens > b->n_tokens) b->max_tokens = b->n_tokens;
-  if (b->n_seqs == 0 || b->max_tokens == 0) return 1;
-  // rows and work-groups stay inside 32 bits
-  if ((long long)b->n_tokens * heads > ROWS_MAX || (long long)b->n_seqs * b->max_tokens > ROWS_MAX / heads ||
-      (long long)b->n_seqs * ceil_div(b->max_ctx, TILE) > ROWS_MAX)
-    return HCR_EINVAL;
-  return HCR_OK;
-}
-// Page lists whose positions and tiles (all tokens' together) 32 bits hold.
-bool lists_fit(const CacheArgs& c, const BatchArgs& b, int n_sel) {
-  return n_sel >= 0 && (long long)n_sel << c.shift <= ROWS_MAX &&
-         ((long long)n_sel << (c.shift - TILE_SHIFT)) * b.n_tokens <= ROWS_MAX;
-}
-int check_arrays(const BatchArgs& b) {
-  if (!b.q_start || !b.ctx_len || (!b.table && b.table_stride)) return HCR_EINVAL;
-  if (!aligned(b.q_start, 4) || !aligned(b.ctx_len, 4) || !aligned(b.table, 4)) return HCR_EALIGN;
-  return HCR_OK;
-}
-
-// Rows of heads of one input: their span, or an error.
-int check_rows(const hcr_rows* r, int type, int n_tokens, int heads, int head_dim, Span* s) {
-  if (!r || !r->data) return HCR_EINVAL;
-  const long long unit = type == HCR_F32 ? 4 : 8, size = type == HCR_F32 ? 4 : 2;
-  const long long most = 1ll << 48;  // elements on the way to the last row
-  if (r->token_stride < 0 || r->head_stride < 0 || r->token_stride > most / n_tokens || r->head_stride > most / heads)
-    return HCR_EINVAL;
-  if (!aligned(r->data, 16) || r->token_stride % unit || r->head_stride % unit) return HCR_EALIGN;
-  const long long last = (n_tokens - 1) * r->token_stride + (heads - 1) * r->head_stride + head_dim;
-  *s = span(r->data, (size_t)last * size);
-  return HCR_OK;
-}
 
 long long attn_grid(const CacheArgs& c, const AttnPlan& p) {
   return ((long long)p.items * c.kv_heads + XCDS - 1) / XCDS * XCDS * p.row_blocks;
@@ -106,8 +21,23 @@ size_t scratch_of(const CacheArgs& c, const AttnPlan& p) {
   return align256((size_t)c.kv_heads * p.row_blocks * p.items * 2 * attn_rows(p) * (c.head_dim + 2) * 4);
 }
 
+// The plan of any kind of call.
+AttnPlan plan_of(const hcr_cache& h, const BatchArgs& b, int heads, int n_sel, const WindowArgs& w) {
+  return coded(h.code) || w.size ? attn_plan_more(h.args, h.code, w, b, heads, n_sel)
+                                 : attn_plan(h.args, b, heads, n_sel);
+}
+// A window held to the longest sequence: no sum with a position passes 32 bits.
+WindowArgs held(WindowArgs w, const BatchArgs& b) {
+  const int most = b.max_ctx > 1 ? b.max_ctx : 1;
+  if (w.size > most) w.size = most;
+  if (w.first > most) w.first = most;
+  return w;
+}
+
+}  // namespace
+
 int attn(hcr_cache_t h, const hcr_batch* batch, int heads, double scale, const void* q, const int* sel, int n_sel,
-         int out_type, void* out, void* scratch, size_t scratch_bytes, void* stream) {
+         const WindowArgs& w, int out_type, void* out, void* scratch, size_t scratch_bytes, void* stream) {
   if (!h) return HCR_EINVAL;
   const CacheArgs& c = h->args;
   AttnArgs a{};
@@ -121,7 +51,9 @@ int attn(hcr_cache_t h, const hcr_batch* batch, int heads, double scale, const v
   if (!q || !out) return HCR_EINVAL;
   if (const int e = check_arrays(a.b)) return e;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(sel, 4) || !aligned(scratch, 256)) return HCR_EALIGN;
-  a.plan = attn_plan(c, a.b, heads, n_sel);
+  a.code = h->code;
+  a.window = held(w, a.b);
+  a.plan = plan_of(*h, a.b, heads, n_sel, a.window);
   if (attn_grid(c, a.plan) * 64 * 16 > THREADS_MAX || (long long)a.b.n_tokens * heads * 256 > THREADS_MAX)
     return HCR_EINVAL;
   const size_t need = scratch_of(c, a.plan);
@@ -132,8 +64,8 @@ int attn(hcr_cache_t h, const hcr_batch* batch, int heads, double scale, const v
   const Span sl = span(sel, (size_t)a.b.n_tokens * c.kv_heads * n_sel * 4);
   const Span written[] = {so, ss};
   if (overlap(so, ss)) return HCR_EALIAS;
-  for (const Span& w : written)
-    if (overlap(w, sq) || overlap(w, sl) || overlap_any(w, cache_spans(c)) || overlap_any(w, batch_spans(a.b)))
+  for (const Span& s : written)
+    if (overlap(s, sq) || overlap(s, sl) || overlap_any(s, cache_spans(*h)) || overlap_any(s, batch_spans(a.b)))
       return HCR_EALIAS;
   a.q = static_cast<const uint16_t*>(q);
   a.sel = sel;
@@ -147,7 +79,8 @@ int attn(hcr_cache_t h, const hcr_batch* batch, int heads, double scale, const v
   a.scale_hi = (float)log2e;
   if (fabs(a.scale_hi) >= fabs(log2e)) a.scale_hi = nextafterf(a.scale_hi, 0.f);
   a.scale_lo = (float)(log2e - a.scale_hi);
-  if (scale != 0) {
+  // (over codes and windows for a scale of zero too: what a row does not see is hidden ahead of the product)
+  if (scale != 0 || coded(a.code) || a.window.size) {
     const float least = copysignf(FLT_TRUE_MIN, (float)scale);
     if (a.scale_hi == 0.f) a.scale_hi = least;
     if (a.scale_lo == 0.f) a.scale_lo = least;
@@ -157,7 +90,31 @@ int attn(hcr_cache_t h, const hcr_batch* batch, int heads, double scale, const v
   return launch_attn(a, stream);
 }
 
-}  // namespace
+size_t attn_scratch(hcr_cache_t h, const hcr_batch* batch, int heads, int n_sel, const WindowArgs& w) {
+  BatchArgs b;
+  if (!h || check_bounds(h->args, batch, heads, &b) != HCR_OK || !lists_fit(h->args, b, n_sel)) return 0;
+  return scratch_of(h->args, plan_of(*h, b, heads, n_sel, held(w, b)));
+}
+
+int check_cache(const CacheArgs& c, const CodeArgs& x) {
+  if (!aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(c.means, 16) || !aligned(x.k_scales, 16) ||
+      !aligned(x.v_scales, 16))
+    return HCR_EALIGN;
+  const CacheSpans s = cache_spans(c, x);
+  for (int i = 0; i < 5; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(s.s[i], s.s[j])) return HCR_EALIAS;
+  return HCR_OK;
+}
+
+int new_cache(const CacheArgs& c, const CodeArgs& x, hcr_cache_t* out) {
+  hcr_cache* h = static_cast<hcr_cache*>(malloc(sizeof(hcr_cache)));
+  if (!h) return HCR_EINVAL;
+  h->args = c;
+  h->code = x;
+  *out = h;
+  return HCR_OK;
+}
 
 // Measured on MI355X, 8 kv heads, graphs of calls on rotated inputs (us a call), lengths from an eighth of the
 // longest up to it:
@@ -189,13 +146,12 @@ int attn(hcr_cache_t h, const hcr_batch* batch, int heads, double scale, const v
 //              against 575 with 4); 4, two work-groups a CU, for runs where no sequence is longer than 2,048 (one of
 //              2,000, D = 256: 13.4 against 14.5) and for many sets of up to 512 (300: 14 against 17), since a short
 //              one is mostly the wait for its first loads
-AttnPlan attn_plan(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel) {
+static AttnPlan plan_for(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel, int tiles) {
   constexpr int CUS = 256;
   AttnPlan p{};
   const int group = heads / c.kv_heads;
   const int rows = n_sel ? group : b.max_tokens * group;
   const bool wide = c.head_dim == 256;
-  const int tiles = n_sel ? n_sel << (c.shift - TILE_SHIFT) : ceil_div(b.max_ctx, TILE);
   const long long sets = n_sel ? b.n_tokens : b.n_seqs;
   const bool lengthy = rows > 48 && rows <= 64 && tiles >= 256 && sets * tiles >= 512;
   p.q_tiles = rows > 16 && (c.head_dim == 128 || (wide && (rows <= 32 || lengthy))) ? 2 : 1;
@@ -240,6 +196,22 @@ AttnPlan attn_plan(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel)
   return p;
 }
 
+AttnPlan attn_plan(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel) {
+  return plan_for(c, b, heads, n_sel, n_sel ? n_sel << (c.shift - TILE_SHIFT) : ceil_div(b.max_ctx, TILE));
+}
+
+AttnPlan attn_plan_more(const CacheArgs& c, const CodeArgs& x, const WindowArgs& w, const BatchArgs& b, int heads,
+                        int n_sel) {
+  const int shift = tile_shift(coded(x), c.head_dim);
+  long long tiles = n_sel ? n_sel << (c.shift - shift) : ((long long)b.max_ctx + (1 << shift) - 1) >> shift;
+  if (w.size) {  // the first tiles and those of the longest window of a sequence (of a row block: fewer)
+    const long long most = ((w.first + (1ll << shift) - 1) >> shift) +
+                           ((w.size + (long long)b.max_tokens + (1 << shift) - 2) >> shift) + 1;
+    if (tiles > most) tiles = most;
+  }
+  return plan_for(c, b, heads, n_sel, (int)tiles);
+}
+
 }  // namespace hcr
 
 using namespace hcr;
@@ -258,16 +230,11 @@ int hcr_cache_create(void* k_pages, void* v_pages, void* k_means, int n_pages, i
   if (!k_pages || !v_pages || n_pages < 1 || kv_heads < 1 || kv_heads > 4096 || !head_dim_ok(head_dim) ||
       !page_ok(page))
     return HCR_EINVAL;
-  if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(k_means, 16)) return HCR_EALIGN;
   const CacheArgs c{static_cast<uint16_t*>(k_pages), static_cast<uint16_t*>(v_pages), static_cast<uint16_t*>(k_means),
                     n_pages, kv_heads, head_dim, log2_of(page)};
-  const CacheSpans s = cache_spans(c);
-  if (overlap(s.s[0], s.s[1]) || overlap(s.s[0], s.s[2]) || overlap(s.s[1], s.s[2])) return HCR_EALIAS;
-  hcr_cache* h = static_cast<hcr_cache*>(malloc(sizeof(hcr_cache)));
-  if (!h) return HCR_EINVAL;
-  h->args = c;
-  *out = h;
-  return HCR_OK;
+  const CodeArgs none{nullptr, nullptr, HCR_BF16};
+  if (const int e = check_cache(c, none)) return e;
+  return new_cache(c, none, out);
 }
 
 void hcr_cache_destroy(hcr_cache_t c) { free(c); }
@@ -300,7 +267,7 @@ int hcr_cache_append(hcr_cache_t h, const hcr_batch* batch, int heads, int type,
   in[5] = span(rope_dim ? rope : nullptr, (size_t)rope_rows * rope_dim * 4);
   if (append_grid(c, a.b, heads).groups * APPEND_THREADS > THREADS_MAX) return HCR_EINVAL;
   const Span so = span(q_out, (size_t)a.b.n_tokens * heads * c.head_dim * 2);
-  const CacheSpans sc = cache_spans(c);
+  const CacheSpans sc = cache_spans(*h);
   if (overlap_any(so, sc) || overlap_any(so, batch_spans(a.b))) return HCR_EALIAS;
   for (const Span& s : in)
     if (overlap(so, s) || overlap_any(s, sc)) return HCR_EALIAS;
@@ -318,24 +285,23 @@ int hcr_cache_append(hcr_cache_t h, const hcr_batch* batch, int heads, int type,
   a.rope_dim = rope_dim;
   a.rope_style = rope_style;
   a.q_out = static_cast<uint16_t*>(q_out);
+  a.code = h->code;
   return launch_append(a, stream);
 }
 
 size_t hcr_attn_scratch_bytes(hcr_cache_t h, const hcr_batch* batch, int heads, int n_sel) {
-  BatchArgs b;
-  if (!h || check_bounds(h->args, batch, heads, &b) != HCR_OK || !lists_fit(h->args, b, n_sel)) return 0;
-  return scratch_of(h->args, attn_plan(h->args, b, heads, n_sel));
+  return attn_scratch(h, batch, heads, n_sel, WindowArgs{0, 0});
 }
 
 int hcr_attn(hcr_cache_t c, const hcr_batch* batch, int heads, double scale, const void* q, int out_type, void* out,
              void* scratch, size_t scratch_bytes, void* stream) {
-  return attn(c, batch, heads, scale, q, nullptr, 0, out_type, out, scratch, scratch_bytes, stream);
+  return attn(c, batch, heads, scale, q, nullptr, 0, WindowArgs{0, 0}, out_type, out, scratch, scratch_bytes, stream);
 }
 
 int hcr_attn_blocks(hcr_cache_t c, const hcr_batch* batch, int heads, double scale, const void* q, const int* sel,
                     int n_sel, int out_type, void* out, void* scratch, size_t scratch_bytes, void* stream) {
   if (n_sel < 1 || !sel) return HCR_EINVAL;
-  return attn(c, batch, heads, scale, q, sel, n_sel, out_type, out, scratch, scratch_bytes, stream);
+  return attn(c, batch, heads, scale, q, sel, n_sel, WindowArgs{0, 0}, out_type, out, scratch, scratch_bytes, stream);
 }
 
 int hcr_block_scores(hcr_cache_t h, const hcr_batch* batch, int heads, const void* q, float* scores, int scores_stride,
@@ -354,7 +320,7 @@ int hcr_block_scores(hcr_cache_t h, const hcr_batch* batch, int heads, const voi
   if (!aligned(q, 16) || !aligned(scores, 16)) return HCR_EALIGN;
   if ((long long)a.b.n_seqs * c.kv_heads * (pages / 64 + 1) * 256 > THREADS_MAX) return HCR_EINVAL;
   const Span so = span(scores, (size_t)a.b.n_tokens * c.kv_heads * scores_stride * 4);
-  if (overlap(so, span(q, (size_t)a.b.n_tokens * heads * c.head_dim * 2)) || overlap_any(so, cache_spans(c)) ||
+  if (overlap(so, span(q, (size_t)a.b.n_tokens * heads * c.head_dim * 2)) || overlap_any(so, cache_spans(*h)) ||
       overlap_any(so, batch_spans(a.b)))
     return HCR_EALIAS;
   a.q = static_cast<const uint16_t*>(q);
@@ -384,7 +350,7 @@ int hcr_block_topk(hcr_cache_t h, const hcr_batch* batch, const float* scores, i
   const size_t rows = (size_t)a.b.n_tokens * c.kv_heads;
   if (rows * 1024 > (size_t)THREADS_MAX) return HCR_EINVAL;
   const Span so = span(sel, rows * n_sel * 4);
-  if (overlap(so, span(scores, rows * scores_stride * 4)) || overlap_any(so, cache_spans(c)) ||
+  if (overlap(so, span(scores, rows * scores_stride * 4)) || overlap_any(so, cache_spans(*h)) ||
       overlap_any(so, batch_spans(a.b)))
     return HCR_EALIAS;
   a.scores = scores;

@@ -8,6 +8,7 @@
 
 #include "hcr_layout.h"
 #include "hcr_paged.h"
+#include "hcr_paged_q8.h"
 
 #if defined(__HIPCC__)
 #define HCR_HD __host__ __device__ inline __attribute__((always_inline))
@@ -34,6 +35,17 @@ struct CacheArgs {
   uint16_t* means;
   int n_pages, kv_heads, head_dim, shift;  // page = 1 << shift
 };
+// What they take besides of a cache of codes (code HCR_BF16: none, BF16 pages).
+struct CodeArgs {
+  float* k_scales;
+  float* v_scales;
+  int code;
+};
+HCR_HD bool coded(const CodeArgs& x) { return x.code == HCR_INT8 || x.code == HCR_E4M3; }
+// The positions that a token sees: all up to its own (size 0), or its last `size` and the first `first`.
+struct WindowArgs {
+  int size, first;
+};
 struct BatchArgs {
   const int* q_start;
   const int* ctx_len;
@@ -48,6 +60,10 @@ HCR_HD size_t head_base(const CacheArgs& c, int page, int h) {
 // Element of dimension d of slot s within a head's page.
 HCR_HD int k_at(int shift, int s, int d) { return (((d >> 3) << shift) + s) * 8 + (d & 7); }
 HCR_HD int v_at(int head_dim, int s, int d) { return ((s >> 3) * head_dim + d) * 8 + (s & 7); }
+// The same for codes, 16 in the place of 8, and a slot's scale.
+HCR_HD int k_code_at(int shift, int s, int d) { return (((d >> 4) << shift) + s) * 16 + (d & 15); }
+HCR_HD int v_code_at(int head_dim, int s, int d) { return ((s >> 4) * head_dim + d) * 16 + (s & 15); }
+HCR_HD size_t scale_base(const CacheArgs& c, int page, int h) { return ((size_t)page * c.kv_heads + h) << c.shift; }
 
 // A sequence's rows [row, row + tokens) and the position of its first new token (negative where the sequence is
 // shorter than its window), held to the bounds of the batch whatever q_start and ctx_len say.
@@ -76,6 +92,10 @@ HCR_HD int ceil_div(int a, int b) { return (a + b - 1) / b; }
 // pages), tiles of 32 positions, and splits of the length into chunks of tiles
 constexpr int TILE = 32;
 constexpr int TILE_SHIFT = 5;
+// A tile of codes has 64 positions, so that a wave has as many bytes on their way as of BF16 (and 32 of D = 256, whose
+// accumulators leave no room for more).  Pages of codes hold 64 positions at least.
+HCR_HD bool code_page_ok(int page) { return page_ok(page) && page >= 64; }
+constexpr int tile_shift(bool codes, int D) { return codes && D != 256 ? TILE_SHIFT + 1 : TILE_SHIFT; }
 // Waves of a work-group at most: what its registers leave room for on a CU (one 16-row tile of D = 256 takes 249
 // of 512 registers of a lane, two 334; of D = 128 153 and 207; of D = 64 105).
 constexpr int attn_waves(int D, int q_tiles) { return D == 64 ? 16 : D == 256 && q_tiles > 1 ? 4 : 8; }
@@ -127,6 +147,25 @@ HCR_HD int attn_lds(int D, const AttnPlan& p) {
   return p.groups > 1 ? p.groups * (p.row_waves * 16 * D * 4 + rows * 8) : rows * D * 2;
 }
 AttnPlan attn_plan(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel);
+// The plan over codes or over a window.
+AttnPlan attn_plan_more(const CacheArgs& c, const CodeArgs& x, const WindowArgs& w, const BatchArgs& b, int heads,
+                        int n_sel);
+
+// The tiles that rows of lengths len_min to len_max (a row's position + 1; 0 and less: it sees nothing) see through a
+// window: the first `firsts`, then those from tile `low` on.
+struct WindowTiles {
+  int firsts, low, tiles;
+};
+HCR_HD WindowTiles window_tiles(const WindowArgs& w, int len_min, int len_max, int shift) {
+  const int start = len_min > w.size ? len_min - w.size : 0;
+  WindowTiles t;
+  t.low = start >> shift;
+  t.firsts = (w.first + (1 << shift) - 1) >> shift;
+  if (t.firsts > t.low) t.firsts = t.low;
+  t.tiles = t.firsts + (len_max > 0 ? ((len_max - 1) >> shift) + 1 - t.low : 0);
+  if (t.tiles < 1) t.tiles = 1;
+  return t;
+}
 
 struct AttnArgs {
   CacheArgs c;
@@ -138,8 +177,13 @@ struct AttnArgs {
   void* out;
   float* part;  // [kv_heads][row_blocks][items][2][rows][D], then (m, l) pairs [kv_heads][row_blocks][items][2][rows]
   AttnPlan plan;
+  CodeArgs code;
+  WindowArgs window;
 };
-int launch_attn(const AttnArgs& a, void* stream);
+int launch_attn(const AttnArgs& a, void* stream);  // of every kind: takes those below
+int launch_attn_window(const AttnArgs& a, void* stream);
+int launch_attn_int8(const AttnArgs& a, void* stream);
+int launch_attn_e4m3(const AttnArgs& a, void* stream);
 
 // ---- append
 struct AppendArgs {
@@ -151,8 +195,10 @@ struct AppendArgs {
   float eps;
   int rope_dim, rope_style;
   uint16_t* q_out;
+  CodeArgs code;
 };
-int launch_append(const AppendArgs& a, void* stream);
+int launch_append(const AppendArgs& a, void* stream);  // of either kind
+int launch_append_q8(const AppendArgs& a, void* stream);
 constexpr int APPEND_THREADS = 256;
 constexpr int APPEND_EACH = 4;  // tokens of a work-group of query heads, one where there are few
 HCR_HD int append_each(const BatchArgs& b) { return b.max_tokens >= 32 ? APPEND_EACH : 1; }
@@ -169,6 +215,22 @@ HCR_HD AppendGrid append_grid(const CacheArgs& c, const BatchArgs& b, int heads)
   g.groups = g.kv_groups + (long long)b.n_seqs * ceil_div(b.max_tokens, append_each(b)) * g.passes;
   return g;
 }
+
+// ---- read back
+struct ReadArgs {
+  CacheArgs c;
+  CodeArgs code;
+  BatchArgs b;
+  int out_type;
+  void *k_out, *v_out;  // either may be null
+};
+int launch_read(const ReadArgs& a, void* stream);
+constexpr int READ_THREADS = 256;
+constexpr int READ_SLOTS = 32;  // positions of a work-group
+// The aligned position that a sequence's parts begin at (negative for a padded one), and the parts of READ_SLOTS that its
+// rows can touch.
+HCR_HD int read_start(int first) { return first & ~(READ_SLOTS - 1); }
+HCR_HD int read_parts(const BatchArgs& b) { return (b.max_tokens - 1) / READ_SLOTS + 2; }
 
 // ---- scores and selection
 struct ScoreArgs {

@@ -1,17 +1,20 @@
-"""ctypes binding of the paged key-value cache of libhcr.so (C ABI in include/hcr_paged.h).
+"""ctypes binding of the paged key-value cache of libhcr.so (C ABI in include/hcr_paged.h and hcr_paged_q8.h).
 
 A decode window's path behind the attn_q projection (``hcr.matvec_bf16``): ``PagedCache.append`` normalises and
 rotates the heads of the new tokens and writes their keys and values into pages, ``attend`` attends over the pages,
 and at long contexts ``block_scores``, ``block_topk`` and ``attend_blocks`` attend over the pages of the highest
-scores alone.  Argument marshalling only, as in ``hcr.py``: every step runs in the library's kernels, on torch's
-current stream of the cache's device or on ``stream`` (a raw hipStream_t).  There is no fallback.
+scores alone, or ``attend_window`` over the last positions and the first few.  Pages hold BF16 or, in half the bytes,
+int8 or E4M3 codes with a scale for each position and head; ``read`` gives rows of either back.  Argument marshalling
+only, as in ``hcr.py``: every step runs in the library's kernels, on torch's current stream of the cache's device or on
+``stream`` (a raw hipStream_t).  There is no fallback.
 
 Outputs and scratch made here are made on the stream of the call; with another ``stream`` than torch's current one,
 outputs are noted on that one too (``Tensor.record_stream``), so that the caller takes them there, once it has waited
 for ``stream``, as any tensor of its own.  The inputs' memory is the caller's: a tensor that may be freed before the
 kernels have run is recorded on ``stream``, as for any call of torch's.
 
-A decode step (``y``: the projections' output, [tokens][heads + 2 kv_heads][head_dim])::
+A decode step (``y``: the projections' output, [tokens][heads + 2 kv_heads][head_dim]; with ``dtype=torch.int8`` or
+``torch.float8_e4m3fn`` the same cache is one of codes)::
 
     from bf16_hyper_connection_amd.paged import Batch, PagedCache
     cache = PagedCache.allocate(n_pages=4096, kv_heads=8, head_dim=128, page=64)
@@ -19,6 +22,7 @@ A decode step (``y``: the projections' output, [tokens][heads + 2 kv_heads][head
     q = cache.append(batch, y[:, :32], y[:, 32:40], y[:, 40:], q_norm=wq, k_norm=wk, rope=angles)
     out = cache.attend(batch, q)                                                # or, over the best 32 pages a token:
     out = cache.attend_blocks(batch, q, cache.block_topk(batch, cache.block_scores(batch, q), 32))
+    out = cache.attend_window(batch, q, window=4096, n_first=4)                 # or, over the last 4,096 positions
 """
 
 import ctypes
@@ -28,9 +32,10 @@ import torch
 from bf16_hyper_connection_amd import hcr
 from bf16_hyper_connection_amd.hcr import HCR_OK, HCRError
 
-HCR_F32, HCR_BF16 = 0, 1
+HCR_F32, HCR_BF16, HCR_INT8, HCR_E4M3 = 0, 1, 2, 3
 HCR_ROPE_HALVES, HCR_ROPE_PAIRS = 0, 1
 _TYPES = {torch.float32: HCR_F32, torch.bfloat16: HCR_BF16}
+_CODES = {torch.int8: HCR_INT8, torch.float8_e4m3fn: HCR_E4M3}
 
 _vp, _ip, _sz, _ll, _fl, _db = (ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong, ctypes.c_float,
                                      ctypes.c_double)
@@ -72,6 +77,16 @@ def lib():
         L.hcr_block_scores.argtypes = [_vp, pb, _ip, _vp, _vp, _ip, _vp]
         L.hcr_block_topk.restype = _ip
         L.hcr_block_topk.argtypes = [_vp, pb, _vp, _ip, _ip, _ip, _ip, _vp, _vp]
+        L.hcr_cache_create_q8.restype = _ip
+        L.hcr_cache_create_q8.argtypes = [_vp, _vp, _vp, _vp, _vp, _ip, _ip, _ip, _ip, _ip, ctypes.POINTER(_vp)]
+        L.hcr_cache_pages_bytes_q8.restype = _sz
+        L.hcr_cache_pages_bytes_q8.argtypes = [_ip, _ip, _ip, _ip]
+        L.hcr_cache_read.restype = _ip
+        L.hcr_cache_read.argtypes = [_vp, pb, _ip, _vp, _vp, _vp]
+        L.hcr_attn_window_scratch_bytes.restype = _sz
+        L.hcr_attn_window_scratch_bytes.argtypes = [_vp, pb, _ip, _ip, _ip]
+        L.hcr_attn_window.restype = _ip
+        L.hcr_attn_window.argtypes = [_vp, pb, _ip, _db, _vp, _ip, _ip, _ip, _vp, _vp, _sz, _vp]
         _lib = L
     return _lib
 
@@ -135,39 +150,66 @@ class PagedCache:
     [n_pages][kv_heads][page / 8][head_dim][8], ``k_means`` BF16 [n_pages][kv_heads][head_dim] or None (no block
     scores).  head_dim is 64, 128 or 256, page 32, 64, 128 or 256.  The pages are fixed (their contents are not): for
     others make another cache.
+
+    A cache of codes: int8 or float8_e4m3fn ``k_pages`` [n_pages][kv_heads][head_dim / 16][page][16] and ``v_pages``
+    [n_pages][kv_heads][page / 16][head_dim][16], float32 ``k_scales`` and ``v_scales`` [n_pages][kv_heads][page]; page
+    64, 128 or 256.
     """
 
-    def __init__(self, k_pages, v_pages, k_means=None):
-        for name, t in (("k_pages", k_pages), ("v_pages", v_pages), ("k_means", k_means)):
-            if t is not None and (t.dtype != torch.bfloat16 or not t.is_contiguous() or not t.is_cuda):
-                raise ValueError(f"{name}: a contiguous bfloat16 device tensor")
-        if k_pages.dim() != 5 or k_pages.shape[4] != 8:
-            raise ValueError("k_pages: [n_pages][kv_heads][head_dim / 8][page][8]")
+    def __init__(self, k_pages, v_pages, k_means=None, k_scales=None, v_scales=None):
+        dtype = k_pages.dtype
+        code = _CODES.get(dtype)
+        if code is None and (k_scales is not None or v_scales is not None):
+            raise ValueError("k_scales and v_scales: of int8 or float8_e4m3fn pages")
+        if code is not None and (k_scales is None or v_scales is None):
+            raise ValueError("k_scales and v_scales: float32 [n_pages][kv_heads][page]")
+        kind, each = (torch.bfloat16, 8) if code is None else (dtype, 16)
+        for name, t, want in (("k_pages", k_pages, kind), ("v_pages", v_pages, kind), ("k_means", k_means, torch.bfloat16),
+                              ("k_scales", k_scales, torch.float32), ("v_scales", v_scales, torch.float32)):
+            if t is not None and (t.dtype != want or not t.is_contiguous() or not t.is_cuda):
+                raise ValueError(f"{name}: a contiguous {str(want)[6:]} device tensor")
+        if k_pages.dim() != 5 or k_pages.shape[4] != each:
+            raise ValueError(f"k_pages: [n_pages][kv_heads][head_dim / {each}][page][{each}]")
         n, heads, chunks, page, _ = k_pages.shape
-        if tuple(v_pages.shape) != (n, heads, page // 8, chunks * 8, 8):
-            raise ValueError(f"v_pages: expected {(n, heads, page // 8, chunks * 8, 8)}")
-        if k_means is not None and tuple(k_means.shape) != (n, heads, chunks * 8):
-            raise ValueError(f"k_means: expected {(n, heads, chunks * 8)}")
-        if v_pages.device != k_pages.device or (k_means is not None and k_means.device != k_pages.device):
-            raise ValueError("pages and means on one device")
+        if tuple(v_pages.shape) != (n, heads, page // each, chunks * each, each):
+            raise ValueError(f"v_pages: expected {(n, heads, page // each, chunks * each, each)}")
+        if k_means is not None and tuple(k_means.shape) != (n, heads, chunks * each):
+            raise ValueError(f"k_means: expected {(n, heads, chunks * each)}")
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            if t is not None and tuple(t.shape) != (n, heads, page):
+                raise ValueError(f"{name}: expected {(n, heads, page)}")
+        if any(t is not None and t.device != k_pages.device for t in (v_pages, k_means, k_scales, v_scales)):
+            raise ValueError("pages, means and scales on one device")
         self.k_pages, self.v_pages, self.k_means = k_pages, v_pages, k_means
-        self.n_pages, self.kv_heads, self.page, self.head_dim = n, heads, page, chunks * 8
+        self.k_scales, self.v_scales = k_scales, v_scales
+        self.n_pages, self.kv_heads, self.page, self.head_dim = n, heads, page, chunks * each
         self.device = k_pages.device
         self._L, self.handle = lib(), None
         h = _vp()
-        _check(self._L.hcr_cache_create(k_pages.data_ptr(), v_pages.data_ptr(),
-                                        None if k_means is None else k_means.data_ptr(), n, heads, self.head_dim,
-                                        page, ctypes.byref(h)), "hcr_cache_create")
+        means = None if k_means is None else k_means.data_ptr()
+        if code is None:
+            _check(self._L.hcr_cache_create(k_pages.data_ptr(), v_pages.data_ptr(), means, n, heads, self.head_dim,
+                                            page, ctypes.byref(h)), "hcr_cache_create")
+        else:
+            _check(self._L.hcr_cache_create_q8(k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+                                               v_scales.data_ptr(), means, code, n, heads, self.head_dim, page,
+                                               ctypes.byref(h)), "hcr_cache_create_q8")
         self.handle = h.value
         self._vp, self._destroy_fn = _vp, self._L.hcr_cache_destroy
 
     @classmethod
-    def allocate(cls, n_pages, kv_heads, head_dim, page=64, device="cuda", means=True):
-        """A cache of newly allocated (uninitialised) pages."""
-        def make(*shape):
-            return torch.empty(shape, dtype=torch.bfloat16, device=device)
-        return cls(make(n_pages, kv_heads, head_dim // 8, page, 8), make(n_pages, kv_heads, page // 8, head_dim, 8),
-                   make(n_pages, kv_heads, head_dim) if means else None)
+    def allocate(cls, n_pages, kv_heads, head_dim, page=64, device="cuda", means=True, dtype=torch.bfloat16):
+        """A cache of newly allocated (uninitialised) pages, of BF16 or of int8 or float8_e4m3fn codes."""
+        if dtype is not torch.bfloat16 and dtype not in _CODES:
+            raise ValueError("dtype: bfloat16, int8 or float8_e4m3fn")
+        each = 16 if dtype in _CODES else 8
+
+        def make(*shape, dtype=dtype):
+            return torch.empty(shape, dtype=dtype, device=device)
+        scales = [make(n_pages, kv_heads, page, dtype=torch.float32) for _ in range(2)] if each == 16 else []
+        return cls(make(n_pages, kv_heads, head_dim // each, page, each),
+                   make(n_pages, kv_heads, page // each, head_dim, each),
+                   make(n_pages, kv_heads, head_dim, dtype=torch.bfloat16) if means else None, *scales)
 
     def __del__(self):
         # references bound at creation: at interpreter exit this module's globals may already be gone
@@ -177,7 +219,7 @@ class PagedCache:
             fn(vp(h))
 
     # what the handle was made of, and what it is destroyed with
-    _FIXED = frozenset(("k_pages", "v_pages", "k_means", "n_pages", "kv_heads", "page", "head_dim", "device", "handle",
+    _FIXED = frozenset(("k_pages", "v_pages", "k_means", "k_scales", "v_scales", "n_pages", "kv_heads", "page", "head_dim", "device", "handle",
                         "_L", "_vp", "_destroy_fn"))
 
     def __setattr__(self, name, value):
@@ -191,7 +233,8 @@ class PagedCache:
         super().__delattr__(name)
 
     def __reduce__(self):  # a copy makes a handle of its own
-        return type(self), (self.k_pages, self.v_pages, self.k_means)
+        scales = () if self.k_scales is None else (self.k_scales, self.v_scales)
+        return type(self), (self.k_pages, self.v_pages, self.k_means, *scales)
 
     def _call(self, fn, batch, stream, *args):
         """The entry point on the cache's device, its stream last."""
@@ -287,7 +330,7 @@ class PagedCache:
                    HCR_ROPE_PAIRS if interleaved else HCR_ROPE_HALVES, q_out.data_ptr())
         return q_out
 
-    def _attend(self, fn, batch, q, sel, scale, out, out_dtype, scratch, stream):
+    def _attend(self, fn, batch, q, sel, scale, out, out_dtype, scratch, stream, window=()):
         n, heads = self._heads_of(q)
         if out is None:
             out = self._new(stream, (n, heads, self.head_dim), out_dtype)
@@ -297,13 +340,14 @@ class PagedCache:
             raise ValueError("out: float32 or bfloat16")
         n_sel = 0 if sel is None else sel.shape[2]
         c_batch = batch._of(n)
-        need = self._L.hcr_attn_scratch_bytes(self.handle, c_batch, heads, n_sel)
+        need = self._L.hcr_attn_window_scratch_bytes(self.handle, c_batch, heads, *window) if window else \
+            self._L.hcr_attn_scratch_bytes(self.handle, c_batch, heads, n_sel)
         if scratch is None:
             scratch = self._new(stream, need, torch.uint8, returned=False) if need else None
         elif not scratch.is_cuda or scratch.device != self.device or not scratch.is_contiguous():
             raise ValueError(f"scratch: a contiguous tensor on {self.device}")
         room = 0 if scratch is None else scratch.numel() * scratch.element_size()
-        listed = () if sel is None else (sel.data_ptr(), n_sel)
+        listed = window if sel is None else (sel.data_ptr(), n_sel)
         self._call(fn, batch, stream, c_batch, heads, self.head_dim ** -0.5 if scale is None else scale,
                    q.data_ptr(), *listed, _TYPES[out.dtype], out.data_ptr(),
                    None if scratch is None else scratch.data_ptr(), room)
@@ -326,9 +370,48 @@ class PagedCache:
         self._given("sel", sel, (n, self.kv_heads, sel.shape[2]), torch.int32)
         return self._attend(self._L.hcr_attn_blocks, batch, q, sel, scale, out, out_dtype, scratch, stream)
 
+    def attend_window(self, batch, q, window, n_first=0, scale=None, out=None, out_dtype=torch.float32, scratch=None,
+                      stream=None):
+        """``attend`` over a sliding window: each token sees the last ``window`` positions up to its own and the first
+        ``n_first`` of the sequence.  Table entries of pages that no token sees may be -1."""
+        if not -1 << 31 <= min(window, n_first) <= max(window, n_first) < 1 << 31:  # ctypes would cut them to 32 bits
+            raise ValueError("window and n_first: whole numbers of 32 bits")
+        return self._attend(self._L.hcr_attn_window, batch, q, None, scale, out, out_dtype, scratch, stream,
+                            (window, n_first))
+
     def scratch_bytes(self, batch, n_tokens, heads, n_sel=0):
         """Bytes that ``attend`` (n_sel 0) or ``attend_blocks`` needs for this batch."""
         return int(self._L.hcr_attn_scratch_bytes(self.handle, batch._of(n_tokens), heads, n_sel))
+
+    def window_scratch_bytes(self, batch, n_tokens, heads, window, n_first=0):
+        """Bytes that ``attend_window`` needs for this batch."""
+        return int(self._L.hcr_attn_window_scratch_bytes(self.handle, batch._of(n_tokens), heads, window, n_first))
+
+    def read(self, batch, n_tokens, out_dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
+        """Keys and values of the batch's positions as rows, [n_tokens][kv_heads][head_dim] each.
+
+        The positions are those that ``append`` would write: the last q_start[b + 1] - q_start[b] of sequence b (for a
+        whole sequence its length).  BF16 or float32 (``out_dtype``, or ``k_out``'s and ``v_out``'s, of one type).  Rows
+        of padded tokens and of pages outside the cache are zeros; rows behind the last sequence's are not written.
+        """
+        if not 0 <= n_tokens < 1 << 31:
+            raise ValueError("n_tokens: not negative, under 2^31")
+        shape = (n_tokens, self.kv_heads, self.head_dim)
+        given = k_out if k_out is not None else v_out
+        dtype = out_dtype if given is None else given.dtype
+        if dtype not in _TYPES:
+            raise ValueError("k_out and v_out: float32 or bfloat16")
+        if k_out is None:
+            k_out = self._new(stream, shape, dtype)
+        else:
+            self._given("k_out", k_out, shape, dtype)
+        if v_out is None:
+            v_out = self._new(stream, shape, dtype)
+        else:
+            self._given("v_out", v_out, shape, dtype)
+        self._call(self._L.hcr_cache_read, batch, stream, batch._of(n_tokens), _TYPES[dtype], k_out.data_ptr(),
+                   v_out.data_ptr())
+        return k_out, v_out
 
     def block_scores(self, batch, q, scores=None, stream=None):
         """Scores of the complete pages before each token's own: float32 [n_tokens][kv_heads][pages].

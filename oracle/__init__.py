@@ -19,4 +19,4 @@ from .reference import (  # noqa: F401
 )
 from .q8_0 import dequantize_q8_0, hc_read_q8_0, quantize_q8_0  # noqa: F401,E402
 from .matvec import matvec_bf16  # noqa: F401,E402
-from . import paged  # noqa: F401,E402
+from . import paged, paged_codes  # noqa: F401,E402
