@@ -25,8 +25,8 @@ SOURCES = ["hcr_kernels.hip", "hcr_matvec.hip", "hcr_api.cpp"]
 PAGED_SOURCES = ["hcr_attn_int8.hip", "hcr_attn_e4m3.hip", "hcr_attn.hip", "hcr_attn_window.hip", "hcr_append.hip",
                  "hcr_append_q8.hip", "hcr_cache_read.hip", "hcr_blocks.hip", "hcr_paged_api.cpp",
                  "hcr_paged_q8_api.cpp"]
-PAGED_HEADERS = ["hcr_paged_device.h", "hcr_paged_layout.h", "hcr_attn_device.h", "hcr_append_device.h",
-                 "hcr_paged_check.h"]
+PAGED_HEADERS = ["hcr_paged_device.h", "hcr_paged_layout.h", "hcr_attn_device.h", "hcr_attn_rows.h", "hcr_attn_launch.h",
+                 "hcr_append_device.h", "hcr_paged_check.h"]
 # the calibration kernels (include/hcr_calib.h): a library of their own, measurement only
 CALIB_LIB = os.path.join(PKG, "libhcr_calib.so")
 CALIB_SOURCES = ["hcr_calib.hip"]

@@ -1,6 +1,6 @@
 // Attention over BF16 pages, all of a sequence's or the listed ones (hcr_attn_device.h).
 
-#include "hcr_attn_device.h"
+#include "hcr_attn_launch.h"
 
 namespace hcr {
 

@@ -103,6 +103,19 @@ __device__ __forceinline__ uint4 split_rest(const float (&v)[8], const uint4& hi
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
+__device__ __forceinline__ uint2 split_rest4(const f32x4& v, const uint2& hi, const uint2& lo) {
+  const uint32_t h[2] = {hi.x, hi.y}, l[2] = {lo.x, lo.y};
+  uint32_t r[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    f32x2 x = {v[2 * e], v[2 * e + 1]};
+    x -= f32x2{__uint_as_float(h[e] << 16), __uint_as_float(h[e] & 0xFFFF0000u)};
+    x -= f32x2{__uint_as_float(l[e] << 16), __uint_as_float(l[e] & 0xFFFF0000u)};
+    r[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
+  }
+  return make_uint2(r[0], r[1]);
+}
+
 __device__ __forceinline__ void store4(void* out, int type, size_t at, const f32x4& v) {
   if (type == HCR_F32) {
     *reinterpret_cast<f32x4*>(static_cast<float*>(out) + at) = v;
@@ -424,6 +437,20 @@ __device__ __forceinline__ uint4 drop_odd_but(uint4& v, uint32_t bits) {
 }
 // Of a word of four E4M3 codes, bit 8 k + 7 where code k is a NaN (0x7F, 0xFF).
 __device__ __forceinline__ uint32_t odd_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+// The same as drop_odd_but for 8 codes.
+__device__ __forceinline__ uint4 drop_odd_codes(uint32_t& lo, uint32_t& hi, uint32_t bits) {
+  uint32_t drop = 0;  // bit i: code i
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    drop |= (odd_codes(lo) >> (8 * k + 7) & 1u) << k | (odd_codes(hi) >> (8 * k + 7) & 1u) << (4 + k);
+  drop &= ~bits;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    lo &= ~(bit_mask(drop, k) & 0xFFu << 8 * k);
+    hi &= ~(bit_mask(drop, 4 + k) & 0xFFu << 8 * k);
+  }
+  return ones8(drop);
+}
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_or(uint32_t v) {
   return v | (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
@@ -810,20 +837,32 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
           split_hi_lo(x, ph[m], pl[m]);
           if (a.out_type == HCR_F32) pr[m] = split_rest(x, ph[m], pl[m]);
         }
+        constexpr int GROUP = 1;
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          uint4 value;
-          if constexpr (sizeof(V) == 16)
-            value = operand<CODE>(vf[d], u);
-          else
-            value = widened<CODE>(vf[d].x, vf[d].y);
+        for (int d0 = 0; d0 < DT; d0 += GROUP) {
+          uint4 value[GROUP];
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            acc[m][d] = mfma(value, ph[m], acc[m][d]);
-            acc[m][d] = mfma(value, pl[m], acc[m][d]);
-            if (a.out_type == HCR_F32) acc[m][d] = mfma(value, pr[m], acc[m][d]);
+          for (int d = 0; d < GROUP; ++d) {
+            if constexpr (sizeof(V) == 16)
+              value[d] = operand<CODE>(vf[d0 + d], u);
+            else
+              value[d] = widened<CODE>(vf[d0 + d].x, vf[d0 + d].y);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) acc[m][d0 + d] = mfma(value[d], ph[m], acc[m][d0 + d]);
           }
-          if (d % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int d = 0; d < GROUP; ++d) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) acc[m][d0 + d] = mfma(value[d], pl[m], acc[m][d0 + d]);
+          }
+          if (a.out_type == HCR_F32) {
+#pragma unroll
+            for (int d = 0; d < GROUP; ++d) {
+#pragma unroll
+              for (int m = 0; m < MT; ++m) acc[m][d0 + d] = mfma(value[d], pr[m], acc[m][d0 + d]);
+            }
+          }
+          if (d0 % 4 == 3) __builtin_amdgcn_sched_barrier(0);
         }
       }
     } else {
@@ -915,11 +954,10 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
   }
 }
 
-template <int D, int MT, int SEEN, bool ONCE, int CODE>
-__global__ __launch_bounds__(64 * attn_waves(D, MT)) void attn_part(AttnArgs a) {
+// A work-group's part of a call: its kv head, row block and tiles, set by set.
+template <int SHIFT, int SEEN, class Run>
+__device__ __forceinline__ void part_of(const AttnArgs& a, const Run& run) {
   constexpr bool SEL = SEEN == LISTED;
-  constexpr int SHIFT = Format<CODE, D>::SHIFT;
-  extern __shared__ uint4 lds[];
   const int lane = threadIdx.x & 63;
   // work-group -> (run, kv head, row block); the row blocks of one run sit on one XCD (its L2 then serves all but
   // the first)
@@ -955,11 +993,19 @@ __global__ __launch_bounds__(64 * attn_waves(D, MT)) void attn_part(AttnArgs a) 
   while (set.b >= 0) {
     const int lo = max(begin - set.first, 0), hi = min(begin + cut.run - set.first, set.tiles);
     const Out out{a, lo == 0 && hi == set.tiles, slot + part_slot(item, cut.run, set.first), slots};
-    attn_run<D, MT, SEEN, ONCE, CODE>(a, set, h, rb, lo, hi, entry, out, lds);
+    run(set, h, rb, lo, hi, entry, out);
     if (SEL || cut.apart || set.first + set.tiles >= begin + cut.run) break;
     set = next_seq<SEEN>(a, set, lane, tiles_of);
     __syncthreads();  // the LDS of the set before is free
   }
+}
+
+template <int D, int MT, int SEEN, bool ONCE, int CODE>
+__global__ __launch_bounds__(64 * attn_waves(D, MT)) void attn_part(AttnArgs a) {
+  extern __shared__ uint4 lds[];
+  part_of<Format<CODE, D>::SHIFT, SEEN>(a, [&](const Set& set, int h, int rb, int lo, int hi, int entry, const Out& out) {
+    attn_run<D, MT, SEEN, ONCE, CODE>(a, set, h, rb, lo, hi, entry, out, lds);
+  });
 }
 
 // One row's parts joined: D / 4 lanes hold a row of 4 values each, the groups of lanes take the parts in turn and
@@ -1036,43 +1082,6 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
   }
   const float f = sum > 0.f ? 1.f / sum : 0.f;
   store4(a.out, a.out_type, ((size_t)row * a.heads + hq) * D + 4 * l, acc * f);
-}
-
-// ---- launches (of a kind of cache and of Seen; instantiated in the files that include this)
-template <int D, int MT, int SEEN, int CODE>
-void run_part(const AttnArgs& a, int grid, hipStream_t st) {
-  const dim3 threads(64 * a.plan.row_waves * a.plan.groups);
-  const int lds = attn_lds(D, a.plan);
-  // one wave's rows, and not several tokens' lists, which mostly name the same pages
-  if (a.plan.row_waves * a.plan.row_blocks == 1 && (SEEN != LISTED || a.b.max_tokens == 1))
-    hipLaunchKernelGGL((attn_part<D, MT, SEEN, true, CODE>), dim3(grid), threads, lds, st, a);
-  else
-    hipLaunchKernelGGL((attn_part<D, MT, SEEN, false, CODE>), dim3(grid), threads, lds, st, a);
-}
-template <int D, int SEEN, int CODE>
-void run_attn(const AttnArgs& a, int grid, int join_grid, hipStream_t st) {
-  // a wave a row where rows have few parts, four where many
-  const int join = a.plan.items > 2 * (SEEN == LISTED ? a.b.n_tokens : a.b.n_seqs) ? 256 : 64;
-  if (a.plan.q_tiles == 1) {
-    run_part<D, 1, SEEN, CODE>(a, grid, st);
-  } else if constexpr (D != 64) {
-    run_part<D, 2, SEEN, CODE>(a, grid, st);
-  }
-  if (join_grid) hipLaunchKernelGGL((attn_join<D, SEEN, Format<CODE, D>::SHIFT>), dim3(join_grid), dim3(join), 0, st, a);
-}
-template <int SEEN, int CODE>
-int launch_seen(const AttnArgs& a, void* stream) {
-  const AttnPlan& p = a.plan;
-  const int grid = ceil_div(p.items * a.c.kv_heads, XCDS) * XCDS * p.row_blocks;
-  const int join_grid = attn_joins(p) ? a.b.n_tokens * a.heads : 0;
-  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  (void)hipGetLastError();
-  switch (a.c.head_dim) {
-    case 64: run_attn<64, SEEN, CODE>(a, grid, join_grid, st); break;
-    case 128: run_attn<128, SEEN, CODE>(a, grid, join_grid, st); break;
-    default: run_attn<256, SEEN, CODE>(a, grid, join_grid, st);
-  }
-  return hipGetLastError() == hipSuccess ? HCR_OK : HCR_EHIP;
 }
 
 }  // namespace hcr

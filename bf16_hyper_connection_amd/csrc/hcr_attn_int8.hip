@@ -1,6 +1,6 @@
 // Attention over pages of int8 codes (hcr_attn_device.h).
 
-#include "hcr_attn_device.h"
+#include "hcr_attn_launch.h"
 
 namespace hcr {
 

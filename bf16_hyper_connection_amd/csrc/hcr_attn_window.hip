@@ -1,6 +1,6 @@
 // Attention over BF16 pages through a sliding window (hcr_attn_device.h).
 
-#include "hcr_attn_device.h"
+#include "hcr_attn_launch.h"
 
 namespace hcr {
 

@@ -146,7 +146,7 @@ int new_cache(const CacheArgs& c, const CodeArgs& x, hcr_cache_t* out) {
 //              against 575 with 4); 4, two work-groups a CU, for runs where no sequence is longer than 2,048 (one of
 //              2,000, D = 256: 13.4 against 14.5) and for many sets of up to 512 (300: 14 against 17), since a short
 //              one is mostly the wait for its first loads
-static AttnPlan plan_for(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel, int tiles) {
+static AttnPlan plan_for(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel, int tiles, bool one_tile) {
   constexpr int CUS = 256;
   AttnPlan p{};
   const int group = heads / c.kv_heads;
@@ -154,7 +154,7 @@ static AttnPlan plan_for(const CacheArgs& c, const BatchArgs& b, int heads, int 
   const bool wide = c.head_dim == 256;
   const long long sets = n_sel ? b.n_tokens : b.n_seqs;
   const bool lengthy = rows > 48 && rows <= 64 && tiles >= 256 && sets * tiles >= 512;
-  p.q_tiles = rows > 16 && (c.head_dim == 128 || (wide && (rows <= 32 || lengthy))) ? 2 : 1;
+  p.q_tiles = !one_tile && rows > 16 && (c.head_dim == 128 || (wide && (rows <= 32 || lengthy))) ? 2 : 1;
   const int row_tiles = ceil_div(rows, 16 * p.q_tiles);
   p.row_blocks = ceil_div(row_tiles, wide ? 4 : 8);
   p.row_waves = ceil_div(row_tiles, p.row_blocks);
@@ -197,19 +197,48 @@ static AttnPlan plan_for(const CacheArgs& c, const BatchArgs& b, int heads, int 
 }
 
 AttnPlan attn_plan(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel) {
-  return plan_for(c, b, heads, n_sel, n_sel ? n_sel << (c.shift - TILE_SHIFT) : ceil_div(b.max_ctx, TILE));
+  return plan_for(c, b, heads, n_sel, n_sel ? n_sel << (c.shift - TILE_SHIFT) : ceil_div(b.max_ctx, TILE), false);
+}
+
+// Over codes and windows.  Up to 16 rows: as above, a row tile a wave.  More: the rows' work-groups of four waves
+// (hcr_attn_rows.h), up to four row tiles each, where a tile of 64 positions lies in a page.
+static AttnPlan rows_plan(const CacheArgs& c, bool codes, const BatchArgs& b, int rows, int n_sel, int tiles) {
+  constexpr int CUS = 256;
+  AttnPlan p{};
+  p.shared = 1;
+  const int row_tiles = ceil_div(rows, 16);
+  p.row_blocks = ceil_div(row_tiles, 4);
+  p.q_tiles = ceil_div(row_tiles, p.row_blocks);
+  p.row_waves = p.groups = 1;
+  const long long sets = n_sel ? b.n_tokens : b.n_seqs, units = (long long)c.kv_heads * p.row_blocks;
+  const long long full = sets * units;
+  p.whole = full < CUS ? tiles <= 4 : full < 2 * CUS ? tiles <= 16 : tiles <= 64;
+  p.least = 2;
+  const int fill = CUS * rows_held(codes, c.head_dim, p.q_tiles);
+  const long long runs = ceil_div(tiles > 0 ? tiles : 1, p.least);
+  long long items = fill / units;
+  if (n_sel) {
+    items /= sets;
+    items = (items > runs ? runs : items > 1 ? items : 1) * sets;
+  } else if (items > runs * sets) {
+    items = runs * sets;
+  }
+  p.items = p.whole ? (int)sets : items > 1 ? (int)items : 1;
+  return p;
 }
 
 AttnPlan attn_plan_more(const CacheArgs& c, const CodeArgs& x, const WindowArgs& w, const BatchArgs& b, int heads,
                         int n_sel) {
-  const int shift = tile_shift(coded(x), c.head_dim);
+  const int rows = (n_sel ? 1 : b.max_tokens) * (heads / c.kv_heads);
+  const bool shared = rows > 16 && c.shift >= ROWS_SHIFT;
+  const int shift = shared ? ROWS_SHIFT : tile_shift(coded(x), c.head_dim);
   long long tiles = n_sel ? n_sel << (c.shift - shift) : ((long long)b.max_ctx + (1 << shift) - 1) >> shift;
   if (w.size) {  // the first tiles and those of the longest window of a sequence (of a row block: fewer)
     const long long most = ((w.first + (1ll << shift) - 1) >> shift) +
                            ((w.size + (long long)b.max_tokens + (1 << shift) - 2) >> shift) + 1;
     if (tiles > most) tiles = most;
   }
-  return plan_for(c, b, heads, n_sel, (int)tiles);
+  return shared ? rows_plan(c, coded(x), b, rows, n_sel, (int)tiles) : plan_for(c, b, heads, n_sel, (int)tiles, true);
 }
 
 }  // namespace hcr

@@ -95,6 +95,7 @@ constexpr int TILE_SHIFT = 5;
 // A tile of codes has 64 positions, so that a wave has as many bytes on their way as of BF16 (and 32 of D = 256, whose
 // accumulators leave no room for more).  Pages of codes hold 64 positions at least.
 HCR_HD bool code_page_ok(int page) { return page_ok(page) && page >= 64; }
+constexpr int ROWS_SHIFT = 6;  // tiles of work-groups whose waves share their rows (hcr_attn_rows.h)
 constexpr int tile_shift(bool codes, int D) { return codes && D != 256 ? TILE_SHIFT + 1 : TILE_SHIFT; }
 // Waves of a work-group at most: what its registers leave room for on a CU (one 16-row tile of D = 256 takes 249
 // of 512 registers of a lane, two 334; of D = 128 153 and 207; of D = 64 105).
@@ -106,6 +107,9 @@ constexpr int attn_waves(int D, int q_tiles) { return D == 64 ? 16 : D == 256 &&
 // below the bounds.  The host fixes the number of work-groups, the device the run's length.  Where the work-groups
 // suffice, every set begins a run of its own (a second set costs a work-group the wait for its first loads again);
 // else a run goes on from one set to the next.
+constexpr int rows_held(bool codes, int D, int q_tiles) {
+  return D == 256 ? (q_tiles > (codes ? 3 : 2) ? 2 : 3) : D == 128 && q_tiles > 2 ? 3 : 4;
+}
 struct AttnPlan {
   int q_tiles;     // 16-row tiles a wave holds
   int row_waves;   // waves of a work-group over the rows
@@ -114,6 +118,7 @@ struct AttnPlan {
   int items;       // work-groups over the tiles
   int least;       // tiles that are worth a work-group
   int whole;       // a work-group for each set instead, with all of its tiles: nothing to join
+  int shared;      // the work-group's four waves share q_tiles row tiles, and tiles of 64 positions
 };
 HCR_HD int attn_rows(const AttnPlan& p) { return p.row_waves * p.q_tiles * 16; }  // of a work-group
 // Tiles of one run, from those of all sets (every set has one at least: a set without positions writes its zeros).

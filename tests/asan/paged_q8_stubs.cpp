@@ -119,7 +119,7 @@ static const char* check_windows() {
 static const char* check_plans() {
   for (int code : {(int)HCR_BF16, (int)HCR_INT8, (int)HCR_E4M3})
     for (int D : {64, 128, 256})
-      for (int page : {64, 256})
+      for (int page : {32, 64, 256})
         for (int kv : {1, 3, 8})
           for (int group : {1, 6, 16, 33, 64})
             for (int seqs : {1, 3, 64, 1000})
@@ -130,14 +130,17 @@ static const char* check_plans() {
                       if (n_sel && size) continue;
                       const CodeArgs x{nullptr, nullptr, code};
                       if (!coded(x) && !size) continue;
+                      if (coded(x) && page == 32) continue;
                       const CacheArgs c{nullptr, nullptr, nullptr, 10, kv, D, log2_of(page)};
                       const BatchArgs b{nullptr, nullptr, nullptr, ctx / page + 1, seqs, seqs * tokens, tokens, ctx};
                       const AttnPlan p = attn_plan_more(c, x, WindowArgs{size, 4}, b, kv * group, n_sel);
                       const int rows = n_sel ? group : tokens * group;
-                      CHECK(p.q_tiles == 1 || (p.q_tiles == 2 && D != 64));
+                      CHECK(p.shared ? p.q_tiles >= 2 && p.q_tiles <= 4 && p.groups == 1 && p.row_waves == 1
+                                     : p.q_tiles == 1);
                       CHECK(p.row_waves * p.groups <= attn_waves(D, p.q_tiles) && p.groups >= 1 && p.row_waves >= 1);
                       CHECK(p.row_blocks * attn_rows(p) >= rows && (p.row_blocks - 1) * attn_rows(p) < rows);
-                      CHECK(attn_lds(D, p) <= 160 * 1024 && attn_lds(D, p) >= attn_rows(p) * D * 2);
+                      if (!p.shared) CHECK(attn_lds(D, p) <= 160 * 1024 && attn_lds(D, p) >= attn_rows(p) * D * 2);
+                      if (p.shared) CHECK(page >= 64);
                       CHECK(p.least >= 1 && p.items >= 1);
                       if (p.whole) CHECK(p.items == (n_sel ? seqs * tokens : seqs) && !attn_joins(p));
                     }
