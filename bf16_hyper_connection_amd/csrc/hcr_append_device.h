@@ -245,8 +245,7 @@ __device__ __forceinline__ uint32_t head_top(uint32_t v) {
   }
   return v;
 }
-// A head's 8 values of this lane as codes, and the head's scale.  Divided, not multiplied by an inverse: the nearest
-// code of the quotient is the definition.
+// A head's 8 values of this lane as codes, and the head's scale.
 template <int LANES, int CODE>
 __device__ __forceinline__ uint2 quantised(const Values& x, float& scale) {
   constexpr float TOP = CODE == HCR_INT8 ? 127.f : 448.f;
@@ -259,12 +258,18 @@ __device__ __forceinline__ uint2 quantised(const Values& x, float& scale) {
   top = head_top<LANES>(top);
   scale = __uint_as_float(top) / TOP;
   if (top >= 0x7F800000u) scale = __uint_as_float(0x7FC00000u);  // a value that is not finite: the head is NaN
+  // one inverse for the head's quotients (a division each where it would be infinite or the scale has few bits)
+  const float inverse = 1.f / scale;
+  const bool small = !(scale >= 0x1p-100f);
   float c[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    c[e] = scale > 0.f ? x.v[e] / scale : 0.f;  // (a scale that rounds to few bits: over TOP)
-    c[e] = fminf(fmaxf(c[e], -TOP), TOP);
+  for (int e = 0; e < 8; ++e) c[e] = x.v[e] * inverse;
+  if (__any(small)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[e] = scale > 0.f ? (small ? x.v[e] / scale : c[e]) : 0.f;
   }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) c[e] = fminf(fmaxf(c[e], -TOP), TOP);
   uint32_t w[2] = {0, 0};
   if constexpr (CODE == HCR_INT8) {
 #pragma unroll

@@ -1,121 +1,177 @@
 // Reading the paged cache back as rows, gfx950 (MI355X): keys and values of either kind of pages, a code times its scale
 // in FP32, rounded once.
 //
-// A work-group takes READ_SLOTS positions of a sequence (aligned, so that they lie in one page and in whole chunks) of
-// one kv head, keys or values.  Keys: 16 bytes of a page are some dimensions of one position, a lane's part of a row as
-// they are.  Values: 16 bytes are some positions of one dimension; they are turned in LDS, four bytes (codes) or two
-// values (BF16) at a time.
+// A work-group takes READ_SLOTS positions of a sequence (aligned, so that each 32 of them lie in one page and in whole
+// chunks) of one kv head, keys and values, all of their loads on their way together.  Keys: 16 bytes of a page are some
+// dimensions of one position, a lane's part of a row as they are.  Values: 16 bytes are some positions of one dimension;
+// they are turned in registers, four bytes (codes) or two values (BF16) at a time, and go through LDS.
+#include <type_traits>
 
 #include "hcr_append_device.h"
 
 namespace hcr {
+
+// Rows are stored once and read later: past the caches.
+template <typename T>
+__device__ __forceinline__ void put16(void* p, const T& v) {
+  static_assert(sizeof(T) == 16, "16 bytes");
+  __builtin_nontemporal_store(v, static_cast<T*>(p));
+}
+
+
+// 8 values of a page, as loaded; a lane's share of a row, so that neighbouring lanes store neighbouring 16 bytes.
+template <int CODE>
+using Eight = std::conditional_t<CODE == HCR_BF16, uint4, uint2>;
+template <int CODE>
+__device__ __forceinline__ Eight<CODE> load_eight(const void* p) {
+  if constexpr (CODE == HCR_BF16)
+    return ldw16(p);
+  else
+    return ldw8(p);
+}
+// Times a scale in FP32, stored; `none`: zeros.
+template <int CODE, bool F32>
+__device__ __forceinline__ void store_eight(const Eight<CODE>& u, float scale, bool none, void* out, size_t at) {
+  Values x{};
+  if (!none) {
+    if constexpr (CODE == HCR_BF16) {
+      Raw<false> r;
+      r.u[0] = u;
+      x = values<false>(r);
+    } else {
+      x = code_values<CODE>(u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x.v[e] *= scale;
+    }
+  }
+  if constexpr (F32) {
+    float* to = static_cast<float*>(out) + at;
+    put16(to, f32x4{x.v[0], x.v[1], x.v[2], x.v[3]});
+    put16(to + 4, f32x4{x.v[4], x.v[5], x.v[6], x.v[7]});
+  } else {
+    const uint4 r = round8(x);
+    put16(static_cast<uint16_t*>(out) + at, u32x4_t{r.x, r.y, r.z, r.w});
+  }
+}
+
+// Byte of the c-th 8 dimensions of a slot's key.
+template <bool CODED>
+__device__ __forceinline__ int k_eight(int shift, int s, int c) {
+  return CODED ? k_code_at(shift, s, 8 * c) : 2 * k_at(shift, s, 8 * c);
+}
 
 template <int D, int CODE, bool F32>
 __global__ __launch_bounds__(READ_THREADS) void cache_read(ReadArgs a, int parts) {
   constexpr bool CODED = CODE != HCR_BF16;
   constexpr int BYTES = CODED ? 1 : 2, EACH = 16 / BYTES;  // of a value; values in 16 bytes
   constexpr int ROW = D * BYTES + 16;                      // a row in LDS, 16 bytes more: rows start in other banks
-  constexpr int LANES = D / 8;                             // of a row, 8 values each
+  constexpr int LANES = D / 8;                             // of a row
+  constexpr int ITEMS = READ_SLOTS * LANES / READ_THREADS;   // eights of a thread
+  constexpr int N = 4 / BYTES;                             // dimensions of a thread's values
+  constexpr int VITEMS = (READ_SLOTS / EACH * (D / N) + READ_THREADS - 1) / READ_THREADS;
+  static_assert(ITEMS * READ_THREADS == READ_SLOTS * LANES && READ_SLOTS == 64, "a part has whole passes");
   __shared__ __align__(16) uint8_t tile[READ_SLOTS * ROW];
   int g = blockIdx.x;
-  const bool key = g & 1;
-  g >>= 1;
   const int h = g % a.c.kv_heads;
   g /= a.c.kv_heads;
-  const int b = g / parts;
-  if (!(key ? a.k_out : a.v_out)) return;
-  const Seq seq = wave_seq(a.b, b);
+  const Seq seq = wave_seq(a.b, g / parts);
   if (seq.tokens <= 0) return;
   const int tid = threadIdx.x;
-  // positions [lo, hi) of this part (one that begins before position 0 lies there whole)
+  // positions [lo, hi) of this part
   const int start = read_start(seq.first) + g % parts * READ_SLOTS;
   const int lo = max(start, seq.first), hi = min(start + READ_SLOTS, seq.first + seq.tokens);
   if (lo >= hi) return;
-  const int pg = start >> a.c.shift, slot = start & ((1 << a.c.shift) - 1);
-  const int number =
-      start < 0 ? -1 : page_or_none(a.b.table[(size_t)b * a.b.table_stride + pg], a.c.n_pages);
-  const uint8_t* in = nullptr;
-  const float* scales = nullptr;
-  if (number >= 0) {
-    in = reinterpret_cast<const uint8_t*>(key ? a.c.k : a.c.v) + head_base(a.c, number, h) * BYTES;
-    if (CODED) scales = (key ? a.code.k_scales : a.code.v_scales) + scale_base(a.c, number, h) + slot;
-    if (!key) {
-      // 32 bits of a row's dimensions (4 codes, 2 BF16) from as many 16-byte chunks
-      constexpr int N = 4 / BYTES;
-      for (int i = tid; i < READ_SLOTS / EACH * (D / N); i += READ_THREADS) {
-        const int o = i / (D / N), d = N * (i % (D / N));
-        const uint8_t* from = in + ((size_t)(slot / EACH + o) * D + d) * 16;
-        uint32_t w[N][4];
+  // each 32 positions' page (-1: none, or no position asked for) and slot
+  const int* table = a.b.table + (size_t)(g / parts) * a.b.table_stride;
+  int number[2], slot[2];
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const uint4 u = ldw16(from + 16 * e);
-          w[e][0] = u.x;
-          w[e][1] = u.y;
-          w[e][2] = u.z;
-          w[e][3] = u.w;
-        }
+  for (int k = 0; k < 2; ++k) {
+    const int p = start + 32 * k;
+    const bool in = p + 32 > 0 && p + 32 > lo && p < hi && p >= 0;
+    number[k] = in ? table[p >> a.c.shift] : -1;
+    slot[k] = p & ((1 << a.c.shift) - 1);
+  }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t t[N];
-          if constexpr (CODED) {
-            const uint32_t r[4] = {w[0][k], w[1][k], w[2][k], w[3][k]};
-            transpose4(r, t);
-          } else {
-            t[0] = __builtin_amdgcn_perm(w[1][k], w[0][k], 0x05040100u);
-            t[1] = __builtin_amdgcn_perm(w[1][k], w[0][k], 0x07060302u);
-          }
+  for (int k = 0; k < 2; ++k) number[k] = page_or_none(number[k], a.c.n_pages);
+  const uint8_t* kp[2];
+  const uint8_t* vp[2];
+  size_t scales[2];
 #pragma unroll
-          for (int s = 0; s < N; ++s)
-            *reinterpret_cast<uint32_t*>(&tile[(EACH * o + N * k + s) * ROW + d * BYTES]) = t[s];
-        }
-      }
-      __syncthreads();
+  for (int k = 0; k < 2; ++k) {
+    const size_t base = number[k] < 0 ? 0 : head_base(a.c, number[k], h) * BYTES;  // (page 0 is there: not stored)
+    kp[k] = reinterpret_cast<const uint8_t*>(a.c.k) + base;
+    vp[k] = reinterpret_cast<const uint8_t*>(a.c.v) + base;
+    scales[k] = (number[k] < 0 ? 0 : scale_base(a.c, number[k], h)) + slot[k];
+  }
+
+  uint4 w[VITEMS][N];
+  if (a.v_out) {
+#pragma unroll
+    for (int t = 0; t < VITEMS; ++t) {
+      const int i = min(tid + t * READ_THREADS, READ_SLOTS / EACH * (D / N) - 1);
+      const int o = i / (D / N), d = N * (i % (D / N)), k = o * EACH / 32;
+      const uint8_t* from = (k ? vp[1] : vp[0]) + ((size_t)((k ? slot[1] : slot[0]) / EACH + o % (32 / EACH)) * D + d) * 16;
+#pragma unroll
+      for (int e = 0; e < N; ++e) w[t][e] = ldw16(from + 16 * e);
     }
   }
-  for (int i = tid; i < READ_SLOTS * LANES; i += READ_THREADS) {
-    // keys: neighbouring lanes take 8 positions of a chunk, then the next chunks; values: a row's dimensions
-    int s, l;
-    if (key) {
-      s = i % 8 + i / (8 * LANES) * 8;
-      l = i / 8 % LANES;
-    } else {
-      s = i / LANES;
-      l = i % LANES;
+  if (a.k_out) {
+    Eight<CODE> u[ITEMS];
+    float scale[ITEMS];
+#pragma unroll
+    for (int t = 0; t < ITEMS; ++t) {  // neighbouring lanes: a row's values; 64 / LANES rows a wave
+      const int i = tid + t * READ_THREADS, s = i / LANES, c = i % LANES, k = s / 32;
+      const int in = k_eight<CODED>(a.c.shift, (k ? slot[1] : slot[0]) + s % 32, c);
+      u[t] = load_eight<CODE>((k ? kp[1] : kp[0]) + in);
+      if constexpr (CODED) scale[t] = a.code.k_scales[(k ? scales[1] : scales[0]) + s % 32];
     }
+#pragma unroll
+    for (int t = 0; t < ITEMS; ++t) {
+      const int i = tid + t * READ_THREADS, s = i / LANES, c = i % LANES, k = s / 32;
+      const int p = start + s;
+      if (p >= lo && p < hi)
+        store_eight<CODE, F32>(u[t], CODED ? scale[t] : 1.f, (k ? number[1] : number[0]) < 0, a.k_out,
+                               ((size_t)(seq.row + p - seq.first) * a.c.kv_heads + h) * D + 8 * c);
+    }
+  }
+  if (!a.v_out) return;
+#pragma unroll
+  for (int t = 0; t < VITEMS; ++t) {
+    const int i = tid + t * READ_THREADS, o = i / (D / N), d = N * (i % (D / N));
+    if (i >= READ_SLOTS / EACH * (D / N)) break;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t r[N], turned[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) r[e] = k == 0 ? w[t][e].x : k == 1 ? w[t][e].y : k == 2 ? w[t][e].z : w[t][e].w;
+      if constexpr (CODED) {
+        transpose4(r, turned);
+      } else {
+        turned[0] = __builtin_amdgcn_perm(r[1], r[0], 0x05040100u);
+        turned[1] = __builtin_amdgcn_perm(r[1], r[0], 0x07060302u);
+      }
+#pragma unroll
+      for (int s = 0; s < N; ++s)
+        *reinterpret_cast<uint32_t*>(&tile[(EACH * o + N * k + s) * ROW + d * BYTES]) = turned[s];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < ITEMS; ++t) {
+    const int i = tid + t * READ_THREADS, s = i / LANES, c = i % LANES, k = s / 32;
     const int p = start + s;
     if (p < lo || p >= hi) continue;
-    Values x{};
-    if (number >= 0) {
-      if constexpr (CODED) {
-        const uint2 u = key ? *reinterpret_cast<const uint2*>(in + k_code_at(a.c.shift, slot + s, 8 * l))
-                            : *reinterpret_cast<const uint2*>(&tile[s * ROW + 8 * l]);
-        const float scale = scales[s];
-        x = code_values<CODE>(u);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x.v[e] *= scale;
-      } else {
-        Raw<false> r;
-        r.u[0] = key ? *reinterpret_cast<const uint4*>(in + 2 * (size_t)k_at(a.c.shift, slot + s, 8 * l))
-                     : *reinterpret_cast<const uint4*>(&tile[s * ROW + 16 * l]);
-        x = values<false>(r);
-      }
-    }
-    const size_t at = ((size_t)(seq.row + p - seq.first) * a.c.kv_heads + h) * D + 8 * l;
-    void* out = key ? a.k_out : a.v_out;
-    if constexpr (F32) {
-      float* to = static_cast<float*>(out) + at;
-      *reinterpret_cast<f32x4*>(to) = f32x4{x.v[0], x.v[1], x.v[2], x.v[3]};
-      *reinterpret_cast<f32x4*>(to + 4) = f32x4{x.v[4], x.v[5], x.v[6], x.v[7]};
-    } else {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = round8(x);
-    }
+    const float scale = CODED ? a.code.v_scales[(k ? scales[1] : scales[0]) + s % 32] : 1.f;
+    store_eight<CODE, F32>(*reinterpret_cast<const Eight<CODE>*>(&tile[s * ROW + 8 * BYTES * c]), scale,
+                           (k ? number[1] : number[0]) < 0, a.v_out,
+                           ((size_t)(seq.row + p - seq.first) * a.c.kv_heads + h) * D + 8 * c);
   }
 }
 
 template <int D, int CODE>
 void run_read(const ReadArgs& a, hipStream_t st) {
   const int parts = read_parts(a.b);
-  const dim3 grid(a.b.n_seqs * parts * a.c.kv_heads * 2);
+  const dim3 grid(a.b.n_seqs * parts * a.c.kv_heads);
   if (a.out_type == HCR_F32)
     hipLaunchKernelGGL((cache_read<D, CODE, true>), grid, dim3(READ_THREADS), 0, st, a, parts);
   else

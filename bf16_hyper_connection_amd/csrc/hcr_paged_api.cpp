@@ -200,22 +200,35 @@ AttnPlan attn_plan(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel)
   return plan_for(c, b, heads, n_sel, n_sel ? n_sel << (c.shift - TILE_SHIFT) : ceil_div(b.max_ctx, TILE), false);
 }
 
-// Over codes and windows.  Up to 16 rows: as above, a row tile a wave.  More: the rows' work-groups of four waves
-// (hcr_attn_rows.h), up to four row tiles each, where a tile of 64 positions lies in a page.
-static AttnPlan rows_plan(const CacheArgs& c, bool codes, const BatchArgs& b, int rows, int n_sel, int tiles) {
+// Tiles of `1 << shift` positions that rows of `tokens` consecutive tokens see at most.
+static int window_bound(const WindowArgs& w, int max_ctx, long long tokens, int shift) {
+  const long long one = 1ll << shift, all = (max_ctx + one - 1) >> shift;
+  if (!w.size) return (int)all;
+  const long long most = ((w.first + one - 1) >> shift) + ((w.size + tokens + one - 2) >> shift) + 1;
+  return (int)(all < most ? all : most);
+}
+
+// Work-groups of four waves that share their rows (hcr_attn_rows.h), up to four row tiles each.
+static AttnPlan rows_plan(const CacheArgs& c, bool codes, const WindowArgs& w, const BatchArgs& b, int group, int n_sel) {
   constexpr int CUS = 256;
   AttnPlan p{};
   p.shared = 1;
+  const int rows = n_sel ? group : b.max_tokens * group;
   const int row_tiles = ceil_div(rows, 16);
   p.row_blocks = ceil_div(row_tiles, 4);
   p.q_tiles = ceil_div(row_tiles, p.row_blocks);
   p.row_waves = p.groups = 1;
+  const int block = ceil_div(16 * p.q_tiles, group) + 1;  // tokens of a row block
+  const int tiles = n_sel ? n_sel << (c.shift - ROWS_SHIFT)
+                          : window_bound(w, b.max_ctx, block < b.max_tokens ? block : b.max_tokens, ROWS_SHIFT);
   const long long sets = n_sel ? b.n_tokens : b.n_seqs, units = (long long)c.kv_heads * p.row_blocks;
   const long long full = sets * units;
-  p.whole = full < CUS ? tiles <= 4 : full < 2 * CUS ? tiles <= 16 : tiles <= 64;
-  p.least = 2;
-  const int fill = CUS * rows_held(codes, c.head_dim, p.q_tiles);
-  const long long runs = ceil_div(tiles > 0 ? tiles : 1, p.least);
+  p.whole = full < CUS ? tiles <= 4 : full < 2 * CUS ? tiles <= 16 : tiles <= 32;
+  const long long even = (full * tiles + CUS - 1) / CUS;  // of a CU
+  p.least = 1;
+  const int held = rows_held(codes, c.head_dim, p.q_tiles);
+  const int fill = CUS * (even < 8 ? 1 : even < 32 ? 2 : held);
+  const long long runs = tiles > 0 ? tiles : 1;
   long long items = fill / units;
   if (n_sel) {
     items /= sets;
@@ -229,16 +242,19 @@ static AttnPlan rows_plan(const CacheArgs& c, bool codes, const BatchArgs& b, in
 
 AttnPlan attn_plan_more(const CacheArgs& c, const CodeArgs& x, const WindowArgs& w, const BatchArgs& b, int heads,
                         int n_sel) {
-  const int rows = (n_sel ? 1 : b.max_tokens) * (heads / c.kv_heads);
-  const bool shared = rows > 16 && c.shift >= ROWS_SHIFT;
-  const int shift = shared ? ROWS_SHIFT : tile_shift(coded(x), c.head_dim);
-  long long tiles = n_sel ? n_sel << (c.shift - shift) : ((long long)b.max_ctx + (1 << shift) - 1) >> shift;
-  if (w.size) {  // the first tiles and those of the longest window of a sequence (of a row block: fewer)
-    const long long most = ((w.first + (1ll << shift) - 1) >> shift) +
-                           ((w.size + (long long)b.max_tokens + (1 << shift) - 2) >> shift) + 1;
-    if (tiles > most) tiles = most;
+  const int group = heads / c.kv_heads, rows = (n_sel ? 1 : b.max_tokens) * group;
+  if (rows > 16 && c.shift >= ROWS_SHIFT) return rows_plan(c, coded(x), w, b, group, n_sel);
+  const int shift = tile_shift(coded(x), c.head_dim);
+  const int tiles = n_sel ? n_sel << (c.shift - shift) : window_bound(w, b.max_ctx, b.max_tokens, shift);
+  AttnPlan p = plan_for(c, b, heads, n_sel, tiles, true);
+  // sequences are as long as each other through a window: whole ones in two work-groups a CU
+  if (w.size && !p.whole && p.row_waves == 1 && p.groups >= 4 && tiles <= 160 &&
+      (long long)b.n_seqs * c.kv_heads >= 512) {
+    p.whole = 1;
+    p.groups = 4;
+    p.items = b.n_seqs;
   }
-  return shared ? rows_plan(c, coded(x), b, rows, n_sel, (int)tiles) : plan_for(c, b, heads, n_sel, (int)tiles, true);
+  return p;
 }
 
 }  // namespace hcr

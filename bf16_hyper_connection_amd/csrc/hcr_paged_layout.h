@@ -231,7 +231,7 @@ struct ReadArgs {
 };
 int launch_read(const ReadArgs& a, void* stream);
 constexpr int READ_THREADS = 256;
-constexpr int READ_SLOTS = 32;  // positions of a work-group
+constexpr int READ_SLOTS = 64;  // positions of a work-group
 // The aligned position that a sequence's parts begin at (negative for a padded one), and the parts of READ_SLOTS that its
 // rows can touch.
 HCR_HD int read_start(int first) { return first & ~(READ_SLOTS - 1); }
