@@ -346,6 +346,22 @@ def test_attend_blocks(kind, head_dim, page, kv, group, out_dtype):
 
 
 @pytest.mark.parametrize("kind", cu.KINDS)
+@pytest.mark.parametrize("head_dim,page,kv,group", [(128, 64, 1, 24), (64, 128, 2, 33), (256, 64, 1, 64), (128, 64, 1, 17),
+                                                    (256, 256, 1, 48)])
+def test_attend_blocks_of_many_heads(kind, head_dim, page, kv, group):
+    """Groups of more than 16 heads: whole lists, lists cut over work-groups, none at all."""
+    s = cu.scene(kind, 85, kv, head_dim, page, [(2, 60 * page + 5), (1, 20), (3, 2)])
+    g = gen.rng(117, head_dim, group)
+    for n_sel in (3, 50):
+        sel = g.integers(-1, 62, size=(s.n_tokens, kv, n_sel)).astype(np.int32)
+        sel[0, 0, :3] = [0, 60, 60]
+        sel[4, :] = -1
+        out, want, tol = cu.attend(s, kv * group, sel=sel)
+        assert torch.all(out[4] == 0)
+        pu.check_rows(out, want, tol, f"lists of {n_sel}")
+
+
+@pytest.mark.parametrize("kind", cu.KINDS)
 def test_attend_blocks_long_list(kind):
     """A list that is split over work-groups and joined."""
     s = cu.scene(kind, 77, 1, 128, 64, [(2, 12000)])
@@ -520,6 +536,29 @@ def test_calls_are_reproducible(kind):
     for _ in range(5):
         again = [cache.attend(batch, q), cache.attend_window(batch, q, 700, 5), *cache.read(batch, s.n_tokens)]
         assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+@pytest.mark.parametrize("kind", cu.KINDS + ["bf16"])
+def test_two_streams_at_once(kind):
+    """Calls on two streams, each with outputs and scratch of its own, over the same pages."""
+    s = cu.scene(kind, 86, 2, 128, 64, [(5, 9000), (1, 77), (3, 4000)])
+    cache, batch = cu.dev_cache(s), pu.dev_batch(s)
+    qs = [pu.dev_bits(pu.queries(86 + i, s.n_tokens, 16, 128)) for i in range(2)]
+
+    def calls(q):
+        return [cache.attend(batch, q), cache.attend_window(batch, q, 3000, 5), *cache.read(batch, s.n_tokens)]
+    want = [calls(q) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    got = [[], []]
+    for _ in range(10):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(calls(qs[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(want[i], r))
 
 
 @pytest.mark.parametrize("kind", cu.KINDS + ["bf16"])

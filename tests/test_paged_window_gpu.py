@@ -62,6 +62,59 @@ def test_prompts(kind, head_dim, kv, group, T, window, n_first):
     pu.check_rows(out, want, tol, "prompts")
 
 
+@pytest.mark.parametrize("head_dim,kv,group,T", [(128, 1, 4, 1), (64, 2, 8, 5), (256, 1, 6, 9), (128, 1, 17, 40),
+                                                 (64, 1, 64, 3), (256, 1, 33, 20)])
+@pytest.mark.parametrize("window,n_first", [(1, 0), (40, 5), (33, 33), (900, 70)])
+def test_pages_of_32(head_dim, kv, group, T, window, n_first):
+    """BF16 pages shorter than a tile of shared rows, up to many rows."""
+    s = cu.scene("bf16", 140, kv, head_dim, 32, [(T, 1000), (max(T - 1, 1), T), (1, 31), (T, 2500), (0, 9)])
+    out, want, tol = cu.attend(s, kv * group, window=window, n_first=n_first)
+    pu.check_rows(out, want, tol, "pages of 32")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T,group", [(3, 4), (9, 8)])
+def test_rows_behind_the_last_and_loose_bounds(kind, T, group):
+    """Bounds above what the sequences have; rows behind the last sequence's stay as they were."""
+    s = cu.scene(kind, 141, 2, 128, 64, [(T, 1500), (1, 70), (T, 33)], table_extra=40)
+    q = pu.queries(141, s.n_tokens + 5, 2 * group, 128)
+    keys, values = cu.decoded(s)
+    qf = oracle.bf16_bits_to_f64(q)
+    want = o.attend_window(s.batch, keys, values, qf, 0.1, 200, 3)
+    out = torch.full((s.n_tokens + 5, 2 * group, 128), 7.0, device="cuda")
+    cu.dev_cache(s).attend_window(pu.dev_batch(s, max_tokens=2 * T, max_ctx=3000), pu.dev_bits(q), 200, 3, scale=0.1, out=out)
+    torch.cuda.synchronize()
+    pu.check_rows(out, want, pu.rows_tolerance(qf, cu.reach(keys), 0.1, 1500, False), "loose")
+    assert torch.all(out[s.n_tokens:] == 7.0)
+
+
+@pytest.mark.parametrize("head_dim,kv,group,T,window", [(128, 2, 4, 3, 20), (256, 1, 6, 7, 40), (64, 1, 8, 20, 10),
+                                                        (128, 1, 4, 90, 33), (256, 1, 4, 4, 64)])
+def test_codes_that_are_no_numbers_stay_with_the_rows_that_see_them(head_dim, kv, group, T, window):
+    """E4M3 codes 0x7F and 0xFF of values at positions that only some of a window's tokens see."""
+    lens = [300, 400]
+    s = cu.scene("e4m3", 142, kv, head_dim, 64, [(T, c) for c in lens])
+    q = pu.queries(142, s.n_tokens, kv * group, head_dim)
+    keys, values = cu.decoded(s)
+    qf = oracle.bf16_bits_to_f64(q)
+    want = o.attend_window(s.batch, keys, values, qf, 0.1, window, 2)
+    codes, spoilt = o.load_values(s.v_codes), []
+    for b, c in enumerate(lens):
+        spoilt.append([c - T + 1 - window, c - 1] if b == 0 else [c - T - window, c - 1])
+        for i, p in enumerate(spoilt[b]):
+            codes[s.table[b, p // 64], :, p % 64, 5::16] = 0x7F if i else 0xFF
+    s.v_codes = o.store_values(codes)
+    out = cu.dev_cache(s).attend_window(pu.dev_batch(s), pu.dev_bits(q), window, 2, scale=0.1)
+    fine = {}
+    for n, b, p in oracle.paged.tokens(s.q_start, s.ctx_len):
+        if any(p - window < x <= p for x in spoilt[b]):
+            assert torch.isnan(out[n][..., 5::16]).all(), f"row {n} sees a code that is no number"
+        else:
+            fine[n] = want[n]
+    assert len(fine) > 0
+    pu.check_rows(out, fine, pu.rows_tolerance(qf, cu.reach(keys), 0.1, 400, False), "others")
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("head_dim,page,kv,group,T", [(128, 64, 1, 4, 1), (256, 64, 2, 6, 2), (64, 128, 1, 8, 40),
                                                       (128, 256, 1, 16, 20)])
