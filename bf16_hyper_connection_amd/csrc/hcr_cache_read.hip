@@ -110,6 +110,7 @@ __global__ __launch_bounds__(READ_THREADS) void cache_read(ReadArgs a, int parts
     for (int t = 0; t < VITEMS; ++t) {
       const int i = min(tid + t * READ_THREADS, READ_SLOTS / EACH * (D / N) - 1);
       const int o = i / (D / N), d = N * (i % (D / N)), k = o * EACH / 32;
+      if (start + EACH * o >= hi || start + EACH * (o + 1) <= lo) continue;  // no position asked for
       const uint8_t* from = (k ? vp[1] : vp[0]) + ((size_t)((k ? slot[1] : slot[0]) / EACH + o % (32 / EACH)) * D + d) * 16;
 #pragma unroll
       for (int e = 0; e < N; ++e) w[t][e] = ldw16(from + 16 * e);
@@ -121,6 +122,7 @@ __global__ __launch_bounds__(READ_THREADS) void cache_read(ReadArgs a, int parts
 #pragma unroll
     for (int t = 0; t < ITEMS; ++t) {  // neighbouring lanes: a row's values; 64 / LANES rows a wave
       const int i = tid + t * READ_THREADS, s = i / LANES, c = i % LANES, k = s / 32;
+      if (start + s < lo || start + s >= hi) continue;
       const int in = k_eight<CODED>(a.c.shift, (k ? slot[1] : slot[0]) + s % 32, c);
       u[t] = load_eight<CODE>((k ? kp[1] : kp[0]) + in);
       if constexpr (CODED) scale[t] = a.code.k_scales[(k ? scales[1] : scales[0]) + s % 32];

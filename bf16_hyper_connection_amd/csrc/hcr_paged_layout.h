@@ -190,6 +190,9 @@ int launch_attn_window(const AttnArgs& a, void* stream);
 int launch_attn_int8(const AttnArgs& a, void* stream);
 int launch_attn_e4m3(const AttnArgs& a, void* stream);
 
+// Aligned parts of `1 << shift` positions that so many consecutive ones can touch.
+HCR_HD int parts_touched(int tokens, int shift) { return ((tokens - 1 + (1 << shift) - 1) >> shift) + 1; }
+
 // ---- append
 struct AppendArgs {
   CacheArgs c;
@@ -214,7 +217,7 @@ struct AppendGrid {
 };
 HCR_HD AppendGrid append_grid(const CacheArgs& c, const BatchArgs& b, int heads) {
   AppendGrid g;
-  g.pages = ((b.max_tokens - 1) >> c.shift) + 2;
+  g.pages = parts_touched(b.max_tokens, c.shift);
   g.passes = ceil_div(heads, APPEND_THREADS / (c.head_dim / 8));
   g.kv_groups = (long long)b.n_seqs * g.pages * c.kv_heads * 2;
   g.groups = g.kv_groups + (long long)b.n_seqs * ceil_div(b.max_tokens, append_each(b)) * g.passes;
@@ -231,11 +234,12 @@ struct ReadArgs {
 };
 int launch_read(const ReadArgs& a, void* stream);
 constexpr int READ_THREADS = 256;
-constexpr int READ_SLOTS = 64;  // positions of a work-group
+constexpr int READ_SHIFT = 6;
+constexpr int READ_SLOTS = 1 << READ_SHIFT;  // positions of a work-group
 // The aligned position that a sequence's parts begin at (negative for a padded one), and the parts of READ_SLOTS that its
 // rows can touch.
 HCR_HD int read_start(int first) { return first & ~(READ_SLOTS - 1); }
-HCR_HD int read_parts(const BatchArgs& b) { return (b.max_tokens - 1) / READ_SLOTS + 2; }
+HCR_HD int read_parts(const BatchArgs& b) { return parts_touched(b.max_tokens, READ_SHIFT); }
 
 // ---- scores and selection
 struct ScoreArgs {

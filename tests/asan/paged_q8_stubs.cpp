@@ -154,6 +154,8 @@ static const char* check_reads() {
       const BatchArgs b{nullptr, nullptr, nullptr, 1, 1, 1000, max_tokens, 1000};
       const int start = read_start(first);
       CHECK(start <= first && start % READ_SLOTS == 0 && start + read_parts(b) * READ_SLOTS >= first + max_tokens);
+      for (int shift : {5, 6, 8})  // pages that an append can touch, from a sequence's first new position on
+        CHECK((first < 0 ? 0 : first) / (1 << shift) + parts_touched(max_tokens, shift) > (first + max_tokens - 1) / (1 << shift));
     }
   return nullptr;
 }
