@@ -16,6 +16,9 @@ namespace hcr {
 
 constexpr int ROWS_WAVES = 4;
 
+// Waits for every load, in a form that the compiler's own count of them sees.
+__device__ __forceinline__ void loads_done() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+
 template <int CODE>
 struct RowsFormat {
   static constexpr bool CODED = CODE != HCR_BF16;
@@ -78,6 +81,10 @@ __device__ __forceinline__ void rows_run(const AttnArgs& a, const Set& set, int 
     const int len = lds.len[16 * m + li];
     return Reach{SEEN == WINDOW ? len - a.window.size : 0, len, SEEN == WINDOW ? a.window.first : 0};
   };
+  // The query rows are on their way beside the table's entries, and go into LDS behind the first tile's loads: a run
+  // begins after two trips to memory, however many its rows.
+  constexpr int QL = (KS + ROWS_WAVES - 1) / ROWS_WAVES;  // a wave takes the operands w, w + 4, ...
+  uint4 query[RT][QL];
 #pragma unroll
   for (int m = 0; m < RT; ++m) {
     const int r = min(rows.first + 16 * m + li, rows.count - 1);  // behind the last row the last one again, not stored
@@ -88,11 +95,9 @@ __device__ __forceinline__ void rows_run(const AttnArgs& a, const Set& set, int 
       lds.rid[16 * m + li] = rows.first + 16 * m + li < rows.count ? rid : -1;
     }
 #pragma unroll
-    for (int k0 = 0; k0 < KS; k0 += ROWS_WAVES) {  // a wave stores the operands k = w, w + 4, ...
-      const int k = k0 + w;
-      if (KS % ROWS_WAVES == 0 || k < KS)
-        lds.q[m][k][lane] = ld16(a.q + (size_t)rid * D +
-                                 (F::CODED ? 16 * lg + 64 * (k / 2) + 8 * (k % 2) : 8 * lg + 32 * k));
+    for (int j = 0; j < QL; ++j) {
+      const int k = min(ROWS_WAVES * j + w, KS - 1);
+      query[m][j] = ld16(a.q + (size_t)rid * D + (F::CODED ? 16 * lg + 64 * (k / 2) + 8 * (k % 2) : 8 * lg + 32 * k));
     }
   }
 
@@ -105,10 +110,20 @@ __device__ __forceinline__ void rows_run(const AttnArgs& a, const Set& set, int 
 #pragma unroll
     for (int d = 0; d < DL; ++d) acc[m][d] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
+  __builtin_amdgcn_sched_barrier(0);
   bool more = tiles.find();
+  loads_done();
   if (more) {
     load_keys(~0u);
     load_values(~0u);
+  }
+#pragma unroll
+  for (int m = 0; m < RT; ++m) {
+#pragma unroll
+    for (int j = 0; j < QL; ++j) {
+      const int k = ROWS_WAVES * j + w;
+      if (KS % ROWS_WAVES == 0 || k < KS) lds.q[m][k][lane] = query[m][j];
+    }
   }
   lds_barrier();
 
