@@ -1,6 +1,7 @@
 // Attention of a decode window over the paged cache, gfx950 (MI355X):
 //   out[n] = sum_p softmax_p(scale q[n] . k[p]) v[p],   p <= the token's position
-// for every page of a sequence, or for the pages listed per token and kv head.
+// for every page of a sequence, for the pages listed per token and kv head, or through a window (SEEN), over pages of
+// BF16 or of 8-bit codes (CODE).
 //
 // A unit is one kv head of one sequence: its rows are the T x G (tokens x heads of the group) query rows, which
 // all read the same keys and values.  A wave takes tiles of 32 positions and holds 16 or 32 of the rows:
@@ -15,6 +16,17 @@
 // three (the whole FP32 value) for float ones, where two would be the largest error of all (2^-18 of a probability, up
 // to 3.8e-6; the third costs matrix products that the loop has time for).
 //
+// Codes are widened to BF16, which holds each exactly, on their way into the matrix cores; a key's scale multiplies its
+// product, a value's scale its probability ahead of the split:
+//   out = sum_p softmax_p(scale sk[p] (q . ck[p])) sv[p] cv[p]
+// so that scales cost a multiplication a product and no code is ever rounded again.  16 bytes of a page are 16 codes, two
+// operands: a lane's key loads hold 16 dimensions of a key, its value loads the 16 positions whose products it has (tiles
+// of 64 positions, rows 16 (r / 4) + 4 t + r % 4; of D = 256, whose accumulators leave no room, 8 positions in 8 bytes).
+//
+// Through a window a row sees [0, first) and [len - size, len).  Tiles that no row sees are not visited; in a tile that
+// some rows see in part, what a row does not see is hidden by bit masks ahead of its maximum (a product there may be
+// anything) and, of values, ahead of the product.
+//
 // Work: the tiles of all sequences, one behind the other, are cut into equal runs, one for each work-group that the
 // chip holds at once (AttnPlan), so that unlike lengths and loose bounds cost nothing; a run goes from one sequence
 // on to the next.  The waves of a work-group take its tiles in turn and join in LDS; sequences that lie in several
@@ -27,7 +39,14 @@
 // 420,000 positions, 48 heads of 256 over 8, 2 tokens: 505 us, 6.8 TB/s (a 4 GiB device copy moves 4.8); 64 sequences
 // of 1,000 to 8,192, 32 heads of 128 over 8: 194 us, 6.2 TB/s.  36 rows of 4 sequences of up to 9,001: 51 us, 3.3 TB/s:
 // a work-group has 10 tiles behind 6 us of first loads, three row waves share each of them, so that a CU has 64 KB on
-// their way where it has 256 KB with one row wave, and the second launch takes 7.
+// their way where it has 256 KB with one row wave, and the second launch takes 7.  (Rows past 16 over codes and windows
+// go to hcr_attn_rows.h.)
+// Codes, the same calls: 420,000 positions (E4M3, float outputs) 271 us, 6.5 TB/s; 64 sequences (int8) 108 us, 5.8 TB/s;
+// one of 1,000 positions 10.0 us, mostly waits for first loads, one behind the other (lengths, table, keys).  64 windows
+// of 4,096 of BF16 164 us, 6.6 TB/s.
+// Not taken: tiles of 32 for codes of D = 128 with 16 waves (batch 143 us, short call 11.8), tiles of 64 for D = 256 (25
+// registers spilled), two to four row tiles a wave over codes (36 rows of D = 256 130 to 190 us where four waves that
+// share them take 117: past 256 registers each use is a copy).
 
 #pragma once
 
@@ -837,32 +856,22 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
           split_hi_lo(x, ph[m], pl[m]);
           if (a.out_type == HCR_F32) pr[m] = split_rest(x, ph[m], pl[m]);
         }
-        constexpr int GROUP = 1;
 #pragma unroll
-        for (int d0 = 0; d0 < DT; d0 += GROUP) {
-          uint4 value[GROUP];
+        for (int d = 0; d < DT; ++d) {
+          uint4 value;
+          if constexpr (sizeof(V) == 16)
+            value = operand<CODE>(vf[d], u);
+          else
+            value = widened<CODE>(vf[d].x, vf[d].y);
 #pragma unroll
-          for (int d = 0; d < GROUP; ++d) {
-            if constexpr (sizeof(V) == 16)
-              value[d] = operand<CODE>(vf[d0 + d], u);
-            else
-              value[d] = widened<CODE>(vf[d0 + d].x, vf[d0 + d].y);
+          for (int m = 0; m < MT; ++m) acc[m][d] = mfma(value, ph[m], acc[m][d]);
 #pragma unroll
-            for (int m = 0; m < MT; ++m) acc[m][d0 + d] = mfma(value[d], ph[m], acc[m][d0 + d]);
+          for (int m = 0; m < MT; ++m) acc[m][d] = mfma(value, pl[m], acc[m][d]);
+          if (a.out_type == HCR_F32) {  // (one branch for several dimensions was slower: 62 against 53 us at D = 64)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) acc[m][d] = mfma(value, pr[m], acc[m][d]);
           }
-#pragma unroll
-          for (int d = 0; d < GROUP; ++d) {
-#pragma unroll
-            for (int m = 0; m < MT; ++m) acc[m][d0 + d] = mfma(value[d], pl[m], acc[m][d0 + d]);
-          }
-          if (a.out_type == HCR_F32) {
-#pragma unroll
-            for (int d = 0; d < GROUP; ++d) {
-#pragma unroll
-              for (int m = 0; m < MT; ++m) acc[m][d0 + d] = mfma(value[d], pr[m], acc[m][d0 + d]);
-            }
-          }
-          if (d0 % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+          if (d % 4 == 3) __builtin_amdgcn_sched_barrier(0);
         }
       }
     } else {

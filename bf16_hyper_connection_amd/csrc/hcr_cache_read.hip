@@ -5,6 +5,10 @@
 // chunks) of one kv head, keys and values, all of their loads on their way together.  Keys: 16 bytes of a page are some
 // dimensions of one position, a lane's part of a row as they are.  Values: 16 bytes are some positions of one dimension;
 // they are turned in registers, four bytes (codes) or two values (BF16) at a time, and go through LDS.
+//
+// Bound by the bytes.  Measured on MI355X: 51,190 positions of 8 sequences, 8 kv heads of 128, int8 to BF16 (318 MB) 71
+// us, 4.5 TB/s, where a 4 GiB device copy moves 4.7.  On the way there: 32 positions a work-group 85 us; 64 positions, 16
+// bytes of a lane's own row at a time 83; neighbouring lanes' 16 bytes beside each other and stores past the caches 71.
 #include <type_traits>
 
 #include "hcr_append_device.h"
@@ -17,7 +21,6 @@ __device__ __forceinline__ void put16(void* p, const T& v) {
   static_assert(sizeof(T) == 16, "16 bytes");
   __builtin_nontemporal_store(v, static_cast<T*>(p));
 }
-
 
 // 8 values of a page, as loaded; a lane's share of a row, so that neighbouring lanes store neighbouring 16 bytes.
 template <int CODE>

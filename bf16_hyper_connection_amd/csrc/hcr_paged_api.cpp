@@ -208,7 +208,15 @@ static int window_bound(const WindowArgs& w, int max_ctx, long long tokens, int 
   return (int)(all < most ? all : most);
 }
 
-// Work-groups of four waves that share their rows (hcr_attn_rows.h), up to four row tiles each.
+// Work-groups of four waves that share their rows (hcr_attn_rows.h), up to four row tiles each.  As few row blocks as hold
+// the rows, each with as few row tiles: a block reads the set's keys and values once.  Measured (us a call, graphs):
+//   whole      a work-group a set where sets fill the chip and end soon.  D = 128, 24 rows: 64 sequences of 700 21
+//              against 34, of 4,000 97 against 87; 36 rows of D = 256: 32 of 700 33 against 36, 32 of 2,000 84 against 67,
+//              16 of 700 32 against 27.  Prompts of 2,048 through a window of 1,024 85 against 95
+//   fill       work-groups a CU: one for up to 7 tiles, two for up to 31, else what registers leave room for; fewer, longer
+//              runs leave less to join and wait for their first loads less often.  36 rows of D = 256: 16 of 700 23.7 with
+//              one, 28 with two; 16 of 2,000 23.5 with two, 29 with one; one of 30,000 47 with two, 53 with three.  24 rows
+//              through a window of 8,192 21.5 with one, 24 with three; D = 128, one of 4,000 13.0 with one, 15.4 with four
 static AttnPlan rows_plan(const CacheArgs& c, bool codes, const WindowArgs& w, const BatchArgs& b, int group, int n_sel) {
   constexpr int CUS = 256;
   AttnPlan p{};
@@ -240,6 +248,12 @@ static AttnPlan rows_plan(const CacheArgs& c, bool codes, const WindowArgs& w, c
   return p;
 }
 
+// Over codes and windows rows that fill more than one tile share a work-group's four waves: a row tile a wave would read
+// (and widen) every page once a tile.  Measured, 8 kv heads (us, shared against a tile a wave): D = 256, 36 rows over
+// 100,000 positions of int8 117 against 185, of E4M3 111 against 152; D = 128 over 200,000: 20 rows 104 against 119, 48
+// 133 against 185, 64 161 against 200; D = 64, 20 rows 70 against 78; prompts of BF16 through a window 86 against 92.  Its
+// tiles have 64 positions, so pages of 32 (BF16 through a window) keep a tile a wave.  Up to 16 rows one wave has all of
+// a tile's operands as loaded, with no barrier in its loop.
 AttnPlan attn_plan_more(const CacheArgs& c, const CodeArgs& x, const WindowArgs& w, const BatchArgs& b, int heads,
                         int n_sel) {
   const int group = heads / c.kv_heads, rows = (n_sel ? 1 : b.max_tokens) * group;
@@ -247,7 +261,8 @@ AttnPlan attn_plan_more(const CacheArgs& c, const CodeArgs& x, const WindowArgs&
   const int shift = tile_shift(coded(x), c.head_dim);
   const int tiles = n_sel ? n_sel << (c.shift - shift) : window_bound(w, b.max_ctx, b.max_tokens, shift);
   AttnPlan p = plan_for(c, b, heads, n_sel, tiles, true);
-  // sequences are as long as each other through a window: whole ones in two work-groups a CU
+  // sequences are as long as each other through a window: whole ones in two work-groups a CU (64 windows of 4,096: 166
+  // us, in runs 176)
   if (w.size && !p.whole && p.row_waves == 1 && p.groups >= 4 && tiles <= 160 &&
       (long long)b.n_seqs * c.kv_heads >= 512) {
     p.whole = 1;

@@ -92,14 +92,22 @@ HCR_HD int ceil_div(int a, int b) { return (a + b - 1) / b; }
 // pages), tiles of 32 positions, and splits of the length into chunks of tiles
 constexpr int TILE = 32;
 constexpr int TILE_SHIFT = 5;
-// A tile of codes has 64 positions, so that a wave has as many bytes on their way as of BF16 (and 32 of D = 256, whose
-// accumulators leave no room for more).  Pages of codes hold 64 positions at least.
-HCR_HD bool code_page_ok(int page) { return page_ok(page) && page >= 64; }
-constexpr int ROWS_SHIFT = 6;  // tiles of work-groups whose waves share their rows (hcr_attn_rows.h)
+// A wave's tile of codes has 64 positions, so that it has as many bytes on their way as of BF16 (and 32 of D = 256, whose
+// accumulators leave no room for more): 64 sequences of up to 8,192 positions, D = 128, 108 us where tiles of 32 took 143.
 constexpr int tile_shift(bool codes, int D) { return codes && D != 256 ? TILE_SHIFT + 1 : TILE_SHIFT; }
+// Tiles of work-groups whose four waves share their rows (hcr_attn_rows.h): 16 keys a wave.
+constexpr int ROWS_SHIFT = 6;
+// Pages of codes hold a tile of either kind at least.
+HCR_HD bool code_page_ok(int page) { return page_ok(page) && page >= 64; }
 // Waves of a work-group at most: what its registers leave room for on a CU (one 16-row tile of D = 256 takes 249
 // of 512 registers of a lane, two 334; of D = 128 153 and 207; of D = 64 105).
 constexpr int attn_waves(int D, int q_tiles) { return D == 64 ? 16 : D == 256 && q_tiles > 1 ? 4 : 8; }
+// Work-groups of four waves that share their rows, on a CU: the registers are held to that.  As many as spill no more
+// than a dozen of them (measured, codes: D = 128, 20 rows of 200,000 positions 103 us with four, 113 with two; D = 64 70
+// against 84; D = 256, 36 rows of 100,000 117 with three, 118 with two).
+constexpr int rows_held(bool codes, int D, int q_tiles) {
+  return D == 256 ? (q_tiles > (codes ? 3 : 2) ? 2 : 3) : D == 128 && q_tiles > 2 ? 3 : 4;
+}
 
 // How a call is cut.  Its sets of rows (a sequence's window; one token for listed pages) have their tiles one set
 // behind the other, and the work-groups of a kv head and row block take equal runs of them: as many work-groups as
@@ -107,9 +115,6 @@ constexpr int attn_waves(int D, int q_tiles) { return D == 64 ? 16 : D == 256 &&
 // below the bounds.  The host fixes the number of work-groups, the device the run's length.  Where the work-groups
 // suffice, every set begins a run of its own (a second set costs a work-group the wait for its first loads again);
 // else a run goes on from one set to the next.
-constexpr int rows_held(bool codes, int D, int q_tiles) {
-  return D == 256 ? (q_tiles > (codes ? 3 : 2) ? 2 : 3) : D == 128 && q_tiles > 2 ? 3 : 4;
-}
 struct AttnPlan {
   int q_tiles;     // 16-row tiles a wave holds
   int row_waves;   // waves of a work-group over the rows
@@ -190,10 +195,9 @@ int launch_attn_window(const AttnArgs& a, void* stream);
 int launch_attn_int8(const AttnArgs& a, void* stream);
 int launch_attn_e4m3(const AttnArgs& a, void* stream);
 
+// ---- append
 // Aligned parts of `1 << shift` positions that so many consecutive ones can touch.
 HCR_HD int parts_touched(int tokens, int shift) { return ((tokens - 1 + (1 << shift) - 1) >> shift) + 1; }
-
-// ---- append
 struct AppendArgs {
   CacheArgs c;
   BatchArgs b;

@@ -9,11 +9,17 @@
  *   scale = max |y| / top        FP32, one for each position and kv head
  *   code  = y / scale, to the nearest code, ties to the even one;  it stands for code * scale
  *
+ * (the quotient in FP32, within two roundings: a y that lies that close to the middle of two
+ * codes may take either)
+ *
  * so that what a position holds depends on that position alone, however windows were cut
  * and whatever was written over.  A head that holds a value that is not finite has the
  * scale NaN and stands for NaN as a whole; zeros have the scale 0.  hcr_attn and
  * hcr_attn_blocks attend over what the codes stand for, in FP32; hcr_block_scores and
  * hcr_block_topk take such a cache as any other (mean keys are of what the codes stand for).
+ * Pages that were filled otherwise may hold any codes and scales: a key that is no number (the
+ * E4M3 codes 0x7F and 0xFF, a scale that is none) makes every output NaN of the rows that see
+ * it, a value at least its own dimension of them; rows that do not see it take nothing from it.
  *
  * Pages hold 64, 128 or 256 positions:
  *   k_pages  : codes [n_pages][kv_heads][D / 16][page][16]   16 dimensions together
