@@ -42,7 +42,7 @@
 // their way where it has 256 KB with one row wave, and the second launch takes 7.  (Rows past 16 over codes and windows
 // go to hcr_attn_rows.h.)
 // Codes, the same calls: 420,000 positions (E4M3, float outputs) 271 us, 6.5 TB/s; 64 sequences (int8) 108 us, 5.8 TB/s;
-// one of 1,000 positions 10.0 us, mostly waits for first loads, one behind the other (lengths, table, keys).  64 windows
+// one of 700 positions 10.0 us, mostly waits for first loads, one behind the other (lengths, table, keys).  64 windows
 // of 4,096 of BF16 164 us, 6.6 TB/s.
 // Not taken: tiles of 32 for codes of D = 128 with 16 waves (batch 143 us, short call 11.8), tiles of 64 for D = 256 (25
 // registers spilled), two to four row tiles a wave over codes (36 rows of D = 256 130 to 190 us where four waves that

@@ -219,8 +219,8 @@ class PagedCache:
             fn(vp(h))
 
     # what the handle was made of, and what it is destroyed with
-    _FIXED = frozenset(("k_pages", "v_pages", "k_means", "k_scales", "v_scales", "n_pages", "kv_heads", "page", "head_dim", "device", "handle",
-                        "_L", "_vp", "_destroy_fn"))
+    _FIXED = frozenset(("k_pages", "v_pages", "k_means", "k_scales", "v_scales", "n_pages", "kv_heads", "page",
+                        "head_dim", "device", "handle", "_L", "_vp", "_destroy_fn"))
 
     def __setattr__(self, name, value):
         if name in self._FIXED and "_destroy_fn" in self.__dict__:
