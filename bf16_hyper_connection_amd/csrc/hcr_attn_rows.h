@@ -4,7 +4,8 @@
 // of a tile's keys and a quarter of its values' dimensions, so that every byte of a page is loaded (and, of codes,
 // widened) by one wave alone, however many the rows:
 //   S^T = K Q^T : a wave's 16 keys with every row tile (query rows in LDS, one copy for the four waves),
-//   the rows' maxima over the four waves through LDS, then the probabilities' BF16 parts into LDS as operands,
+//   where a row's maximum may move the maxima over the four waves through LDS; the probabilities' BF16 parts into LDS as
+//   operands,
 //   O^T += V^T P^T : a wave's dimensions with every row tile, all 64 positions.
 // A wave's accumulators are the outputs of its dimensions: nothing is joined but the sums.  Two barriers a tile, of LDS
 // alone: keys of the next tile are on their way behind this one's products, values behind theirs.
@@ -47,6 +48,7 @@ struct RowsLds {
   f32x4 tops[RT * 16];            // the rows' largest products of a tile, of each wave
   f32x4 sums[RT * 16];            // the rows' sums, of each wave
   int len[RT * 16], rid[RT * 16];  // the rows' lengths, and their rows of q and out (-1: none)
+  int risen;                       // the last tile (counted from 1) in which a row's maximum may move
 };
 
 // A set's tiles [lo, hi) (counted from its own first): its rows' part of the softmax.
@@ -71,22 +73,22 @@ __device__ __forceinline__ void rows_run(const AttnArgs& a, const Set& set, int 
   const uint32_t v_lane = (uint32_t)(lg * D + 16 * DL * w + li) * 16;
   uint4 kf[KL], vf[DL][VL];
   f32x4 ks = {1.f, 1.f, 1.f, 1.f}, vs_next = ks;  // codes: scales of the lane's 4 positions
-  // No branch around the loads of the next tile, so that each wait counts those behind it exactly: past the last tile
-  // (`on` 0) every lane asks for the tile's first 16 bytes again.
-  const auto load_keys = [&](uint32_t on) {
+  // No branch around the loads of the next tile, so that each wait counts those behind it exactly: past the last tile it
+  // is loaded again, and not waited for.
+  const auto load_keys = [&] {
     if constexpr (F::CODED) {  // ahead of the keys: the wait for those covers both
-      const uint32_t at = 16 * w + 4 * lg & on;
+      const int at = 16 * w + 4 * lg;
       ks = ld4(a.code.k_scales + tiles.scales + at);
       vs_next = ld4(a.code.v_scales + tiles.scales + at);
     }
 #pragma unroll
-    for (int k = 0; k < KL; ++k) kf[k] = ld16(tiles.kp + (k * k_step & on) + (k_lane & on));
+    for (int k = 0; k < KL; ++k) kf[k] = ld16(tiles.kp + k * k_step + k_lane);
   };
-  const auto load_values = [&](uint32_t on) {
+  const auto load_values = [&] {
 #pragma unroll
     for (int d = 0; d < DL; ++d) {
 #pragma unroll
-      for (int u = 0; u < VL; ++u) vf[d][u] = ld16(tiles.vp + (v_lane & on) + (64 * u * D + 256 * d & on));
+      for (int u = 0; u < VL; ++u) vf[d][u] = ld16(tiles.vp + v_lane + (64 * u * D + 256 * d));
     }
   };
 
@@ -114,6 +116,9 @@ __device__ __forceinline__ void rows_run(const AttnArgs& a, const Set& set, int 
     }
   }
 
+  // A scale below zero turns the query rows' signs: the largest product is the largest exponent.
+  const uint32_t turn = a.scale_hi < 0.f ? 0x80008000u : 0u;
+  const float scale_hi = fabsf(a.scale_hi), scale_lo = fabsf(a.scale_lo);
   f32x4 acc[RT][DL];
   float mx[RT], sum[RT];
 #pragma unroll
@@ -123,24 +128,27 @@ __device__ __forceinline__ void rows_run(const AttnArgs& a, const Set& set, int 
 #pragma unroll
     for (int d = 0; d < DL; ++d) acc[m][d] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
+  if (w == 0 && lane == 0) lds.risen = 0;
   __builtin_amdgcn_sched_barrier(0);
   bool more = tiles.find();
   loads_done();
   if (more) {
-    load_keys(~0u);
-    load_values(~0u);
+    load_keys();
+    load_values();
   }
 #pragma unroll
   for (int m = 0; m < RT; ++m) {
 #pragma unroll
     for (int j = 0; j < QL; ++j) {
       const int k = ROWS_WAVES * j + w;
-      if (KS % ROWS_WAVES == 0 || k < KS) lds.q[m][k][lane] = query[m][j];
+      const uint4& u = query[m][j];
+      if (KS % ROWS_WAVES == 0 || k < KS)
+        lds.q[m][k][lane] = make_uint4(u.x ^ turn, u.y ^ turn, u.z ^ turn, u.w ^ turn);
     }
   }
   lds_barrier();
 
-  while (more) {
+  for (int count = 1; more; ++count) {
     const int now = tiles.p0;
     const bool whole = rows.all_see(a, now, F::TILE);
     f32x4 s[RT];
@@ -169,41 +177,58 @@ __device__ __forceinline__ void rows_run(const AttnArgs& a, const Set& set, int 
     const f32x4 ks_now = ks, vs = vs_next;
     __builtin_amdgcn_sched_barrier(0);
     more = tiles.find();
-    const uint32_t on = more ? ~0u : 0u;
-    load_keys(on);
+    load_keys();
     __builtin_amdgcn_sched_barrier(0);
 
     const int mine = now + 16 * w + 4 * lg;  // the position of the lane's first product
-    float v[RT][4];
+    float v[RT][4], largest[RT];
+    bool rises = false;
 #pragma unroll
     for (int m = 0; m < RT; ++m) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[m][i] = F::CODED ? s[m][i] * ks_now[i] : s[m][i];
-      if (!whole) hide(v[m], row_reach(m).template bits<4>(mine), a.scale_hi);
-      const float top = rows_max(fmaxf(fmaxf(v[m][0] * a.scale_hi, v[m][1] * a.scale_hi),
-                                       fmaxf(v[m][2] * a.scale_hi, v[m][3] * a.scale_hi)));
-      if (lg == 0) reinterpret_cast<float*>(&lds.tops[16 * m + li])[w] = top;
+      if (!whole) hide(v[m], row_reach(m).template bits<4>(mine), scale_hi);
+      largest[m] = fmaxf(fmaxf(v[m][0], v[m][1]), fmaxf(v[m][2], v[m][3])) * scale_hi;
+      rises |= largest[m] > mx[m] + 8.f;
     }
-    lds_barrier();
-    f32x4 tops[RT];
+    // Maxima move in the first tile and rarely behind it: only then are they taken over lanes and waves (64 rows of D = 64
+    // over 200,000 positions 117 -> 110 us).  Through a window always: runs are short, and prompts were slower (87 -> 89).
+    bool risen = SEEN == WINDOW || count == 1;
+    if (!risen) {
+      if (__any(rises) && lane == 0) lds.risen = count;
+      lds_barrier();
+      risen = __builtin_amdgcn_readfirstlane(lds.risen) == count;
+    }
+    if (risen) {
 #pragma unroll
-    for (int m = 0; m < RT; ++m) tops[m] = lds.tops[16 * m + li];
-    __builtin_amdgcn_sched_barrier(0);
+      for (int m = 0; m < RT; ++m) {
+        const float top = rows_max(largest[m]);
+        if (lg == 0) reinterpret_cast<float*>(&lds.tops[16 * m + li])[w] = top;
+      }
+      lds_barrier();
+      f32x4 tops[RT];
+#pragma unroll
+      for (int m = 0; m < RT; ++m) tops[m] = lds.tops[16 * m + li];
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int m = 0; m < RT; ++m) {
+        const float top = fmaxf(fmaxf(tops[m][0], tops[m][1]), fmaxf(tops[m][2], tops[m][3]));
+        if (__any(top > mx[m] + 8.f)) {
+          const float high = top > mx[m] + 8.f ? top : mx[m];  // a row's own: no row feels another's
+          const float f = exp2_of(mx[m] - high);
+          mx[m] = high;
+          sum[m] *= f;
+#pragma unroll
+          for (int d = 0; d < DL; ++d) acc[m][d] *= f;
+        }
+      }
+    }
 #pragma unroll
     for (int m = 0; m < RT; ++m) {
-      const float top = fmaxf(fmaxf(tops[m][0], tops[m][1]), fmaxf(tops[m][2], tops[m][3]));
-      if (__any(top > mx[m] + 8.f)) {
-        const float high = top > mx[m] + 8.f ? top : mx[m];
-        const float f = exp2_of(mx[m] - high);
-        mx[m] = high;
-        sum[m] *= f;
-#pragma unroll
-        for (int d = 0; d < DL; ++d) acc[m][d] *= f;
-      }
       f32x4 p;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        p[i] = exp2_of(__builtin_fmaf(v[m][i], a.scale_lo, __builtin_fmaf(v[m][i], a.scale_hi, -mx[m])));
+        p[i] = exp2_of(__builtin_fmaf(v[m][i], scale_lo, __builtin_fmaf(v[m][i], scale_hi, -mx[m])));
       sum[m] += (p[0] + p[1]) + (p[2] + p[3]);
       if constexpr (F::CODED) {
 #pragma unroll
@@ -281,7 +306,7 @@ __device__ __forceinline__ void rows_run(const AttnArgs& a, const Set& set, int 
     constexpr bool EARLY = F::CODED && D != 256;
     if constexpr (EARLY) {
       __builtin_amdgcn_sched_barrier(0);
-      load_values(on);
+      load_values();
       __builtin_amdgcn_sched_barrier(0);
     }
     lds_barrier();
@@ -308,7 +333,7 @@ __device__ __forceinline__ void rows_run(const AttnArgs& a, const Set& set, int 
     if (a.out_type == HCR_F32) products(std::integral_constant<int, 2>{}, std::integral_constant<int, 2 * RT>{});
     if constexpr (!EARLY) {
       __builtin_amdgcn_sched_barrier(0);
-      load_values(on);
+      load_values();
       __builtin_amdgcn_sched_barrier(0);
     }
   }
