@@ -969,10 +969,11 @@ __device__ __forceinline__ void part_of(const AttnArgs& a, const Run& run) {
   constexpr bool SEL = SEEN == LISTED;
   const int lane = threadIdx.x & 63;
   // work-group -> (run, kv head, row block); the row blocks of one run sit on one XCD (its L2 then serves all but
-  // the first)
+  // the first), the last one, which sees the most positions, ahead (a prompt of 2,048 tokens, 32 heads of 128 over 8:
+  // int8 82 against 104 us; of 4,096 in BF16 307 against 411)
   const int RB = a.plan.row_blocks;
   const int turn = blockIdx.x / XCDS;
-  const int rb = turn % RB;
+  const int rb = RB - 1 - turn % RB;
   const int u = turn / RB * XCDS + blockIdx.x % XCDS;
   const int h = u % a.c.kv_heads, item = u / a.c.kv_heads;
   if (item >= a.plan.items) return;

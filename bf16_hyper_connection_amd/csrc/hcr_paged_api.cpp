@@ -213,10 +213,13 @@ static int window_bound(const WindowArgs& w, int max_ctx, long long tokens, int 
 //   whole      a work-group a set where sets fill the chip and end soon.  D = 128, 24 rows: 64 sequences of 700 21
 //              against 34, of 4,000 97 against 87; 36 rows of D = 256: 32 of 700 33 against 36, 32 of 2,000 84 against 67,
 //              16 of 700 32 against 27.  Prompts of 2,048 through a window of 1,024 85 against 95
-//   fill       work-groups a CU: one for up to 7 tiles, two for up to 31, else what registers leave room for; fewer, longer
-//              runs leave less to join and wait for their first loads less often.  36 rows of D = 256: 16 of 700 23.7 with
-//              one, 28 with two; 16 of 2,000 23.5 with two, 29 with one; one of 30,000 47 with two, 53 with three.  24 rows
-//              through a window of 8,192 21.5 with one, 24 with three; D = 128, one of 4,000 13.0 with one, 15.4 with four
+//   fill       work-groups a CU, by the tiles there are for each: one for up to 7, two for up to 15 (D = 256 31), three
+//              for up to 31, else what registers leave room for; fewer, longer runs leave less to join and wait for their
+//              first loads less often.  36 rows of D = 256: 16 of 700 23.5 with one, 28 with two; 16 of 2,000 38 with two,
+//              42 with one, 40 with three; one of 60,000 78 with two, 80 with three.  24 rows: D = 128, one of 4,000 12.7
+//              with one, 14.0 with two; 4 of 9,000 21.1 with three, 22.3 with two; one of 80,000 48.1 with four, 51.5 with
+//              three; D = 64, 4 of 9,000 18.7 with three, 20.5 with two.  24 rows through a window of 8,192 21.5 with one,
+//              23 with three
 static AttnPlan rows_plan(const CacheArgs& c, bool codes, const WindowArgs& w, const BatchArgs& b, int group, int n_sel) {
   constexpr int CUS = 256;
   AttnPlan p{};
@@ -235,7 +238,7 @@ static AttnPlan rows_plan(const CacheArgs& c, bool codes, const WindowArgs& w, c
   const long long even = (full * tiles + CUS - 1) / CUS;  // of a CU
   p.least = 1;
   const int held = rows_held(codes, c.head_dim, p.q_tiles);
-  const int fill = CUS * (even < 8 ? 1 : even < 32 ? 2 : held);
+  const int fill = CUS * (even < 8 ? 1 : even < 16 || (c.head_dim == 256 && even < 32) ? 2 : even < 32 ? 3 : held);
   const long long runs = tiles > 0 ? tiles : 1;
   long long items = fill / units;
   if (n_sel) {
