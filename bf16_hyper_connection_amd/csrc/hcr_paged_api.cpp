@@ -210,9 +210,15 @@ static int window_bound(const WindowArgs& w, int max_ctx, long long tokens, int 
 
 // Work-groups of four waves that share their rows (hcr_attn_rows.h), up to four row tiles each.  As few row blocks as hold
 // the rows, each with as few row tiles: a block reads the set's keys and values once.  Measured (us a call, graphs):
+//   most       prompts whose blocks of 64 rows are fewer than two a CU (by the tokens there are, whatever the bounds): blocks
+//              of 32, where those then take whole sets; a work-group alone on a CU is mostly waits.  Int8, 32 heads over 8:
+//              one prompt of 512 15.5 against 20.9, of 1,000 28 against 36, 4 of up to 256 behind 2,048 48 against 63, one
+//              of 512 through a window of 1,024 (BF16) 31 against 69.  Not where the chip is full of them (2 of 1,024 at
+//              4,096, D = 256: 332 against 303) or where runs are cut (256 at 8,192: 106 against 93)
 //   whole      a work-group a set where sets fill the chip and end soon.  D = 128, 24 rows: 64 sequences of 700 21
-//              against 34, of 4,000 97 against 87; 36 rows of D = 256: 32 of 700 33 against 36, 32 of 2,000 84 against 67,
-//              16 of 700 32 against 27.  Prompts of 2,048 through a window of 1,024 85 against 95
+//              against 34, of 4,000 97 against 87, 128 of 4,000 121 against 155; 36 rows of D = 256: 32 of 700 33 against
+//              36, 32 of 2,000 84 against 67, 16 of 700 32 against 27.  8 prompts of up to 512 at 4,096 200 against 295.
+//              Never beyond 4,096 positions, as above
 //   fill       work-groups a CU, by the tiles there are for each: one for up to 7, two for up to 15 (D = 256 31), three
 //              for up to 31, else what registers leave room for; fewer, longer runs leave less to join and wait for their
 //              first loads less often.  36 rows of D = 256: 16 of 700 23.5 with one, 28 with two; 16 of 2,000 38 with two,
@@ -226,15 +232,26 @@ static AttnPlan rows_plan(const CacheArgs& c, bool codes, const WindowArgs& w, c
   p.shared = 1;
   const int rows = n_sel ? group : b.max_tokens * group;
   const int row_tiles = ceil_div(rows, 16);
-  p.row_blocks = ceil_div(row_tiles, 4);
+  const long long sets = n_sel ? b.n_tokens : b.n_seqs;
+  const auto full_of = [&](int most) { return sets * c.kv_heads * ceil_div(row_tiles, most); };  // work-groups of whole sets
+  const auto tiles_of = [&](int row_blocks) {
+    const int block = ceil_div(16 * ceil_div(row_tiles, row_blocks), group) + 1;  // tokens of a row block
+    return n_sel ? n_sel << (c.shift - ROWS_SHIFT)
+                 : window_bound(w, b.max_ctx, block < b.max_tokens ? block : b.max_tokens, ROWS_SHIFT);
+  };
+  const auto whole_of = [&](long long full, int tiles) {
+    return full < CUS ? tiles <= 4 : full < 2 * CUS ? tiles <= 16 : full < 4 * CUS ? tiles <= 32 : tiles <= 64;
+  };
+  int most = 4;
+  if (!n_sel && row_tiles > 4 && (long long)c.kv_heads * ceil_div(b.n_tokens * group, 64) < 2 * CUS &&
+      full_of(2) >= 2 * CUS && whole_of(full_of(2), tiles_of(ceil_div(row_tiles, 2))))
+    most = 2;
+  p.row_blocks = ceil_div(row_tiles, most);
   p.q_tiles = ceil_div(row_tiles, p.row_blocks);
   p.row_waves = p.groups = 1;
-  const int block = ceil_div(16 * p.q_tiles, group) + 1;  // tokens of a row block
-  const int tiles = n_sel ? n_sel << (c.shift - ROWS_SHIFT)
-                          : window_bound(w, b.max_ctx, block < b.max_tokens ? block : b.max_tokens, ROWS_SHIFT);
-  const long long sets = n_sel ? b.n_tokens : b.n_seqs, units = (long long)c.kv_heads * p.row_blocks;
-  const long long full = sets * units;
-  p.whole = full < CUS ? tiles <= 4 : full < 2 * CUS ? tiles <= 16 : tiles <= 32;
+  const int tiles = tiles_of(p.row_blocks);
+  const long long units = (long long)c.kv_heads * p.row_blocks, full = sets * units;
+  p.whole = whole_of(full, tiles);
   const long long even = (full * tiles + CUS - 1) / CUS;  // of a CU
   p.least = 1;
   const int held = rows_held(codes, c.head_dim, p.q_tiles);
