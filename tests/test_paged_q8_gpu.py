@@ -296,6 +296,29 @@ def test_attend_many_rows(kind, head_dim, kv, group, T):
 
 
 @pytest.mark.parametrize("kind", cu.KINDS)
+@pytest.mark.parametrize("head_dim,kv,group,T", [(64, 1, 16, 20), (128, 2, 10, 17), (256, 1, 24, 14)])
+def test_attend_ragged_prompts(kind, head_dim, kv, group, T):
+    """Far fewer tokens than the bounds allow, over many sequences: smaller row blocks, most of them empty."""
+    g = gen.rng(118, head_dim)
+    s = cu.scene(kind, 86, kv, head_dim, 64,
+                 [(int(t), int(t) + int(c)) for t, c in zip(g.integers(0, 4, 60), g.integers(0, 200, 60))] + [(T, 400), (T, T)])
+    out, want, tol = cu.attend(s, kv * group, out_dtype=torch.bfloat16)
+    pu.check_rows(out, want, tol, "ragged prompts")
+
+
+@pytest.mark.parametrize("kind", cu.KINDS)
+@pytest.mark.parametrize("head_dim,group", [(64, 64), (128, 40), (256, 33)])
+def test_attend_whole_sets_that_fill_the_chip(kind, head_dim, group):
+    """Many sets of many rows, up to 4,096 positions: a work-group each row block and set, nothing joined."""
+    g = gen.rng(119, head_dim)
+    windows = [(int(t), int(t) + int(c)) for t, c in zip(g.integers(0, 9, 250), g.integers(0, 70, 250))]
+    windows[100], windows[249] = (8, 4096), (8, 2049)
+    s = cu.scene(kind, 87, 1, head_dim, 64, windows)
+    out, want, tol = cu.attend(s, group, out_dtype=torch.bfloat16)
+    pu.check_rows(out, want, tol, "whole sets")
+
+
+@pytest.mark.parametrize("kind", cu.KINDS)
 @pytest.mark.parametrize("head_dim,page,kv,group,T", [(128, 64, 1, 4, 1), (256, 64, 2, 6, 2), (64, 128, 1, 8, 4),
                                                       (128, 256, 1, 16, 5), (256, 64, 1, 8, 8)])
 @pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])

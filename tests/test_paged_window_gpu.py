@@ -62,6 +62,18 @@ def test_prompts(kind, head_dim, kv, group, T, window, n_first):
     pu.check_rows(out, want, tol, "prompts")
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("head_dim,kv,group,T", [(64, 1, 16, 20), (128, 2, 10, 17), (256, 1, 24, 14)])
+@pytest.mark.parametrize("window,n_first", [(50, 4), (130, 0)])
+def test_ragged_prompts(kind, head_dim, kv, group, T, window, n_first):
+    """Far fewer tokens than the bounds allow, over many sequences: smaller row blocks, most of them empty."""
+    g = gen.rng(120, head_dim)
+    s = cu.scene(kind, 143, kv, head_dim, 64,
+                 [(int(t), int(t) + int(c)) for t, c in zip(g.integers(0, 4, 60), g.integers(0, 300, 60))] + [(T, 400), (T, T)])
+    out, want, tol = cu.attend(s, kv * group, window=window, n_first=n_first)
+    pu.check_rows(out, want, tol, "ragged prompts")
+
+
 @pytest.mark.parametrize("head_dim,kv,group,T", [(128, 1, 4, 1), (64, 2, 8, 5), (256, 1, 6, 9), (128, 1, 17, 40),
                                                  (64, 1, 64, 3), (256, 1, 33, 20)])
 @pytest.mark.parametrize("window,n_first", [(1, 0), (40, 5), (33, 33), (900, 70)])
