@@ -226,7 +226,7 @@ static int window_bound(const WindowArgs& w, int max_ctx, long long tokens, int 
 //              with one, 14.0 with two; 4 of 9,000 21.1 with three, 22.3 with two; one of 80,000 48.1 with four, 51.5 with
 //              three; D = 64, 4 of 9,000 18.7 with three, 20.5 with two.  24 rows through a window of 8,192 21.5 with one,
 //              23 with three
-static AttnPlan rows_plan(const CacheArgs& c, bool codes, const WindowArgs& w, const BatchArgs& b, int group, int n_sel) {
+static AttnPlan rows_plan(const CacheArgs& c, const WindowArgs& w, const BatchArgs& b, int group, int n_sel) {
   constexpr int CUS = 256;
   AttnPlan p{};
   p.shared = 1;
@@ -254,7 +254,7 @@ static AttnPlan rows_plan(const CacheArgs& c, bool codes, const WindowArgs& w, c
   p.whole = whole_of(full, tiles);
   const long long even = (full * tiles + CUS - 1) / CUS;  // of a CU
   p.least = 1;
-  const int held = rows_held(codes, c.head_dim, p.q_tiles);
+  const int held = rows_held(c.head_dim, p.q_tiles);
   const int fill = CUS * (even < 8 ? 1 : even < 16 || (c.head_dim == 256 && even < 32) ? 2 : even < 32 ? 3 : held);
   const long long runs = tiles > 0 ? tiles : 1;
   long long items = fill / units;
@@ -277,7 +277,7 @@ static AttnPlan rows_plan(const CacheArgs& c, bool codes, const WindowArgs& w, c
 AttnPlan attn_plan_more(const CacheArgs& c, const CodeArgs& x, const WindowArgs& w, const BatchArgs& b, int heads,
                         int n_sel) {
   const int group = heads / c.kv_heads, rows = (n_sel ? 1 : b.max_tokens) * group;
-  if (rows > 16 && c.shift >= ROWS_SHIFT) return rows_plan(c, coded(x), w, b, group, n_sel);
+  if (rows > 16 && c.shift >= ROWS_SHIFT) return rows_plan(c, w, b, group, n_sel);
   const int shift = tile_shift(coded(x), c.head_dim);
   const int tiles = n_sel ? n_sel << (c.shift - shift) : window_bound(w, b.max_ctx, b.max_tokens, shift);
   AttnPlan p = plan_for(c, b, heads, n_sel, tiles, true);

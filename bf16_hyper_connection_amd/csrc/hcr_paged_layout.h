@@ -104,10 +104,9 @@ HCR_HD bool code_page_ok(int page) { return page_ok(page) && page >= 64; }
 constexpr int attn_waves(int D, int q_tiles) { return D == 64 ? 16 : D == 256 && q_tiles > 1 ? 4 : 8; }
 // Work-groups of four waves that share their rows, on a CU: the registers are held to that.  As many as spill no more
 // than a dozen of them (measured, codes: D = 128, 20 rows of 200,000 positions 103 us with four, 113 with two; D = 64 70
-// against 84; D = 256, 36 rows of 100,000 117 with three, 118 with two).
-constexpr int rows_held(bool codes, int D, int q_tiles) {
-  return D == 256 ? (q_tiles > (codes ? 3 : 2) ? 2 : 3) : D == 128 && q_tiles > 2 ? 3 : 4;
-}
+// against 84, 64 rows through a window of 1,024 68 with four, 77 with three; D = 256, 36 rows of 100,000, E4M3 97 with two,
+// 113 with three, which spill 27, int8 108 with either, 4 sequences of up to 9,001 38 against 42).
+constexpr int rows_held(int D, int q_tiles) { return D == 256 ? (q_tiles > 2 ? 2 : 3) : D == 128 && q_tiles > 2 ? 3 : 4; }
 
 // How a call is cut.  Its sets of rows (a sequence's window; one token for listed pages) have their tiles one set
 // behind the other, and the work-groups of a kv head and row block take equal runs of them: as many work-groups as
