@@ -9,8 +9,6 @@
 // Bound by the bytes.  Measured on MI355X: 51,190 positions of 8 sequences, 8 kv heads of 128, int8 to BF16 (318 MB) 71
 // us, 4.5 TB/s, where a 4 GiB device copy moves 4.7.  On the way there: 32 positions a work-group 85 us; 64 positions, 16
 // bytes of a lane's own row at a time 83; neighbouring lanes' 16 bytes beside each other and stores past the caches 71.
-#include <type_traits>
-
 #include "hcr_append_device.h"
 
 namespace hcr {
@@ -22,45 +20,57 @@ __device__ __forceinline__ void put16(void* p, const T& v) {
   __builtin_nontemporal_store(v, static_cast<T*>(p));
 }
 
-// 8 values of a page, as loaded; a lane's share of a row, so that neighbouring lanes store neighbouring 16 bytes.
-template <int CODE>
-using Eight = std::conditional_t<CODE == HCR_BF16, uint4, uint2>;
-template <int CODE>
-__device__ __forceinline__ Eight<CODE> load_eight(const void* p) {
-  if constexpr (CODE == HCR_BF16)
-    return ldw16(p);
-  else
-    return ldw8(p);
-}
-// Times a scale in FP32, stored; `none`: zeros.
-template <int CODE, bool F32>
-__device__ __forceinline__ void store_eight(const Eight<CODE>& u, float scale, bool none, void* out, size_t at) {
-  Values x{};
-  if (!none) {
-    if constexpr (CODE == HCR_BF16) {
-      Raw<false> r;
-      r.u[0] = u;
-      x = values<false>(r);
+// N values of a page, as loaded: a lane's share of a row.
+template <int CODE, int N>
+struct Share {
+  static constexpr int WORDS = N * (CODE == HCR_BF16 ? 2 : 1) / 4;
+  alignas(4 * WORDS) uint32_t w[WORDS];
+  __device__ __forceinline__ void load(const void* p) {
+    if constexpr (WORDS == 4) {
+      const uint4 u = ldw16(p);
+      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    } else if constexpr (WORDS == 2) {
+      const uint2 u = ldw8(p);
+      w[0] = u.x, w[1] = u.y;
     } else {
-      x = code_values<CODE>(u);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x.v[e] *= scale;
+      w[0] = ldw4(p);
     }
   }
+  __device__ __forceinline__ void values(float (&x)[N]) const {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      if constexpr (CODE == HCR_BF16) {
+        x[e] = __uint_as_float(w[e / 2] << 16);
+        x[e + 1] = __uint_as_float(w[e / 2] & 0xFFFF0000u);
+      } else if constexpr (CODE == HCR_INT8) {
+        x[e] = code(w[e / 4], e % 4);
+        x[e + 1] = code(w[e / 4], e % 4 + 1);
+      } else {
+        const f32x2 v = e % 4 ? __builtin_amdgcn_cvt_pk_f32_fp8(w[e / 4], true)
+                              : __builtin_amdgcn_cvt_pk_f32_fp8(w[e / 4], false);
+        x[e] = v[0];
+        x[e + 1] = v[1];
+      }
+    }
+  }
+};
+// Times a scale in FP32, stored; `none`: zeros.
+template <bool F32, int CODE, int N>
+__device__ __forceinline__ void store_share(const Share<CODE, N>& u, float scale, bool none, void* out, size_t at) {
+  float x[N] = {};
+  if (!none) {
+    u.values(x);
+#pragma unroll
+    for (int e = 0; e < N; ++e) x[e] = CODE == HCR_BF16 ? x[e] : x[e] * scale;
+  }
   if constexpr (F32) {
-    float* to = static_cast<float*>(out) + at;
-    put16(to, f32x4{x.v[0], x.v[1], x.v[2], x.v[3]});
-    put16(to + 4, f32x4{x.v[4], x.v[5], x.v[6], x.v[7]});
+#pragma unroll
+    for (int e = 0; e < N; e += 4)
+      put16(static_cast<float*>(out) + at + e, f32x4{x[e], x[e + 1], x[e + 2], x[e + 3]});
   } else {
-    const uint4 r = round8(x);
+    const uint4 r = round8(Values{{x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]}});
     put16(static_cast<uint16_t*>(out) + at, u32x4_t{r.x, r.y, r.z, r.w});
   }
-}
-
-// Byte of the c-th 8 dimensions of a slot's key.
-template <bool CODED>
-__device__ __forceinline__ int k_eight(int shift, int s, int c) {
-  return CODED ? k_code_at(shift, s, 8 * c) : 2 * k_at(shift, s, 8 * c);
 }
 
 template <int D, int CODE, bool F32>
@@ -68,8 +78,11 @@ __global__ __launch_bounds__(READ_THREADS) void cache_read(ReadArgs a, int parts
   constexpr bool CODED = CODE != HCR_BF16;
   constexpr int BYTES = CODED ? 1 : 2, EACH = 16 / BYTES;  // of a value; values in 16 bytes
   constexpr int ROW = D * BYTES + 16;                      // a row in LDS, 16 bytes more: rows start in other banks
-  constexpr int LANES = D / 8;                             // of a row
-  constexpr int ITEMS = READ_SLOTS * LANES / READ_THREADS;   // eights of a thread
+  // values of a lane's share: 16 bytes of its row, so that a wave stores whole lines (int8 to floats, D = 256: 116 us against
+  // 133 with 32 bytes); of BF16 8 for floats too (128 against 136), whose loads would else be of 8 bytes
+  constexpr int OUT = F32 && CODED ? 4 : 8;
+  constexpr int LANES = D / OUT;                           // of a row
+  constexpr int ITEMS = READ_SLOTS * LANES / READ_THREADS;  // shares of a thread
   constexpr int N = 4 / BYTES;                             // dimensions of a thread's values
   constexpr int VITEMS = (READ_SLOTS / EACH * (D / N) + READ_THREADS - 1) / READ_THREADS;
   static_assert(ITEMS * READ_THREADS == READ_SLOTS * LANES && READ_SLOTS == 64, "a part has whole passes");
@@ -120,14 +133,14 @@ __global__ __launch_bounds__(READ_THREADS) void cache_read(ReadArgs a, int parts
     }
   }
   if (a.k_out) {
-    Eight<CODE> u[ITEMS];
+    Share<CODE, OUT> u[ITEMS];
     float scale[ITEMS];
 #pragma unroll
     for (int t = 0; t < ITEMS; ++t) {  // neighbouring lanes: a row's values; 64 / LANES rows a wave
       const int i = tid + t * READ_THREADS, s = i / LANES, c = i % LANES, k = s / 32;
       if (start + s < lo || start + s >= hi) continue;
-      const int in = k_eight<CODED>(a.c.shift, (k ? slot[1] : slot[0]) + s % 32, c);
-      u[t] = load_eight<CODE>((k ? kp[1] : kp[0]) + in);
+      const int at = (k ? slot[1] : slot[0]) + s % 32;
+      u[t].load((k ? kp[1] : kp[0]) + (CODED ? k_code_at(a.c.shift, at, OUT * c) : 2 * k_at(a.c.shift, at, OUT * c)));
       if constexpr (CODED) scale[t] = a.code.k_scales[(k ? scales[1] : scales[0]) + s % 32];
     }
 #pragma unroll
@@ -135,8 +148,8 @@ __global__ __launch_bounds__(READ_THREADS) void cache_read(ReadArgs a, int parts
       const int i = tid + t * READ_THREADS, s = i / LANES, c = i % LANES, k = s / 32;
       const int p = start + s;
       if (p >= lo && p < hi)
-        store_eight<CODE, F32>(u[t], CODED ? scale[t] : 1.f, (k ? number[1] : number[0]) < 0, a.k_out,
-                               ((size_t)(seq.row + p - seq.first) * a.c.kv_heads + h) * D + 8 * c);
+        store_share<F32>(u[t], CODED ? scale[t] : 1.f, (k ? number[1] : number[0]) < 0, a.k_out,
+                    ((size_t)(seq.row + p - seq.first) * a.c.kv_heads + h) * D + OUT * c);
     }
   }
   if (!a.v_out) return;
@@ -167,9 +180,9 @@ __global__ __launch_bounds__(READ_THREADS) void cache_read(ReadArgs a, int parts
     const int p = start + s;
     if (p < lo || p >= hi) continue;
     const float scale = CODED ? a.code.v_scales[(k ? scales[1] : scales[0]) + s % 32] : 1.f;
-    store_eight<CODE, F32>(*reinterpret_cast<const Eight<CODE>*>(&tile[s * ROW + 8 * BYTES * c]), scale,
-                           (k ? number[1] : number[0]) < 0, a.v_out,
-                           ((size_t)(seq.row + p - seq.first) * a.c.kv_heads + h) * D + 8 * c);
+    store_share<F32>(*reinterpret_cast<const Share<CODE, OUT>*>(&tile[s * ROW + OUT * BYTES * c]), scale,
+                (k ? number[1] : number[0]) < 0, a.v_out,
+                ((size_t)(seq.row + p - seq.first) * a.c.kv_heads + h) * D + OUT * c);
   }
 }
 
