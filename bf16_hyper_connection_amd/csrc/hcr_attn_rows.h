@@ -14,8 +14,8 @@
 // a window of 1,024 (32 heads of 128 over 8, BF16, 64 rows a work-group) a tile takes one 2.4 us alone and three of them
 // 2.4 together, vector instructions being issued in three quarters of the clocks; over codes widening comes on top (E4M3 2
 // instructions for 4 codes, int8 6), exponents and the three BF16 parts of float outputs.  Measured on MI355X: those
-// prompts (2,049 tokens, 34.5 GFLOP) 83 us, 0.42 PFLOP/s; 36 rows of 4 sequences of up to 9,001 (int8, D = 256, float
-// outputs) 31 us, 2.7 TB/s, and 6 for the join: 9 tiles a work-group behind the waits for its first loads; of one of
+// prompts (2,049 tokens, 34.5 GFLOP) 82 us, 0.42 PFLOP/s; 36 rows of 4 sequences of up to 9,001 (int8, D = 256, float
+// outputs) 30 us, 2.9 TB/s, and 7 for the join: 9 tiles a work-group behind the waits for its first loads; of one of
 // 100,000 114 us, 3.7 TB/s (24 rows 97); 24 rows through a window of 8,192 17 us and 4 for the join.
 #pragma once
 
