@@ -261,13 +261,20 @@ __device__ __forceinline__ uint2 quantised(const Values& x, float& scale) {
   top = head_top<LANES>(top);
   scale = __uint_as_float(top) / TOP;
   if (top >= 0x7F800000u) scale = __uint_as_float(0x7FC00000u);  // a value that is not finite: the head is NaN
-  // one inverse for the head's quotients, a rounding more than a division each (with divisions those prompts took
-  // 27.3 us); divisions where it would be infinite or the scale has few bits
+  // FP32's quotient, correctly rounded, from one inverse for the head: the product is off by less than two steps, the first
+  // correction leaves it within one of the quotient, and from there the second is exact (Markstein's theorem: the inverse
+  // is FP32's own, and the remainder is exact).  4,352 tokens of 32 + 16 heads of 128: 29.8 us with divisions, 28.0 so, and
+  // 27.3 with the product alone, which takes another code for one value in 2,000 of BF16 rows.  Divisions where the
+  // remainder may fall below FP32's range; a scale of few bits may be well below max / top, so codes stop at top.
   const float inverse = 1.f / scale;
-  const bool small = !(scale >= 0x1p-100f);
+  const bool small = !(scale >= 0x1p-60f);
   float c[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) c[e] = x.v[e] * inverse;
+  for (int e = 0; e < 8; ++e) {
+    c[e] = x.v[e] * inverse;
+    c[e] = __builtin_fmaf(__builtin_fmaf(-c[e], scale, x.v[e]), inverse, c[e]);
+    c[e] = __builtin_fmaf(__builtin_fmaf(-c[e], scale, x.v[e]), inverse, c[e]);
+  }
   if (__any(small)) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) c[e] = scale > 0.f ? (small ? x.v[e] / scale : c[e]) : 0.f;

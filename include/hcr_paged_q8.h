@@ -9,12 +9,10 @@
  *   scale = max |y| / top        FP32, one for each position and kv head
  *   code  = y / scale, to the nearest code, ties to the even one;  it stands for code * scale
  *
- * (the quotient in FP32, within two roundings: a y that lies that close to the middle of two
- * codes may take either)
- *
- * so that what a position holds depends on that position alone, however windows were cut
- * and whatever was written over.  A head that holds a value that is not finite has the
- * scale NaN and stands for NaN as a whole; zeros have the scale 0.  hcr_attn and
+ * (both quotients are FP32's, correctly rounded; codes stop at top), so that what a position
+ * holds depends on that position alone, however windows were cut and whatever was written
+ * over.  A head that holds a value that is not finite has the scale NaN and stands for NaN as
+ * a whole; zeros, and heads whose scale rounds to 0, have the scale 0.  hcr_attn and
  * hcr_attn_blocks attend over what the codes stand for, in FP32; hcr_block_scores and
  * hcr_block_topk take such a cache as any other (mean keys are of what the codes stand for).
  * Pages that were filled otherwise may hold any codes and scales: a key that is no number (the
