@@ -33,7 +33,8 @@
 // runs are joined by a second launch; each join is (m, l, O) -> (max, sum of l 2^(m - max), sum of O 2^(m - max)),
 // in a fixed order.  Where the chip is full of sequences or they are short, a work-group takes a whole one instead and
 // nothing is left to join (there a long one among short ones, or a bound far above them, does cost: the plan's rule
-// keeps that to sequences of 4,096).
+// keeps that to sequences of 4,096).  Where prompts and single tokens share a batch, the pairs of a sequence and a row
+// block are cut, as many as the device finds, in place of each row block's sequences (pair_cut).
 //
 // Bound by the bytes of keys and values.  Measured on MI355X (graphs of calls, inputs rotated): one sequence of
 // 420,000 positions, 48 heads of 256 over 8, 2 tokens: 505 us, 6.8 TB/s (a 4 GiB device copy moves 4.8); 64 sequences
@@ -297,6 +298,97 @@ __device__ __forceinline__ Set next_seq(const AttnArgs& a, const Set& s, int lan
     }
   }
   return Set{Seq{0, 0, 0}, -1, 0, first, 0};
+}
+
+// How the pairs of the sequences and their row blocks are cut (AttnPlan::paired).
+template <int SHIFT>
+__device__ __forceinline__ PairCut cut_of_pairs(const AttnArgs& a, const Seq& s0, int lane) {
+  if (a.plan.whole) return pair_cut(a.plan, 0, 0, 0, 0);
+  long long tiles = 0;
+  int pairs = 0, fewest = 1 << 30, most = 0;
+  for (int i = 0; i < a.b.n_seqs; i += 64) {
+    const Seq s = i == 0 ? s0 : lane_seq(a.b, i, lane);
+    const int blocks = set_blocks(a.plan, s.tokens * a.group);
+    pairs += blocks;
+    tiles += (long long)blocks * pair_tiles(a.plan, a.window, s, a.group, SHIFT);
+    fewest = blocks ? min(fewest, blocks) : fewest;
+    most = max(most, blocks);
+  }
+  for (int o = 32; o; o >>= 1) {
+    pairs += __shfl_xor(pairs, o);
+    tiles += __shfl_xor(tiles, o);
+    fewest = min(fewest, __shfl_xor(fewest, o));
+    most = max(most, __shfl_xor(most, o));
+  }
+  const PairCut c = pair_cut(a.plan, tiles, pairs, fewest, most);
+  return PairCut{__builtin_amdgcn_readfirstlane(c.kind), __builtin_amdgcn_readfirstlane(c.run),
+                 __builtin_amdgcn_readfirstlane(c.blocks)};
+}
+// A pair that is cut EVEN or APART: the one that run x begins in, or (x < 0) that of row `row`, head g of its group.  A set's
+// row blocks stand from the last on, which sees the most positions; of pairs APART the runs of the same tiles stand
+// together.
+struct Pair {
+  Set set;  // EVEN: its first tile among all; APART: its tiles from 0 on
+  int rb;
+  int part, parts, each;  // APART: the run (of x), how many there are, and their tiles,
+  int slot, step;         // the place of its first part, and how far the next ones are from each other
+};
+template <int SHIFT>
+__device__ __forceinline__ Pair find_pair(const AttnArgs& a, const PairCut& cut, const Seq& s0, int x, int row, int g,
+                                          int lane) {
+  const BatchArgs& b = a.b;
+  const bool even = cut.kind == EVEN;
+  const int want = even ? x * cut.run : x;  // (x is under the shares, tiles under 2^30)
+  int before = 0, slots = 0;
+  for (int i = 0; i < b.n_seqs; i += 64) {
+    const Seq s = i == 0 ? s0 : lane_seq(b, i, lane);
+    const int blocks = set_blocks(a.plan, s.tokens * a.group), tiles = pair_tiles(a.plan, a.window, s, a.group, SHIFT);
+    const PairRuns r = even ? PairRuns{tiles, 1} : pair_runs(tiles, cut.run);
+    const int n = blocks * r.parts, split = r.parts > 1 ? n : 0;  // tiles, or runs
+    const int upto = before + lane_prefix(n, lane, b.n_seqs - i), slots_upto = slots + lane_prefix(split, lane, b.n_seqs - i);
+    const bool mine = x >= 0 ? upto - n <= want && want < upto : row >= s.row && row < s.row + s.tokens;
+    const unsigned long long at = __ballot(mine);
+    if (at) {
+      const int l = __ffsll(at) - 1;
+      const int first = __builtin_amdgcn_readlane(upto - n, l), sets_blocks = __builtin_amdgcn_readlane(blocks, l);
+      Pair p;
+      p.set = Set{of_lane(s, l), i + l, 0, 0, __builtin_amdgcn_readlane(tiles, l)};
+      p.parts = __builtin_amdgcn_readlane(r.parts, l);
+      p.each = __builtin_amdgcn_readlane(r.each, l);
+      const int from_last = x < 0 ? sets_blocks - 1 - ((row - p.set.seq.row) * a.group + g) / attn_rows(a.plan)
+                            : even ? (want - first) / p.set.tiles
+                                   : (want - first) % sets_blocks;
+      p.rb = sets_blocks - 1 - from_last;
+      p.part = x < 0 || even ? 0 : (want - first) / sets_blocks;
+      if (even) p.set.first = first + from_last * p.set.tiles;
+      p.slot = __builtin_amdgcn_readlane(slots_upto - split, l) + from_last;
+      p.step = sets_blocks;
+      return p;
+    }
+    const int last = min(b.n_seqs - i, 64) - 1;
+    before = __builtin_amdgcn_readlane(upto, last);
+    slots = __builtin_amdgcn_readlane(slots_upto, last);
+  }
+  return Pair{Set{Seq{0, 0, 0}, -1, 0, 0, 0}, 0, 0, 1, 1, 0, 1};
+}
+// The pair behind this one where they are cut EVEN.
+template <int SHIFT>
+__device__ __forceinline__ Set next_pair(const AttnArgs& a, const Set& s, int& rb, int lane) {
+  if (rb > 0) {
+    --rb;
+    return Set{s.seq, s.b, 0, s.first + s.tiles, s.tiles};
+  }
+  for (int b = s.b + 1; b < a.b.n_seqs; b += 64) {
+    const Seq q = lane_seq(a.b, b, lane);
+    const unsigned long long at = __ballot(q.tokens > 0);
+    if (at) {
+      const int l = __ffsll(at) - 1;
+      const Seq found = of_lane(q, l);
+      rb = set_blocks(a.plan, found.tokens * a.group) - 1;
+      return Set{found, b + l, 0, s.first + s.tiles, pair_tiles(a.plan, a.window, found, a.group, SHIFT)};
+    }
+  }
+  return Set{Seq{0, 0, 0}, -1, 0, 0, 0};
 }
 
 // Entry idx of a row's list of pages (behind its end the last one, which no tile takes).
@@ -963,89 +1055,148 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
   }
 }
 
-// A work-group's part of a call: its kv head, row block and tiles, set by set.
-template <int SHIFT, int SEEN, class Run>
+// A work-group's part of a call: its kv head, row block and tiles, set by set.  PAIRED: of a call that has AttnPlan::paired (a
+// kernel of its own, so that others do not hold its registers).
+template <int SHIFT, int SEEN, bool PAIRED, class Run>
 __device__ __forceinline__ void part_of(const AttnArgs& a, const Run& run) {
   constexpr bool SEL = SEEN == LISTED;
   const int lane = threadIdx.x & 63;
   // work-group -> (run, kv head, row block); the row blocks of one run sit on one XCD (its L2 then serves all but
   // the first), the last one, which sees the most positions, ahead (a prompt of 2,048 tokens, 32 heads of 128 over 8:
   // int8 82 against 104 us; of 4,096 in BF16 307 against 411)
-  const int RB = a.plan.row_blocks;
+  int RB = a.plan.row_blocks;
   const int turn = blockIdx.x / XCDS;
-  const int rb = RB - 1 - turn % RB;
-  const int u = turn / RB * XCDS + blockIdx.x % XCDS;
-  const int h = u % a.c.kv_heads, item = u / a.c.kv_heads;
-  if (item >= a.plan.items) return;
+  int rb = RB - 1 - turn % RB;
+  const int u = PAIRED ? blockIdx.x : turn / RB * XCDS + blockIdx.x % XCDS;
+  const int h = u % a.c.kv_heads;
+  int item = u / a.c.kv_heads;
   Cut cut;
   Set set;
   int entry = 0, begin = 0;
-  const Count<SEEN, SHIFT> tiles_of(a, rb);
-  if (SEL) {
-    const Lists<SHIFT> lists(a);
-    const int row = item / lists.runs;
-    if (row >= a.b.n_tokens) return;
-    begin = item * lists.run;
-    cut = Cut{lists.run, true};
-    // the list's load goes out beside the sequence's, one wait less (4 tokens, 64 pages
-    // of 64, D = 256: 28.7 against 29.7 us)
-    entry = listed(a, row, h, ((begin - row * lists.runs * lists.run) >> (a.c.shift - SHIFT)) + lane);
-    set = lists.set(a, row, lane);
-  } else if (a.plan.whole) {
-    set = seq_set(a.b, item, tiles_of);
-    cut = Cut{set.tiles, true};
-  } else {
-    set = find_seq(a.b, item, 0, lane, a.plan, tiles_of, &cut);
-    begin = item * cut.run;
+  size_t slot = (size_t)h * attn_slots(a.plan);
+  const size_t slots = (size_t)a.c.kv_heads * attn_slots(a.plan);
+  bool pairs = false;  // cut EVEN or APART
+  if constexpr (PAIRED) {
+    if (item >= a.plan.paired) return;
+    const Seq s0 = lane_seq(a.b, 0, lane);
+    const PairCut c = cut_of_pairs<SHIFT>(a, s0, lane);
+    if (!a.plan.whole && blockIdx.x == 0 && threadIdx.x == 0)
+      *reinterpret_cast<PairCut*>(a.part + slots * attn_rows(a.plan) * (a.c.head_dim + 2)) = c;
+    if (c.kind == ALIKE) {
+      RB = c.blocks;
+      rb = RB - 1 - item % RB;
+      item /= RB;
+    } else {
+      if (c.kind == EVEN && item >= a.plan.shares) return;
+      const Pair p = find_pair<SHIFT>(a, c, s0, item, 0, 0, lane);
+      pairs = true;
+      set = p.set;
+      rb = p.rb;
+      if (c.kind == EVEN) {
+        begin = item * c.run;
+        cut = Cut{c.run, false};
+        slot += part_slot(item, c.run, set.first);
+      } else {
+        begin = p.part * p.each;
+        cut = Cut{p.each, true};
+        slot += p.slot + p.part * p.step;
+      }
+    }
   }
-  const size_t slots = (size_t)a.c.kv_heads * RB * a.plan.items * 2;
-  const size_t slot = ((size_t)h * RB + rb) * a.plan.items * 2;
+  const Count<SEEN, SHIFT> tiles_of(a, rb);
+  if (!pairs) {
+    if (item >= a.plan.items) return;
+    if (SEL) {
+      const Lists<SHIFT> lists(a);
+      const int row = item / lists.runs;
+      if (row >= a.b.n_tokens) return;
+      begin = item * lists.run;
+      cut = Cut{lists.run, true};
+      // the list's load goes out beside the sequence's, one wait less (4 tokens, 64 pages
+      // of 64, D = 256: 28.7 against 29.7 us)
+      entry = listed(a, row, h, ((begin - row * lists.runs * lists.run) >> (a.c.shift - SHIFT)) + lane);
+      set = lists.set(a, row, lane);
+    } else if (!PAIRED && a.plan.whole) {
+      set = seq_set(a.b, item, tiles_of);
+      cut = Cut{set.tiles, true};
+    } else {
+      set = find_seq(a.b, item, 0, lane, a.plan, tiles_of, &cut);
+      begin = item * cut.run;
+    }
+    slot += (size_t)rb * a.plan.items * 2 + part_slot(item, cut.run, set.first);
+  }
   while (set.b >= 0) {
     const int lo = max(begin - set.first, 0), hi = min(begin + cut.run - set.first, set.tiles);
-    const Out out{a, lo == 0 && hi == set.tiles, slot + part_slot(item, cut.run, set.first), slots};
+    const Out out{a, lo == 0 && hi == set.tiles, slot, slots};
     run(set, h, rb, lo, hi, entry, out);
     if (SEL || cut.apart || set.first + set.tiles >= begin + cut.run) break;
-    set = next_seq<SEEN>(a, set, lane, tiles_of);
+    if (PAIRED && pairs)
+      set = next_pair<SHIFT>(a, set, rb, lane);
+    else
+      set = next_seq<SEEN>(a, set, lane, tiles_of);
+    slot |= 1;        // of the sets that begin behind the run's first tile
     __syncthreads();  // the LDS of the set before is free
   }
 }
 
-template <int D, int MT, int SEEN, bool ONCE, int CODE>
+template <int D, int MT, int SEEN, bool ONCE, int CODE, bool PAIRED>
 __global__ __launch_bounds__(64 * attn_waves(D, MT)) void attn_part(AttnArgs a) {
   extern __shared__ uint4 lds[];
-  part_of<Format<CODE, D>::SHIFT, SEEN>(a, [&](const Set& set, int h, int rb, int lo, int hi, int entry, const Out& out) {
-    attn_run<D, MT, SEEN, ONCE, CODE>(a, set, h, rb, lo, hi, entry, out, lds);
-  });
+  part_of<Format<CODE, D>::SHIFT, SEEN, PAIRED>(
+      a, [&](const Set& set, int h, int rb, int lo, int hi, int entry, const Out& out) {
+        attn_run<D, MT, SEEN, ONCE, CODE>(a, set, h, rb, lo, hi, entry, out, lds);
+      });
 }
 
 // One row's parts joined: D / 4 lanes hold a row of 4 values each, the groups of lanes take the parts in turn and
 // join in LDS, in a fixed order.
-template <int D, int SEEN, int SHIFT>
+template <int D, int SEEN, int SHIFT, bool PAIRED>
 __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
   constexpr bool SEL = SEEN == LISTED;
   constexpr int LANES = D / 4;
   const int GROUPS = blockDim.x / LANES;
   const int l = threadIdx.x % LANES, grp = threadIdx.x / LANES, lane = threadIdx.x & 63;
   const int hq = blockIdx.x % a.heads, row = blockIdx.x / a.heads;
-  Cut cut;
-  int rb = 0;  // through a window a row block counts its own tiles
-  if (SEEN == WINDOW && a.plan.row_blocks > 1) {
-    const RowOf of = seq_of_row(a.b, row, lane);
-    if (of.b < 0) return;
-    rb = (of.token * a.group + hq % a.group) / attn_rows(a.plan);
-  }
-  const Count<SEEN, SHIFT> tiles_of(a, rb);
-  const Set set =
-      SEL ? Lists<SHIFT>(a).set(a, row, lane) : find_seq(a.b, -1, row, lane, a.plan, tiles_of, &cut);
-  if (set.b < 0) return;
-  const int run = SEL ? Lists<SHIFT>(a).run : cut.run, n = run_parts(set.first, set.tiles, run);
-  if (n == 1) return;  // the row is out already
   const int h = hq / a.group, g0 = hq % a.group;
-  const int r = SEL ? g0 : (row - set.seq.row) * a.group + g0;  // of the set's rows
   const int slot_rows = attn_rows(a.plan);
-  const size_t slots = (size_t)a.c.kv_heads * a.plan.row_blocks * a.plan.items * 2;
-  const size_t slot = ((size_t)h * a.plan.row_blocks + r / slot_rows) * a.plan.items * 2;
+  Cut cut;
+  Set set;
+  int rb = 0;  // through a window a row block counts its own tiles
+  size_t slot = (size_t)h * attn_slots(a.plan);
+  const size_t slots = (size_t)a.c.kv_heads * attn_slots(a.plan);
+  int n = 0, step = 0;  // of pairs APART: a row's parts, and how far they are from each other
+  bool pairs = false;
+  if constexpr (PAIRED) {
+    const int* at = reinterpret_cast<const int*>(a.part + slots * slot_rows * (D + 2));  // what the other launch went by
+    const PairCut c{__builtin_amdgcn_readfirstlane(at[0]), __builtin_amdgcn_readfirstlane(at[1]), 0};
+    if (c.kind != ALIKE) {
+      const Pair p = find_pair<SHIFT>(a, c, lane_seq(a.b, 0, lane), -1, row, g0, lane);
+      pairs = true;
+      set = p.set;
+      cut = Cut{c.run, false};
+      if (c.kind == APART) {
+        n = p.parts;
+        slot += p.slot;
+        step = p.step;
+      }
+    }
+  }
+  if (!pairs) {
+    if (SEEN == WINDOW && a.plan.row_blocks > 1) {
+      const RowOf of = seq_of_row(a.b, row, lane);
+      if (of.b < 0) return;
+      rb = (of.token * a.group + g0) / slot_rows;
+    }
+    const Count<SEEN, SHIFT> tiles_of(a, rb);
+    set = SEL ? Lists<SHIFT>(a).set(a, row, lane) : find_seq(a.b, -1, row, lane, a.plan, tiles_of, &cut);
+  }
+  if (set.b < 0) return;
+  const int run = SEL ? Lists<SHIFT>(a).run : cut.run;
+  const int r = SEL ? g0 : (row - set.seq.row) * a.group + g0;  // of the set's rows
   const int part0 = set.first / run;
+  if (!n) n = run_parts(set.first, set.tiles, run);
+  if (n == 1) return;  // the row is out already
+  if (!pairs) slot += (size_t)(r / slot_rows) * a.plan.items * 2;
   const float* pa = a.part + (slot * slot_rows + r % slot_rows) * D + 4 * l;
   const float* ml = a.part + slots * slot_rows * D + (slot * slot_rows + r % slot_rows) * 2;
   float mx = -FLT_MAX, sum = 0.f;
@@ -1056,7 +1207,8 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // four at a time on their way; past the end the last one, as nothing
       const int s = s0 + i * GROUPS;
-      const size_t to = (size_t)part_slot(part0 + min(s, n - 1), run, set.first) * slot_rows;
+      const int part = min(s, n - 1);
+      const size_t to = (size_t)(PAIRED && step ? part * step : part_slot(part0 + part, run, set.first)) * slot_rows;
       v[i] = ld2(ml + to * 2);
       o[i] = ld4(pa + to * D);
       if (s >= n) v[i] = f32x2{-FLT_MAX, 0.f};

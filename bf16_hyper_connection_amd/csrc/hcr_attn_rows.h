@@ -358,11 +358,11 @@ __device__ __forceinline__ void rows_run(const AttnArgs& a, const Set& set, int 
   }
 }
 
-template <int D, int RT, int SEEN, int CODE>
+template <int D, int RT, int SEEN, int CODE, bool PAIRED>
 __global__ __launch_bounds__(64 * ROWS_WAVES, rows_held(D, RT)) void attn_rows_part(AttnArgs a) {
   __shared__ RowsLds<D, RT> lds;
   arguments_near(a);
-  part_of<ROWS_SHIFT, SEEN>(a, [&](const Set& set, int h, int rb, int lo, int hi, int entry, const Out& out) {
+  part_of<ROWS_SHIFT, SEEN, PAIRED>(a, [&](const Set& set, int h, int rb, int lo, int hi, int entry, const Out& out) {
     rows_run<D, RT, SEEN, CODE>(a, set, h, rb, lo, hi, entry, out, lds);
   });
 }

@@ -12,13 +12,10 @@ namespace hcr {
 
 namespace {
 
-long long attn_grid(const CacheArgs& c, const AttnPlan& p) {
-  return ((long long)p.items * c.kv_heads + XCDS - 1) / XCDS * XCDS * p.row_blocks;
-}
-
 size_t scratch_of(const CacheArgs& c, const AttnPlan& p) {
   if (!attn_joins(p)) return 0;
-  return align256((size_t)c.kv_heads * p.row_blocks * p.items * 2 * attn_rows(p) * (c.head_dim + 2) * 4);
+  return align256((size_t)c.kv_heads * attn_slots(p) * attn_rows(p) * (c.head_dim + 2) * 4 +
+                  (p.paired ? sizeof(PairCut) : 0));
 }
 
 // The plan of any kind of call.
@@ -116,6 +113,22 @@ int new_cache(const CacheArgs& c, const CodeArgs& x, hcr_cache_t* out) {
   return HCR_OK;
 }
 
+// Several sets of several row blocks: the device counts the pairs of a set and a row block (pair_cut), whole ones where less
+// than half of the sets times row blocks may be there.  fill: work-groups that the chip holds at once.  Measured (us a
+// call, D = 128, 32 heads over 8, against a plan in which each row block of the longest prompt took runs over all sets):
+//   a prompt of 2,048 and 63 single tokens of up to 8,192: int8 350 against 7,740, BF16 805 against 14,430, through a window
+//   of 5,000 339 against 6,220; of up to 4,096 (whole) int8 227 against 468, BF16 449 against 1,260.  512 tokens at 60,000
+//   beside three single ones 1,099 against 2,360; 3 prompts of 1,000 to 1 through a window of 6,000 297 against 400; 4 of 300
+//   at 9,000 (BF16, D = 64) 637 against 783.  Alike sets pay for the count (3 of 128 at 9,000 141 against
+//   136); whole ones of 2,048 and 1, which are not counted, would (89 against 87)
+static void plan_pairs(AttnPlan& p, const CacheArgs& c, const BatchArgs& b, int group, int fill) {
+  if (p.row_blocks == 1 || b.n_seqs == 1) return;
+  const long long pairs = pairs_bound(p, b.n_seqs, (long long)b.n_tokens * group);
+  if (p.whole && 2 * pairs >= (long long)b.n_seqs * p.row_blocks) return;
+  p.shares = fill / c.kv_heads > 1 ? fill / c.kv_heads : 1;
+  p.paired = (int)pairs + (p.whole ? 0 : 2 * p.shares);
+}
+
 // Measured on MI355X, 8 kv heads, graphs of calls on rotated inputs (us a call), lengths from an eighth of the
 // longest up to it:
 //   row tiles  two 16-row tiles a wave from 17 rows on.  D = 128: 24 rows 154 against 160, 64 rows 161 against 185.
@@ -193,19 +206,12 @@ static AttnPlan plan_for(const CacheArgs& c, const BatchArgs& b, int heads, int 
     items = runs * sets;
   }
   p.items = p.whole ? (int)sets : items > 1 ? (int)items : 1;
+  if (!n_sel) plan_pairs(p, c, b, group, fill);
   return p;
 }
 
 AttnPlan attn_plan(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel) {
   return plan_for(c, b, heads, n_sel, n_sel ? n_sel << (c.shift - TILE_SHIFT) : ceil_div(b.max_ctx, TILE), false);
-}
-
-// Tiles of `1 << shift` positions that rows of `tokens` consecutive tokens see at most.
-static int window_bound(const WindowArgs& w, int max_ctx, long long tokens, int shift) {
-  const long long one = 1ll << shift, all = (max_ctx + one - 1) >> shift;
-  if (!w.size) return (int)all;
-  const long long most = ((w.first + one - 1) >> shift) + ((w.size + tokens + one - 2) >> shift) + 1;
-  return (int)(all < most ? all : most);
 }
 
 // Work-groups of four waves that share their rows (hcr_attn_rows.h), up to four row tiles each.  As few row blocks as hold
@@ -265,6 +271,7 @@ static AttnPlan rows_plan(const CacheArgs& c, const WindowArgs& w, const BatchAr
     items = runs * sets;
   }
   p.items = p.whole ? (int)sets : items > 1 ? (int)items : 1;
+  if (!n_sel) plan_pairs(p, c, b, group, fill);
   return p;
 }
 

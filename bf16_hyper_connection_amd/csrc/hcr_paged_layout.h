@@ -114,6 +114,8 @@ constexpr int rows_held(int D, int q_tiles) { return D == 256 ? (q_tiles > 2 ? 2
 // below the bounds.  The host fixes the number of work-groups, the device the run's length.  Where the work-groups
 // suffice, every set begins a run of its own (a second set costs a work-group the wait for its first loads again);
 // else a run goes on from one set to the next.
+// Sets of more rows than a work-group takes may have unlike numbers of row blocks (a prompt many, a single token one),
+// which the host does not know: with several of them the device counts the pairs of a set and a row block (pair_cut).
 struct AttnPlan {
   int q_tiles;     // 16-row tiles a wave holds
   int row_waves;   // waves of a work-group over the rows
@@ -123,6 +125,8 @@ struct AttnPlan {
   int least;       // tiles that are worth a work-group
   int whole;       // a work-group for each set instead, with all of its tiles: nothing to join
   int shared;      // the work-group's four waves share q_tiles row tiles, and tiles of 64 positions
+  int paired;      // work-groups of a kv head over the pairs of a set and a row block; 0: they are not counted
+  int shares;      // work-groups of a kv head that the chip holds at once
 };
 HCR_HD int attn_rows(const AttnPlan& p) { return p.row_waves * p.q_tiles * 16; }  // of a work-group
 // Tiles of one run, from those of all sets (every set has one at least: a set without positions writes its zeros).
@@ -147,8 +151,54 @@ HCR_HD int run_tiles_listed(const AttnPlan& p, int list_tiles, int n_tokens) {
 // A run has two places for parts: of the set that began before it, and of the set that goes on behind it.
 HCR_HD int run_parts(int first, int tiles, int run) { return (first + tiles - 1) / run - first / run + 1; }
 HCR_HD int part_slot(int run_index, int run, int first) { return 2 * run_index + (first >= run_index * run); }
+// Row blocks of a set of `rows` rows, and how many pairs there are at most.
+HCR_HD int set_blocks(const AttnPlan& p, int rows) { return ceil_div(rows, attn_rows(p)); }
+HCR_HD long long pairs_bound(const AttnPlan& p, long long sets, long long rows_of_all) {
+  const long long each = sets * p.row_blocks, all = sets + rows_of_all / attn_rows(p);
+  return each < all ? each : all;
+}
+// How pairs are cut, from the tiles of all of them, their number and the row blocks of the sets that have rows:
+//   ALIKE  as many row blocks each, more runs than one: each row block's tiles as one row block's sets are cut, in `items`
+//          equal runs that may go on from one set to the next
+//   EVEN   no more pairs than the chip's share for a kv head: the tiles of all pairs, one behind the other, in one equal
+//          run for each share
+//   APART  more of them: each by itself, what is longer than half a share and than the average pair (by a sixteenth: what
+//          is not much longer stays whole) in several runs
+enum PairKind { ALIKE, EVEN, APART };
+struct PairCut {
+  int kind, run, blocks;  // ALIKE: row blocks of a set
+};
+HCR_HD PairCut pair_cut(const AttnPlan& p, long long tiles, int pairs, int fewest_blocks, int most_blocks) {
+  constexpr long long MOST = 1 << 26;  // a pair has 2^25 at most
+  if (p.whole || pairs == 0) return PairCut{APART, (int)MOST, 0};
+  if (p.items > 1 && fewest_blocks == most_blocks) return PairCut{ALIKE, 0, most_blocks};
+  const bool even = pairs <= p.shares && tiles < 1 << 30;
+  const int parts = even ? p.shares : 2 * p.shares < pairs ? 2 * p.shares : pairs;
+  long long run = (tiles + parts - 1) / parts;
+  if (!even) run += run / 16;
+  run = run > p.least ? run : p.least;
+  return PairCut{even ? EVEN : APART, (int)(run < MOST ? run : MOST), 0};
+}
+// A pair APART in even runs: `parts` of `each` tiles (the last may be shorter).  One that is cut has less than twice
+// tiles / run parts, all of them together less than four for each share.
+struct PairRuns {
+  int parts, each;
+};
+HCR_HD PairRuns pair_runs(int tiles, int run) {
+  const int each = ceil_div(tiles, ceil_div(tiles, run));
+  return PairRuns{ceil_div(tiles, each), each};
+}
+// Work-groups of a call.
+HCR_HD long long attn_grid(const CacheArgs& c, const AttnPlan& p) {
+  const long long items = (long long)(p.paired ? p.paired : p.items) * c.kv_heads;
+  return (items + XCDS - 1) / XCDS * XCDS * (p.paired ? 1 : p.row_blocks);
+}
+// Places for parts of a kv head.
+HCR_HD long long attn_slots(const AttnPlan& p) {
+  return p.paired ? 4ll * p.shares : 2ll * p.items * p.row_blocks;
+}
 // Whether a set may have several parts, to be joined by a second launch.
-HCR_HD bool attn_joins(const AttnPlan& p) { return p.items > 1 && !p.whole; }
+HCR_HD bool attn_joins(const AttnPlan& p) { return !p.whole && (p.paired || p.items > 1); }
 // Bytes of LDS of a work-group: its query rows, in their place what its groups join in, a 16-row tile of each wave
 // at a time, and the groups' (m, l).
 HCR_HD int attn_lds(int D, const AttnPlan& p) {
@@ -176,6 +226,20 @@ HCR_HD WindowTiles window_tiles(const WindowArgs& w, int len_min, int len_max, i
   return t;
 }
 
+// Tiles that rows of `tokens` consecutive tokens see at most, none of them past position max_ctx (size 0: all).
+HCR_HD int window_bound(const WindowArgs& w, int max_ctx, long long tokens, int shift) {
+  const long long one = 1ll << shift, all = (max_ctx + one - 1) >> shift;
+  if (!w.size) return (int)all;
+  const long long most = ((w.first + one - 1) >> shift) + ((w.size + tokens + one - 2) >> shift) + 1;
+  return (int)(all < most ? all : most);
+}
+// The tiles that each of a set's row blocks counts as, where pairs are counted: those of the block that has most (one at least).
+HCR_HD int pair_tiles(const AttnPlan& p, const WindowArgs& w, const Seq& s, int group, int shift) {
+  const int len = s.first + s.tokens, block = ceil_div(attn_rows(p), group) + 1;  // tokens of a row block
+  const int tiles = len > 0 ? window_bound(w, len, block < s.tokens ? block : s.tokens, shift) : 0;
+  return tiles > 1 ? tiles : 1;
+}
+
 struct AttnArgs {
   CacheArgs c;
   BatchArgs b;
@@ -184,7 +248,8 @@ struct AttnArgs {
   int n_sel, heads, group, out_type;
   float scale_hi, scale_lo;  // scale / ln 2 (probabilities are powers of two) in two parts
   void* out;
-  float* part;  // [kv_heads][row_blocks][items][2][rows][D], then (m, l) pairs [kv_heads][row_blocks][items][2][rows]
+  float* part;  // [kv_heads][slots][rows][D], then (m, l) pairs [kv_heads][slots][rows]; slots: [row_blocks][items][2], or
+                // of cut pairs alone; behind them the PairCut that the join goes by
   AttnPlan plan;
   CodeArgs code;
   WindowArgs window;

@@ -1,0 +1,150 @@
+"""Batches of prompts and single tokens together: attention counts the pairs of a sequence and a row block that there are, so
+that no work-group has much more to do than its share.  The index arithmetic on the host, under AddressSanitizer and
+UndefinedBehaviorSanitizer (tests/asan/paged_pairs_stubs.cpp); outputs on the GPU against the FP64 reference."""
+
+import os
+import shutil
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from bf16_hyper_connection_amd import inputs as gen
+from bf16_hyper_connection_amd import paged
+from tests import paged_codes_util as cu
+from tests import paged_util as pu
+from tests.libhcr_util import ROOT, ensure_built
+
+CSRC = os.path.join(ROOT, "bf16_hyper_connection_amd", "csrc")
+
+
+@pytest.fixture(scope="module")
+def sanitized(tmp_path_factory):
+    cxx = next((c for c in ("g++", "c++") if shutil.which(c)), None)
+    if cxx is None:
+        pytest.skip("no host C++ compiler")
+    out = str(tmp_path_factory.mktemp("paged_pairs") / "libpaged_pairs_asan.so")
+    asan = [os.path.join(ROOT, "tests", "asan", f) for f in ("paged_stubs.cpp", "paged_q8_stubs.cpp", "paged_pairs_stubs.cpp")]
+    cmd = [cxx, "-std=c++17", "-O1", "-g", "-fno-omit-frame-pointer", "-fsanitize=address,undefined",
+           "-fno-sanitize-recover=undefined", "-shared", "-fPIC", "-Wall", "-Werror", "-D__host__=", "-D__device__=",
+           "-I", os.path.join(ROOT, "include"), "-I", CSRC, os.path.join(CSRC, "hcr_paged_api.cpp"),
+           os.path.join(CSRC, "hcr_paged_q8_api.cpp"), *asan, "-o", out]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout + r.stderr
+    libasan = subprocess.run([cxx, "-print-file-name=libasan.so"], capture_output=True, text=True).stdout.strip()
+
+    def run(code):
+        env = dict(os.environ, LD_PRELOAD=libasan, ASAN_OPTIONS="detect_leaks=0:abort_on_error=1:halt_on_error=1",
+                   UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1")
+        head = f"import ctypes\nL = ctypes.CDLL({out!r})\nL.paged_pairs_checks.restype = ctypes.c_char_p\n" \
+               "L.paged_pairs_longest.restype = ctypes.c_longlong\n"
+        r = subprocess.run([sys.executable, "-c", head + code], env=env, capture_output=True, text=True, timeout=900)
+        assert r.returncode == 0, (r.stdout + r.stderr)[-3000:]
+        assert "ERROR: AddressSanitizer" not in r.stderr and "runtime error" not in r.stderr
+        return r.stdout.strip()
+    return run
+
+
+def test_index_runs_of_pairs_cover_every_tile_once(sanitized):
+    assert sanitized("print(L.paged_pairs_checks().decode())") == "ok"
+
+
+@pytest.mark.parametrize("code", [1, 2, 3])
+@pytest.mark.parametrize("size", [0, 5000])
+@pytest.mark.parametrize("head_dim,heads", [(64, 64), (128, 32), (256, 48)])
+@pytest.mark.parametrize("ctx", [8192, 60000])
+def test_index_a_prompt_among_single_tokens_leaves_no_work_group_with_many(sanitized, code, size, head_dim, heads, ctx):
+    """63 single tokens beside a prompt of 2,048: no run is longer than two shares of what 256 CUs have to do together (a
+    work-group used to walk all of the 63 sequences)."""
+    longest, total = map(int, sanitized(
+        "t = ctypes.c_longlong()\n"
+        f"print(L.paged_pairs_longest({code}, {head_dim}, 8, {heads}, {size}, 2048, 63, {ctx}, ctypes.byref(t)), t.value)").split())
+    assert 0 < longest <= 2 * total * 8 / 256
+
+
+BATCHES = {  # windows (new tokens, positions), bounds above what there is
+    "a prompt among single tokens": ([(1, 3 + 37 * i) for i in range(20)] + [(230, 230)] + [(1, 900 - 41 * i) for i in range(20)], {}),
+    "prompts behind long contexts": ([(97, 5000), (1, 9001), (33, 33), (150, 700), (0, 300), (1, 0)], {}),
+    "past 64 sequences": ([(0, 50)] * 30 + [(1, 7000)] + [(1, 40)] * 40 + [(140, 300)] + [(1, 11)] * 30 + [(35, 4500)], {}),
+    "loose bounds": ([(1, 600), (70, 800), (1, 2300), (2, 1)], dict(max_tokens=400, max_ctx=9000)),
+    "tokens before the first position": ([(130, 100), (1, 6000), (40, 20)], {}),
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", cu.KINDS + ["bf16"])
+@pytest.mark.parametrize("head_dim,page,kv,group", [(128, 64, 1, 5), (64, 128, 2, 8), (256, 64, 1, 6)])
+@pytest.mark.parametrize("name", sorted(BATCHES))
+def test_attend(kind, head_dim, page, kv, group, name):
+    ensure_built()
+    windows, bounds = BATCHES[name]
+    s = cu.scene(kind, 140, kv, head_dim, page, windows, table_extra=150)
+    if kind == "bf16":  # their scenes take the same path
+        heads = kv * group
+        q = pu.queries(140, s.n_tokens + 3, heads, head_dim)
+        qf = oracle.bf16_bits_to_f64(q)
+        keys, values = cu.decoded(s)
+        want = oracle.paged.attend(s.batch, keys, values, qf, head_dim ** -0.5)
+        tol = pu.rows_tolerance(qf, cu.reach(keys), head_dim ** -0.5, int(s.ctx_len.max()), False)
+        out = torch.full((s.n_tokens + 3, heads, head_dim), 5.0, device="cuda")
+        cu.dev_cache(s).attend(pu.dev_batch(s, **bounds), pu.dev_bits(q), out=out)
+        assert torch.all(out[s.n_tokens:] == 5.0)
+    else:
+        out, want, tol = cu.attend(s, kv * group, extra_rows=3, **bounds)
+    pu.check_rows(out, want, tol, name)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", cu.KINDS + ["bf16"])
+@pytest.mark.parametrize("head_dim,page,kv,group", [(128, 64, 1, 5), (64, 32, 2, 8), (256, 64, 1, 6)])
+@pytest.mark.parametrize("window,n_first", [(90, 0), (6000, 70)])
+@pytest.mark.parametrize("name", sorted(BATCHES))
+def test_attend_window(kind, head_dim, page, kv, group, window, n_first, name):
+    ensure_built()
+    windows, bounds = BATCHES[name]
+    s = cu.scene(kind, 141, kv, head_dim, page if kind == "bf16" else max(page, 64), windows, table_extra=300)
+    out, want, tol = cu.attend(s, kv * group, out_dtype=torch.bfloat16, window=window, n_first=n_first, **bounds)
+    pu.check_rows(out, want, tol, name)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", cu.KINDS + ["bf16"])
+def test_a_graph_of_mixed_batches_reads_the_lengths_of_its_replay(kind):
+    """Which sequence is the prompt, and how long they all are, changes between replays."""
+    ensure_built()
+    windows = [(200, 200), (1, 6000), (1, 33), (40, 3000)]
+    s = cu.scene(kind, 142, 2, 128, 64, [(1, 6000)] * 4)
+    cache = cu.dev_cache(s)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    starts, lens = torch.zeros(5, **i32), torch.ones(4, **i32)
+    batch = paged.Batch(starts, lens, torch.from_numpy(s.table).cuda(), 200, 6000)
+    bits = pu.queries(142, 242, 8, 128)
+    q = pu.dev_bits(bits)
+    tol = pu.rows_tolerance(oracle.bf16_bits_to_f64(bits), cu.reach(cu.decoded(s)[0]), 128 ** -0.5, 6000, False)
+
+    def calls():
+        return [cache.attend(batch, q), cache.attend_window(batch, q, 1000, 5)]
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = calls()
+    for turn in range(5):
+        now = windows[turn % 4:] + windows[:turn % 4]
+        starts.copy_(torch.from_numpy(np.cumsum([0] + [t for t, _ in now])))
+        lens.copy_(torch.tensor([c for _, c in now]))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in held]
+        assert all(torch.equal(a, b) for a, b in zip(got, calls()))
+        # each sequence by itself: the same sums in another cut
+        for b, (t, c) in enumerate(now):
+            one = paged.Batch(torch.tensor([0, t], **i32), lens[b:b + 1].contiguous(), batch.block_table[b:b + 1].contiguous(), t, c)
+            rows = slice(int(starts[b]), int(starts[b]) + t)
+            for all_, alone in zip(got, (cache.attend(one, q[rows].contiguous()),
+                                         cache.attend_window(one, q[rows].contiguous(), 1000, 5))):
+                off, norm = ((x.double().norm(dim=2) for x in (all_[rows] - alone, alone)))
+                assert torch.all(off <= 2 * tol * norm)
