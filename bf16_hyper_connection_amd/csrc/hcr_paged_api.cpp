@@ -159,14 +159,29 @@ static void plan_pairs(AttnPlan& p, const CacheArgs& c, const BatchArgs& b, int 
 //              against 575 with 4); 4, two work-groups a CU, for runs where no sequence is longer than 2,048 (one of
 //              2,000, D = 256: 13.4 against 14.5) and for many sets of up to 512 (300: 14 against 17), since a short
 //              one is mostly the wait for its first loads
-static AttnPlan plan_for(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel, int tiles, bool one_tile) {
+// The bounds are in positions, whatever a tile has (BF16 and codes of D = 256 32, codes of D <= 128 64).
+// Over codes (the same calls, whole or with four waves against the other):
+//   whole      fewer sets than CUs: a set in one work-group takes longer with its length, in runs with the number of sets.
+//              One of 512 positions, D = 128 10.5 against 11.2, of 768 12.3 against 11.2, of 1,400 17.8 against 11.6; D = 64
+//              768 9.1 against 10.2, 1,024 10.5 against 10.3; D = 256 256 11.3 against 11.8, 384 13.0 against 11.9.  8 of
+//              up to 768, D = 128 12.7 against 13.2, of 900 14.5 against 13.4; 16 of 1,024 15.5 against 16.8, of 1,400
+//              19.2 against 17.5; D = 256 16 of 640 17.9 against 18.2, of 768 20.9 against 18.5.  32 sets, D = 128: of 3,000
+//              33.5 against 38.9, 4,096 42 against 43; D = 256: 3,000 64 against 57.  64 and more to 4,096 as above:
+//              one of 8,192 beside 63 of 100 takes 24 in runs, 66 whole, one of 5,000 28 and 45 (lengths from an
+//              eighth of 8,192 up to it 114 and 105, all of 8,192 174 and 177)
+//   waves      four for 64 and more whole sets of up to 1,024 (D = 256, 64 of 700 29.8 against 32.4, 128 47.9 against 60.4),
+//              for runs of few sets up to 4,096 (8 of 4,096 20.3 against 23.3), and for runs of more than CUs' sets of any
+//              length: 64 of up to 8,192 115 against 128 with eight, 12,000 156 against 168, 20,000 246 against 253
+static AttnPlan plan_for(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel, int tiles, int shift, bool one_tile,
+                         bool codes) {
   constexpr int CUS = 256;
   AttnPlan p{};
   const int group = heads / c.kv_heads;
   const int rows = n_sel ? group : b.max_tokens * group;
   const bool wide = c.head_dim == 256;
   const long long sets = n_sel ? b.n_tokens : b.n_seqs;
-  const bool lengthy = rows > 48 && rows <= 64 && tiles >= 256 && sets * tiles >= 512;
+  const long long span = (long long)tiles << shift;  // positions of a set at most
+  const bool lengthy = rows > 48 && rows <= 64 && span >= 8192 && sets * span >= 16384;
   p.q_tiles = !one_tile && rows > 16 && (c.head_dim == 128 || (wide && (rows <= 32 || lengthy))) ? 2 : 1;
   const int row_tiles = ceil_div(rows, 16 * p.q_tiles);
   p.row_blocks = ceil_div(row_tiles, wide ? 4 : 8);
@@ -179,12 +194,24 @@ static AttnPlan plan_for(const CacheArgs& c, const BatchArgs& b, int heads, int 
 
   const int units = c.kv_heads * p.row_blocks;
   const long long full = sets * units;  // work-groups of whole sets
-  p.whole = full < CUS              ? tiles <= (wide ? (rows > 16 ? 6 : 12) : 3 * most_groups)
-            : n_sel                 ? 1  // lists are alike
-            : alone                 ? tiles <= 32
-            : full < 2 * CUS        ? tiles <= 64
-                                    : tiles <= 128;
-  const bool few = p.whole ? full >= 2 * CUS && tiles <= 16 : !n_sel && tiles <= 64;
+  // positions up to which a work-group takes a whole set, and up to which four waves a work-group do
+  long long whole_to, few_to;
+  if (full < CUS)
+    whole_to = codes ? (c.head_dim == 64 ? 768 : 65536 / c.head_dim) + full * (wide ? 2 : 4)
+               : wide ? (rows > 16 ? 192 : 384)
+                      : 96 * most_groups;
+  else if (n_sel)
+    whole_to = span;  // lists are alike
+  else if (alone)
+    whole_to = 1024;
+  else
+    whole_to = full < 2 * CUS && !(codes && !wide) ? 2048 : 4096;
+  p.whole = span <= whole_to;
+  if (p.whole)
+    few_to = full < 2 * CUS ? -1 : codes ? 1024 : 512;
+  else
+    few_to = n_sel ? -1 : !codes ? 2048 : full < CUS ? 4096 : span;
+  const bool few = span <= few_to;
   p.groups = few && p.row_waves <= 4 && most_groups > 4 / p.row_waves ? 4 / p.row_waves : most_groups;
   if (p.groups > tiles) p.groups = tiles;
   if (p.groups < 1) p.groups = 1;
@@ -211,7 +238,8 @@ static AttnPlan plan_for(const CacheArgs& c, const BatchArgs& b, int heads, int 
 }
 
 AttnPlan attn_plan(const CacheArgs& c, const BatchArgs& b, int heads, int n_sel) {
-  return plan_for(c, b, heads, n_sel, n_sel ? n_sel << (c.shift - TILE_SHIFT) : ceil_div(b.max_ctx, TILE), false);
+  return plan_for(c, b, heads, n_sel, n_sel ? n_sel << (c.shift - TILE_SHIFT) : ceil_div(b.max_ctx, TILE), TILE_SHIFT,
+                  false, false);
 }
 
 // Work-groups of four waves that share their rows (hcr_attn_rows.h), up to four row tiles each.  As few row blocks as hold
@@ -287,10 +315,13 @@ AttnPlan attn_plan_more(const CacheArgs& c, const CodeArgs& x, const WindowArgs&
   if (rows > 16 && c.shift >= ROWS_SHIFT) return rows_plan(c, w, b, group, n_sel);
   const int shift = tile_shift(coded(x), c.head_dim);
   const int tiles = n_sel ? n_sel << (c.shift - shift) : window_bound(w, b.max_ctx, b.max_tokens, shift);
-  AttnPlan p = plan_for(c, b, heads, n_sel, tiles, true);
-  // sequences are as long as each other through a window: whole ones in two work-groups a CU (64 windows of 4,096: 166
-  // us, in runs 176)
-  if (w.size && !p.whole && p.row_waves == 1 && p.groups >= 4 && tiles <= 160 &&
+  AttnPlan p = plan_for(c, b, heads, n_sel, tiles, shift, true, coded(x));
+  // Windows of 4,096 are whole sets too, although the ends of their tiles are more: four waves, two work-groups a CU.  Sequences
+  // longer than the window are then as long as each other: 64 windows of 4,096 of BF16 D = 128 165 us, in runs 175, D =
+  // 64 84 against 96, D = 256 320 against 335, int8 94 against 98, 128 of them 178 against 192.  Those that are shorter
+  // are not (one of 4,196 beside 63 of 200: 62 against 35), so that no longer window is: of 5,000 in runs 210 against 200,
+  // 8,192 330 against 323, one of 5,100 beside 63 of 200 35 against 75.
+  if (w.size && !p.whole && p.row_waves == 1 && p.groups >= 4 && ((long long)tiles << shift) <= 4096 + 256 &&
       (long long)b.n_seqs * c.kv_heads >= 512) {
     p.whole = 1;
     p.groups = 4;

@@ -164,3 +164,10 @@ extern "C" long long paged_pairs_longest(int code, int D, int kv, int heads, int
   const long long n = longest_run(c, x, w, b, heads, seqs, p, &fail);
   return fail ? -2 : n;
 }
+
+// Whether a work-group takes a set whole, of `sets` single tokens with up to `ctx` positions in pages of 64 (size: of a window).
+extern "C" int paged_plan_whole(int code, int D, int kv, int heads, int size, int sets, int ctx) {
+  const CacheArgs c{nullptr, nullptr, nullptr, 10, kv, D, 6};
+  const BatchArgs b{nullptr, nullptr, nullptr, 1 << 20, sets, sets, 1, ctx};
+  return plan_of(c, CodeArgs{nullptr, nullptr, code}, WindowArgs{size, 0}, b, heads).whole;
+}

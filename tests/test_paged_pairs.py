@@ -65,6 +65,27 @@ def test_index_a_prompt_among_single_tokens_leaves_no_work_group_with_many(sanit
     assert 0 < longest <= 2 * total * 8 / 256
 
 
+@pytest.mark.parametrize("code", [1, 2, 3])
+@pytest.mark.parametrize("head_dim", [64, 128, 256])
+def test_index_no_set_of_more_than_4096_positions_is_one_work_groups(sanitized, code, head_dim):
+    """Whatever a tile has: a long sequence among short ones would hold a single CU for the whole call."""
+    lines = sanitized(f"for size in (0, 4096, 4500, 10000):\n  for sets in (1, 4, 16, 31, 32, 63, 64, 128, 1000):\n"
+                      f"    for ctx in (1000, 1500, 2040, 4096, 4160, 5000, 8192, 10000, 20000):\n"
+                      f"      print(size, sets, ctx, L.paged_plan_whole({code}, {head_dim}, 8, 32, size, sets, ctx))").splitlines()
+    assert len(lines) == 4 * 9 * 9
+    for line in lines:
+        size, sets, ctx, whole = map(int, line.split())
+        if code != 1 or size:
+            # fewer sets than CUs: those that end as soon as runs and their join
+            most = (768 if head_dim == 64 else 65536 // head_dim) + 8 * sets * (2 if head_dim == 256 else 4)
+            if whole and sets < 32 and code != 1:
+                assert min(ctx, size or ctx) <= most, line
+            if whole:
+                assert min(ctx, size or ctx) <= 4096 + (256 if size else 0), line  # the ends of a window's tiles
+            elif sets >= 64:
+                assert min(ctx, size or ctx) > 4096, line
+
+
 BATCHES = {  # windows (new tokens, positions), bounds above what there is
     "a prompt among single tokens": ([(1, 3 + 37 * i) for i in range(20)] + [(230, 230)] + [(1, 900 - 41 * i) for i in range(20)], {}),
     "prompts behind long contexts": ([(97, 5000), (1, 9001), (33, 33), (150, 700), (0, 300), (1, 0)], {}),
