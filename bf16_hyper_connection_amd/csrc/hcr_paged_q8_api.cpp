@@ -39,7 +39,7 @@ int hcr_cache_read(hcr_cache_t h, const hcr_batch* batch, int out_type, void* k_
   if (!k_out && !v_out) return HCR_EINVAL;
   if (const int e = check_arrays(a.b)) return e;
   if (!aligned(k_out, 16) || !aligned(v_out, 16)) return HCR_EALIGN;
-  if ((long long)a.b.n_seqs * read_parts(a.b) * c.kv_heads * 2 * READ_THREADS > THREADS_MAX) return HCR_EINVAL;
+  if ((long long)a.b.n_seqs * read_parts(a.b) * c.kv_heads * READ_THREADS > THREADS_MAX) return HCR_EINVAL;
   const size_t bytes = (size_t)a.b.n_tokens * c.kv_heads * c.head_dim * (out_type == HCR_F32 ? 4 : 2);
   const Span sk = span(k_out, bytes), sv = span(v_out, bytes);
   if (overlap(sk, sv)) return HCR_EALIAS;
