@@ -562,14 +562,6 @@ __device__ __forceinline__ uint4 drop_odd_codes(uint32_t& lo, uint32_t& hi, uint
   }
   return ones8(drop);
 }
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_or(uint32_t v) {
-  return v | (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
-}
-__device__ __forceinline__ uint32_t or_sixteen(uint32_t v) {
-  return dpp_or<0x140>(dpp_or<0x141>(dpp_or<0x4E>(dpp_or<0xB1>(v))));
-}
-
 // Ones at the positions, of 8 from p on, that a row of length len sees.
 __device__ __forceinline__ uint4 seen8(int p, int len) {
   return visible8(make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u), p, len);
@@ -814,6 +806,41 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
     }
     const int now = tiles.p0;
     const bool whole = rows.all_see(a, now, F::TILE);
+    const int mine = now + F::TILE / 4 * lg;  // the position of the lane's first product and value
+    // A value that is no number and that only some of the rows see: zero times it would reach the others.  It leaves the
+    // product, and its dimension of the rows that see it becomes NaN: those where a product of such places with the
+    // rows' visible ones is not zero.
+    const auto spoil = [&](int m, int d, const f32x4& met) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][d][i] = met[i] > 0.f ? NAN : acc[m][d][i];
+    };
+    const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+    const Reach any{rows.start_min, rows.len_max, a.window.first}, all{rows.start_max, rows.len_min, a.window.first};
+    if constexpr (CODE == HCR_E4M3) {  // ahead of the products, whose registers it would not have
+      uint32_t hit = 0;
+      if (!whole) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          hit |= odd_codes(vf[d].x) | odd_codes(vf[d].y);
+          if constexpr (sizeof(V) == 16) hit |= odd_codes(vf[d].z) | odd_codes(vf[d].w);
+        }
+      }
+      if (__any(hit != 0)) {
+        const uint32_t common = all.bits<NV>(mine);
+        const auto drop = [&](int d, uint32_t& lo, uint32_t& hi, int u) {  // codes 8 u and on
+          const uint4 at = drop_odd_codes(lo, hi, common >> 8 * u & 0xFFu);
+#pragma unroll
+          for (int m = 0; !SEL && m < MT; ++m)  // (a list's rows see the same positions: what is dropped nobody sees)
+            spoil(m, d, mfma(at, ones8(row_reach(m).template bits<8>(mine + 8 * u)), none));
+          __builtin_amdgcn_sched_barrier(0);
+        };
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          drop(d, vf[d].x, vf[d].y, 0);
+          if constexpr (sizeof(V) == 16) drop(d, vf[d].z, vf[d].w, 1);
+        }
+      }
+    }
     f32x4 s[MT][KT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -853,16 +880,6 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
     if (BLIND || more) load_keys(on);
     __builtin_amdgcn_sched_barrier(0);
 
-    const int mine = now + F::TILE / 4 * lg;  // the position of the lane's first product and value
-    // A value that is no number and that only some of the rows see: zero times it would reach the others.  It leaves the
-    // product, and its dimension of the rows that see it becomes NaN: those where a product of such places with the
-    // rows' visible ones is not zero.
-    const auto spoil = [&](int m, int d, const f32x4& met) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][d][i] = met[i] > 0.f ? NAN : acc[m][d][i];
-    };
-    const f32x4 none = {0.f, 0.f, 0.f, 0.f};
-    const Reach any{rows.start_min, rows.len_max, a.window.first}, all{rows.start_max, rows.len_min, a.window.first};
     if constexpr (!F::CODED && SEEN != WINDOW) {
       if (!whole) {
 #pragma unroll
@@ -904,37 +921,12 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
         probabilities(a, v, true, 0, 0, mx[m], sum[m], acc[m], p[m]);
         times_each(p[m], vs);
       }
-      // What a row does not see may be anything: a scale there, and an E4M3 code that is no number.  (Such a code goes
-      // as a zero, and its position's probabilities as NaN where they are seen.)
-      if (!whole) {
-        uint32_t odd[sizeof(V) / 4];
-        if constexpr (CODE == HCR_E4M3) {
-#pragma unroll
-          for (uint32_t& o : odd) o = 0;
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            uint32_t w[sizeof(V) / 4];
-            __builtin_memcpy(w, &vf[d], sizeof(V));
-#pragma unroll
-            for (int e = 0; e < (int)sizeof(V) / 4; ++e) {
-              const uint32_t o = odd_codes(w[e]);
-              odd[e] |= o;
-              w[e] &= ~((o << 1) - (o >> 7));
-            }
-            __builtin_memcpy(&vf[d], w, sizeof(V));
-          }
-#pragma unroll
-          for (uint32_t& o : odd) o = or_sixteen(o);  // any dimension's
-        }
+      if (!whole) {  // a scale that the row does not see may be anything
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           const uint32_t seen = row_reach(m).template bits<NV>(mine);
 #pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            uint32_t x = __float_as_uint(p[m][i]);
-            if constexpr (CODE == HCR_E4M3) x |= bit_mask(odd[i >> 2], 8 * (i & 3) + 7);
-            p[m][i] = __uint_as_float(x & bit_mask(seen, i));
-          }
+          for (int i = 0; i < NV; ++i) p[m][i] = __uint_as_float(__float_as_uint(p[m][i]) & bit_mask(seen, i));
         }
       }
 #pragma unroll
@@ -1139,8 +1131,10 @@ __device__ __forceinline__ void part_of(const AttnArgs& a, const Run& run) {
   }
 }
 
+// Over codes a work-group has one row wave (more rows share theirs) and so eight waves at most: held to the registers of
+// 16, D = 64 spilled (E4M3, 64 of up to 8,192 77 us against 70, windows of 4,096 63 against 49).
 template <int D, int MT, int SEEN, bool ONCE, int CODE, bool PAIRED>
-__global__ __launch_bounds__(64 * attn_waves(D, MT)) void attn_part(AttnArgs a) {
+__global__ __launch_bounds__(64 * (CODE == HCR_BF16 ? attn_waves(D, MT) : 8)) void attn_part(AttnArgs a) {
   extern __shared__ uint4 lds[];
   part_of<Format<CODE, D>::SHIFT, SEEN, PAIRED>(
       a, [&](const Set& set, int h, int rb, int lo, int hi, int entry, const Out& out) {

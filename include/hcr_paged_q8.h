@@ -16,8 +16,9 @@
  * hcr_attn_blocks attend over what the codes stand for, in FP32; hcr_block_scores and
  * hcr_block_topk take such a cache as any other (mean keys are of what the codes stand for).
  * Pages that were filled otherwise may hold any codes and scales: a key that is no number (the
- * E4M3 codes 0x7F and 0xFF, a scale that is none) makes every output NaN of the rows that see
- * it, a value at least its own dimension of them; rows that do not see it take nothing from it.
+ * E4M3 codes 0x7F and 0xFF, a scale of NaN) makes every output NaN of the rows that see it, a
+ * value's code that is none its own dimension of them, a value's scale that is not finite all
+ * of theirs no numbers; rows that do not see it take nothing from it.
  *
  * Pages hold 64, 128 or 256 positions:
  *   k_pages  : codes [n_pages][kv_heads][D / 16][page][16]   16 dimensions together

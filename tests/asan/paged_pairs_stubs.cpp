@@ -120,6 +120,7 @@ static const char* check_pairs() {
                       const AttnPlan p = plan_of(c, x, w, b, kv * group);
                       const long long bound = pairs_bound(p, count, (long long)rows * group);
                       CHECK((p.paired > 0) == (p.row_blocks > 1 && count > 1 && (!p.whole || 2 * bound < 1ll * count * p.row_blocks)));
+                      CHECK(!coded(x) || p.shared || p.row_waves * p.groups <= 8);  // what their kernels are held to
                       if (!p.paired) continue;
                       CHECK(p.shares >= 1 && attn_grid(c, p) >= (long long)p.paired * kv && attn_grid(c, p) % XCDS == 0);
                       const char* fail = nullptr;
