@@ -387,8 +387,9 @@ class PagedCache:
         """Bytes that ``attend_window`` needs for this batch."""
         return int(self._L.hcr_attn_window_scratch_bytes(self.handle, batch._of(n_tokens), heads, window, n_first))
 
-    def read(self, batch, n_tokens, out_dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
-        """Keys and values of the batch's positions as rows, [n_tokens][kv_heads][head_dim] each.
+    def read(self, batch, n_tokens, out_dtype=torch.bfloat16, k_out=None, v_out=None, stream=None, keys=True, values=True):
+        """Keys and values of the batch's positions as rows, [n_tokens][kv_heads][head_dim] each; ``keys=False`` or
+        ``values=False`` reads one side alone (None in the other's place).
 
         The positions are those that ``append`` would write: the last q_start[b + 1] - q_start[b] of sequence b (for a
         whole sequence its length).  BF16 or float32 (``out_dtype``, or ``k_out``'s and ``v_out``'s, of one type).  Rows
@@ -396,21 +397,21 @@ class PagedCache:
         """
         if not 0 <= n_tokens < 1 << 31:
             raise ValueError("n_tokens: not negative, under 2^31")
+        if not keys and not values or k_out is not None and not keys or v_out is not None and not values:
+            raise ValueError("keys or values: one at least, and each that an output is given for")
         shape = (n_tokens, self.kv_heads, self.head_dim)
         given = k_out if k_out is not None else v_out
         dtype = out_dtype if given is None else given.dtype
         if dtype not in _TYPES:
             raise ValueError("k_out and v_out: float32 or bfloat16")
-        if k_out is None:
-            k_out = self._new(stream, shape, dtype)
-        else:
-            self._given("k_out", k_out, shape, dtype)
-        if v_out is None:
-            v_out = self._new(stream, shape, dtype)
-        else:
-            self._given("v_out", v_out, shape, dtype)
-        self._call(self._L.hcr_cache_read, batch, stream, batch._of(n_tokens), _TYPES[dtype], k_out.data_ptr(),
-                   v_out.data_ptr())
+
+        def output(name, t, wanted):
+            if t is not None:
+                self._given(name, t, shape, dtype)
+            return self._new(stream, shape, dtype) if wanted and t is None else t
+        k_out, v_out = output("k_out", k_out, keys), output("v_out", v_out, values)
+        self._call(self._L.hcr_cache_read, batch, stream, batch._of(n_tokens), _TYPES[dtype],
+                   k_out.data_ptr() if keys else None, v_out.data_ptr() if values else None)
         return k_out, v_out
 
     def block_scores(self, batch, q, scores=None, stream=None):
