@@ -172,3 +172,23 @@ extern "C" int paged_plan_whole(int code, int D, int kv, int heads, int size, in
   const BatchArgs b{nullptr, nullptr, nullptr, 1 << 20, sets, sets, 1, ctx};
   return plan_of(c, CodeArgs{nullptr, nullptr, code}, WindowArgs{size, 0}, b, heads).whole;
 }
+
+// Pages that the longest run of an attention call over codes or through a window spans, of sequences of up to max_ctx positions
+// that are all as long (n_sel: of lists); 0 where pairs are counted.
+extern "C" int paged_more_run_pages(int code, int D, int kv, int page, int heads, int n_seqs, int max_tokens, int max_ctx,
+                                    int n_sel, int size, int first) {
+  const CodeArgs x{nullptr, nullptr, code};
+  const CacheArgs c{nullptr, nullptr, nullptr, 10, kv, D, log2_of(page)};
+  const WindowArgs w{size, first};
+  const BatchArgs b{nullptr, nullptr, nullptr, ceil_div(max_ctx, page), n_seqs, n_seqs * max_tokens, max_tokens, max_ctx};
+  const AttnPlan p = attn_plan_more(c, x, w, b, heads, n_sel);
+  if (p.paired) return 0;
+  const int shift = shift_of(c, x, p);
+  const int low = attn_rows(p) * (p.row_blocks - 1) / (heads / kv);  // the last row block's first token
+  const int tiles = n_sel ? n_sel << (c.shift - shift)
+                    : size ? window_tiles(w, max_ctx - max_tokens + low + 1, max_ctx, shift).tiles
+                           : ceil_div(max_ctx, 1 << shift);
+  int run = p.whole ? tiles : n_sel ? run_tiles_listed(p, tiles, b.n_tokens) : run_tiles(p, n_seqs * tiles);
+  if (run > tiles) run = tiles;
+  return run >> (c.shift - shift);
+}
