@@ -806,41 +806,6 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
     }
     const int now = tiles.p0;
     const bool whole = rows.all_see(a, now, F::TILE);
-    const int mine = now + F::TILE / 4 * lg;  // the position of the lane's first product and value
-    // A value that is no number and that only some of the rows see: zero times it would reach the others.  It leaves the
-    // product, and its dimension of the rows that see it becomes NaN: those where a product of such places with the
-    // rows' visible ones is not zero.
-    const auto spoil = [&](int m, int d, const f32x4& met) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][d][i] = met[i] > 0.f ? NAN : acc[m][d][i];
-    };
-    const f32x4 none = {0.f, 0.f, 0.f, 0.f};
-    const Reach any{rows.start_min, rows.len_max, a.window.first}, all{rows.start_max, rows.len_min, a.window.first};
-    if constexpr (CODE == HCR_E4M3) {  // ahead of the products, whose registers it would not have
-      uint32_t hit = 0;
-      if (!whole) {
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          hit |= odd_codes(vf[d].x) | odd_codes(vf[d].y);
-          if constexpr (sizeof(V) == 16) hit |= odd_codes(vf[d].z) | odd_codes(vf[d].w);
-        }
-      }
-      if (__any(hit != 0)) {
-        const uint32_t common = all.bits<NV>(mine);
-        const auto drop = [&](int d, uint32_t& lo, uint32_t& hi, int u) {  // codes 8 u and on
-          const uint4 at = drop_odd_codes(lo, hi, common >> 8 * u & 0xFFu);
-#pragma unroll
-          for (int m = 0; !SEL && m < MT; ++m)  // (a list's rows see the same positions: what is dropped nobody sees)
-            spoil(m, d, mfma(at, ones8(row_reach(m).template bits<8>(mine + 8 * u)), none));
-          __builtin_amdgcn_sched_barrier(0);
-        };
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          drop(d, vf[d].x, vf[d].y, 0);
-          if constexpr (sizeof(V) == 16) drop(d, vf[d].z, vf[d].w, 1);
-        }
-      }
-    }
     f32x4 s[MT][KT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -880,6 +845,16 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
     if (BLIND || more) load_keys(on);
     __builtin_amdgcn_sched_barrier(0);
 
+    const int mine = now + F::TILE / 4 * lg;  // the position of the lane's first product and value
+    // A value that is no number and that only some of the rows see: zero times it would reach the others.  It leaves the
+    // product, and its dimension of the rows that see it becomes NaN: those where a product of such places with the
+    // rows' visible ones is not zero.
+    const auto spoil = [&](int m, int d, const f32x4& met) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][d][i] = met[i] > 0.f ? NAN : acc[m][d][i];
+    };
+    const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+    const Reach any{rows.start_min, rows.len_max, a.window.first}, all{rows.start_max, rows.len_min, a.window.first};
     if constexpr (!F::CODED && SEEN != WINDOW) {
       if (!whole) {
 #pragma unroll
@@ -921,12 +896,37 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, const Set& set, int 
         probabilities(a, v, true, 0, 0, mx[m], sum[m], acc[m], p[m]);
         times_each(p[m], vs);
       }
-      if (!whole) {  // a scale that the row does not see may be anything
+      // what a row does not see may be anything: a scale there, and an E4M3 code that is no number (which goes as other
+      // such values do)
+      if (!whole) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           const uint32_t seen = row_reach(m).template bits<NV>(mine);
 #pragma unroll
           for (int i = 0; i < NV; ++i) p[m][i] = __uint_as_float(__float_as_uint(p[m][i]) & bit_mask(seen, i));
+        }
+        if constexpr (CODE == HCR_E4M3) {
+          uint32_t hit = 0;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            hit |= odd_codes(vf[d].x) | odd_codes(vf[d].y);
+            if constexpr (sizeof(V) == 16) hit |= odd_codes(vf[d].z) | odd_codes(vf[d].w);
+          }
+          if (__any(hit != 0)) {
+            const uint32_t common = all.bits<NV>(mine);
+            const auto drop = [&](int d, uint32_t& lo, uint32_t& hi, int u) {  // codes 8 u and on
+              const uint4 at = drop_odd_codes(lo, hi, common >> 8 * u & 0xFFu);
+#pragma unroll
+              for (int m = 0; !SEL && m < MT; ++m)  // (a list's rows see the same positions: what is dropped nobody sees)
+                spoil(m, d, mfma(at, ones8(row_reach(m).template bits<8>(mine + 8 * u)), none));
+              __builtin_amdgcn_sched_barrier(0);
+            };
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+              drop(d, vf[d].x, vf[d].y, 0);
+              if constexpr (sizeof(V) == 16) drop(d, vf[d].z, vf[d].w, 1);
+            }
+          }
         }
       }
 #pragma unroll

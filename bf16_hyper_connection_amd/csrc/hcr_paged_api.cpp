@@ -162,13 +162,14 @@ static void plan_pairs(AttnPlan& p, const CacheArgs& c, const BatchArgs& b, int 
 // The bounds are in positions, whatever a tile has (BF16 and codes of D = 256 32, codes of D <= 128 64).
 // Over codes (the same calls, whole or with four waves against the other):
 //   whole      fewer sets than CUs: a set in one work-group takes longer with its length, in runs with the number of sets.
-//              One of 512 positions, D = 128 10.5 against 11.2, of 768 12.3 against 11.2, of 1,400 17.8 against 11.6; D = 64
-//              768 9.1 against 10.2, 1,024 10.5 against 10.3; D = 256 256 11.3 against 11.8, 384 13.0 against 11.9.  8 of
-//              up to 768, D = 128 12.7 against 13.2, of 900 14.5 against 13.4; 16 of 1,024 15.5 against 16.8, of 1,400
-//              19.2 against 17.5; D = 256 16 of 640 17.9 against 18.2, of 768 20.9 against 18.5.  32 sets, D = 128: of 3,000
-//              33.5 against 38.9, 4,096 42 against 43; D = 256: 3,000 64 against 57.  64 and more to 4,096 as above:
-//              one of 8,192 beside 63 of 100 takes 24 in runs, 66 whole, one of 5,000 28 and 45 (lengths from an
-//              eighth of 8,192 up to it 114 and 105, all of 8,192 174 and 177)
+//              One, D = 128, three caches in turn: 640 positions 9.9 against 10.3, 768 9.7 against 10.4, 832 11.9 against
+//              10.6 (16 caches 12.2 against 11.2 at 768, 17.8 against 11.6 at 1,400); a call that is not in a graph takes
+//              2.5 more for the second launch.  D = 64: 768 8.4 against 10.1, 1,024 9.8 against 10.0; D = 256: 384 10.8
+//              against 11.4, 448 12.4 against 11.2.  4: 768 11.9 against 12.0, 832 13.8 against 12.0; 16: 1,024 15.8 against
+//              17.4, 1,200 16.9 against 20.1; 16 of D = 256: 640 17.9 against 18.2, 768 20.9 against 18.5.
+//              32 sets, D = 128: of 3,000 33.5 against 38.9, 4,096 42 against 43; D = 256: 3,000 64 against 57.  64
+//              and more to 4,096 as above: one of 8,192 beside 63 of 100 takes 24 in runs, 66 whole, one of 5,000 28
+//              and 45 (lengths from an eighth of 8,192 up to it 114 and 105, all of 8,192 174 and 177)
 //   waves      four for 64 and more whole sets of up to 1,024 (D = 256, 64 of 700 29.8 against 32.4, 128 47.9 against 60.4),
 //              for runs of few sets up to 4,096 (8 of 4,096 20.3 against 23.3), and for runs of more than CUs' sets of any
 //              length: 64 of up to 8,192 115 against 128 with eight, 12,000 156 against 168, 20,000 246 against 253
@@ -197,9 +198,7 @@ static AttnPlan plan_for(const CacheArgs& c, const BatchArgs& b, int heads, int 
   // positions up to which a work-group takes a whole set, and up to which four waves a work-group do
   long long whole_to, few_to;
   if (full < CUS)
-    whole_to = codes ? (c.head_dim == 64 ? 768 : 65536 / c.head_dim) + full * (wide ? 2 : 4)
-               : wide ? (rows > 16 ? 192 : 384)
-                      : 96 * most_groups;
+    whole_to = (wide ? (rows > 16 ? 192 : 384) : 96 * most_groups) + (codes && full > 64 ? 4 * (full - 64) : 0);
   else if (n_sel)
     whole_to = span;  // lists are alike
   else if (alone)
