@@ -303,7 +303,7 @@ __device__ __forceinline__ Set next_seq(const AttnArgs& a, const Set& s, int lan
 // How the pairs of the sequences and their row blocks are cut (AttnPlan::paired).
 template <int SHIFT>
 __device__ __forceinline__ PairCut cut_of_pairs(const AttnArgs& a, const Seq& s0, int lane) {
-  if (a.plan.whole) return pair_cut(a.plan, 0, 0, 0, 0);
+  if (a.plan.whole) return pair_cut(a.plan, 0, 0, 0, 0, 0);
   long long tiles = 0;
   int pairs = 0, fewest = 1 << 30, most = 0;
   for (int i = 0; i < a.b.n_seqs; i += 64) {
@@ -320,9 +320,22 @@ __device__ __forceinline__ PairCut cut_of_pairs(const AttnArgs& a, const Seq& s0
     fewest = min(fewest, __shfl_xor(fewest, o));
     most = max(most, __shfl_xor(most, o));
   }
-  const PairCut c = pair_cut(a.plan, tiles, pairs, fewest, most);
+  const PairCut c = pair_cut(a.plan, tiles, pairs, a.b.n_seqs, fewest, most);
   return PairCut{__builtin_amdgcn_readfirstlane(c.kind), __builtin_amdgcn_readfirstlane(c.run),
-                 __builtin_amdgcn_readfirstlane(c.blocks)};
+                 __builtin_amdgcn_readfirstlane(c.blocks), __builtin_amdgcn_readfirstlane(c.joins)};
+}
+// Left for the join by one work-group: how the pairs are cut, and whether one of them is in several runs at all.
+template <int SHIFT>
+__device__ __forceinline__ void leave_cut(const AttnArgs& a, PairCut c, const Seq& s0, int lane, size_t slots) {
+  if (c.kind == APART) {
+    int cut = 0;
+    for (int i = 0; i < a.b.n_seqs; i += 64) {
+      const Seq s = i == 0 ? s0 : lane_seq(a.b, i, lane);
+      cut |= s.tokens > 0 && pair_tiles(a.plan, a.window, s, a.group, SHIFT) > c.run;
+    }
+    c.joins = __any(cut);
+  }
+  if (threadIdx.x == 0) *reinterpret_cast<PairCut*>(a.part + slots * attn_rows(a.plan) * (a.c.head_dim + 2)) = c;
 }
 // A pair that is cut EVEN or APART: the one that run x begins in, or (x < 0) that of row `row`, head g of its group.  A set's
 // row blocks stand from the last on, which sees the most positions; of pairs APART the runs of the same tiles stand
@@ -1072,8 +1085,7 @@ __device__ __forceinline__ void part_of(const AttnArgs& a, const Run& run) {
     if (item >= a.plan.paired) return;
     const Seq s0 = lane_seq(a.b, 0, lane);
     const PairCut c = cut_of_pairs<SHIFT>(a, s0, lane);
-    if (!a.plan.whole && blockIdx.x == 0 && threadIdx.x == 0)
-      *reinterpret_cast<PairCut*>(a.part + slots * attn_rows(a.plan) * (a.c.head_dim + 2)) = c;
+    if (!a.plan.whole && blockIdx.x == 0) leave_cut<SHIFT>(a, c, s0, lane, slots);
     if (c.kind == ALIKE) {
       RB = c.blocks;
       rb = RB - 1 - item % RB;
@@ -1162,7 +1174,8 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
   bool pairs = false;
   if constexpr (PAIRED) {
     const int* at = reinterpret_cast<const int*>(a.part + slots * slot_rows * (D + 2));  // what the other launch went by
-    const PairCut c{__builtin_amdgcn_readfirstlane(at[0]), __builtin_amdgcn_readfirstlane(at[1]), 0};
+    const PairCut c{__builtin_amdgcn_readfirstlane(at[0]), __builtin_amdgcn_readfirstlane(at[1]), 0, 0};
+    if (!__builtin_amdgcn_readfirstlane(at[3])) return;
     if (c.kind != ALIKE) {
       const Pair p = find_pair<SHIFT>(a, c, lane_seq(a.b, 0, lane), -1, row, g0, lane);
       pairs = true;

@@ -116,17 +116,21 @@ int new_cache(const CacheArgs& c, const CodeArgs& x, hcr_cache_t* out) {
 // Several sets of several row blocks: the device counts the pairs of a set and a row block (pair_cut), whole ones where less
 // than half of the sets times row blocks may be there.  fill: work-groups that the chip holds at once.  Measured (us a
 // call, D = 128, 32 heads over 8, against a plan in which each row block of the longest prompt took runs over all sets):
-//   a prompt of 2,048 and 63 single tokens of up to 8,192: int8 350 against 7,740, BF16 805 against 14,430, through a window
-//   of 5,000 339 against 6,220; of up to 4,096 (whole) int8 227 against 468, BF16 449 against 1,260.  512 tokens at 60,000
-//   beside three single ones 1,099 against 2,360; 3 prompts of 1,000 to 1 through a window of 6,000 297 against 400; 4 of 300
-//   at 9,000 (BF16, D = 64) 637 against 783.  Alike sets pay for the count (3 of 128 at 9,000 141 against
-//   136); whole ones of 2,048 and 1, which are not counted, would (89 against 87)
+//   a prompt of 2,048 and 63 single tokens of up to 8,192: int8 331 against 7,730, BF16 801 against 14,420, through a window
+//   of 5,000 330 against 6,220; of up to 4,096 (whole) int8 225 against 467, BF16 448 against 1,262.  300 sequences of
+//   5,000, 3 prompts of 700 among them, D = 64: int8 608 against 16,100; 512 tokens at 60,000 beside three single ones
+//   1,051 against 2,360; 3 prompts of 1,000 to 1 through a window of 6,000 298 against 400; 4 of 300 at 9,000 (BF16, D =
+//   64) 609 against 781.  Alike sets pay for the count (3 of 128 at 9,000 141 against 138, 4 of 100 at 60,000 through a
+//   window of 6,000 134 against 128); whole ones of 2,048 and 1, which are not counted, would (89 against 87)
 static void plan_pairs(AttnPlan& p, const CacheArgs& c, const BatchArgs& b, int group, int fill) {
   if (p.row_blocks == 1 || b.n_seqs == 1) return;
   const long long pairs = pairs_bound(p, b.n_seqs, (long long)b.n_tokens * group);
   if (p.whole && 2 * pairs >= (long long)b.n_seqs * p.row_blocks) return;
-  p.shares = fill / c.kv_heads > 1 ? fill / c.kv_heads : 1;
-  p.paired = (int)pairs + (p.whole ? 0 : 2 * p.shares);
+  const int shares = fill / c.kv_heads > 1 ? fill / c.kv_heads : 1;
+  const long long paired = pairs + (p.whole ? 0 : 2 * shares);
+  if ((paired + XCDS) * c.kv_heads * 1024 > THREADS_MAX) return;  // what a launch does not hold is cut as it was
+  p.shares = shares;
+  p.paired = (int)paired;
 }
 
 // Measured on MI355X, 8 kv heads, graphs of calls on rotated inputs (us a call), lengths from an eighth of the

@@ -157,9 +157,11 @@ HCR_HD long long pairs_bound(const AttnPlan& p, long long sets, long long rows_o
   const long long each = sets * p.row_blocks, all = sets + rows_of_all / attn_rows(p);
   return each < all ? each : all;
 }
-// How pairs are cut, from the tiles of all of them, their number and the row blocks of the sets that have rows:
-//   ALIKE  as many row blocks each, more runs than one: each row block's tiles as one row block's sets are cut, in `items`
-//          equal runs that may go on from one set to the next
+// How pairs are cut, from the tiles of all of them, their number, that of the sets, and the row blocks of those that have
+// rows:
+//   ALIKE  as many row blocks each, more runs than one of each row block, or (of more than 64 sets, which take a work-group
+//          longer to look through than to go through) enough row blocks for the chip: each row block's tiles as one row
+//          block's sets are cut, in `items` equal runs that may go on from one set to the next
 //   EVEN   no more pairs than the chip's share for a kv head: the tiles of all pairs, one behind the other, in one equal
 //          run for each share
 //   APART  more of them: each by itself, what is longer than half a share and than the average pair (by a sixteenth: what
@@ -167,17 +169,19 @@ HCR_HD long long pairs_bound(const AttnPlan& p, long long sets, long long rows_o
 enum PairKind { ALIKE, EVEN, APART };
 struct PairCut {
   int kind, run, blocks;  // ALIKE: row blocks of a set
+  int joins;              // whether a pair has several parts
 };
-HCR_HD PairCut pair_cut(const AttnPlan& p, long long tiles, int pairs, int fewest_blocks, int most_blocks) {
+HCR_HD PairCut pair_cut(const AttnPlan& p, long long tiles, int pairs, int sets, int fewest_blocks, int most_blocks) {
   constexpr long long MOST = 1 << 26;  // a pair has 2^25 at most
-  if (p.whole || pairs == 0) return PairCut{APART, (int)MOST, 0};
-  if (p.items > 1 && fewest_blocks == most_blocks) return PairCut{ALIKE, 0, most_blocks};
+  if (p.whole || pairs == 0) return PairCut{APART, (int)MOST, 0, 0};
+  if (fewest_blocks == most_blocks && (p.items > 1 || (sets > 64 && most_blocks >= p.shares)))
+    return PairCut{ALIKE, 0, most_blocks, p.items > 1};
   const bool even = pairs <= p.shares && tiles < 1 << 30;
   const int parts = even ? p.shares : 2 * p.shares < pairs ? 2 * p.shares : pairs;
   long long run = (tiles + parts - 1) / parts;
   if (!even) run += run / 16;
   run = run > p.least ? run : p.least;
-  return PairCut{even ? EVEN : APART, (int)(run < MOST ? run : MOST), 0};
+  return PairCut{even ? EVEN : APART, (int)(run < MOST ? run : MOST), 0, 1};
 }
 // A pair APART in even runs: `parts` of `each` tiles (the last may be shorter).  One that is cut has less than twice
 // tiles / run parts, all of them together less than four for each share.

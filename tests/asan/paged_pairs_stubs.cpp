@@ -47,12 +47,12 @@ static long long longest_run(const CacheArgs& c, const CodeArgs& x, const Window
     }
   }
   if (pairs > pairs_bound(p, b.n_seqs, (long long)b.n_tokens * group)) return *fail = "more pairs than the bound", -1;
-  const PairCut cut = pair_cut(p, tiles, pairs, fewest, most);
+  const PairCut cut = pair_cut(p, tiles, pairs, b.n_seqs, fewest, most);
   if (cut.kind == ALIKE) {  // what find_seq makes of them fits as it does without pairs
     if (cut.blocks != most || fewest != most) return *fail = "unlike sets (ALIKE)", -1;
     if ((long long)p.items * most > p.paired) return *fail = "more runs than work-groups (ALIKE)", -1;
-    if (2ll * p.items * most > attn_slots(p)) return *fail = "more parts than places (ALIKE)", -1;
-    if (!attn_joins(p)) return *fail = "parts without a join (ALIKE)", -1;
+    if (p.items > 1 && 2ll * p.items * most > attn_slots(p)) return *fail = "more parts than places (ALIKE)", -1;
+    if (!attn_joins(p) || cut.joins != (p.items > 1)) return *fail = "parts without a join (ALIKE)", -1;
     return run_tiles(p, (int)(tiles / most < 1 << 30 ? tiles / most : 1 << 30));
   }
   if (cut.kind == EVEN) {
@@ -119,7 +119,9 @@ static const char* check_pairs() {
                       const BatchArgs b{nullptr, nullptr, nullptr, ctx / page + 1, count, rows, tokens, ctx};
                       const AttnPlan p = plan_of(c, x, w, b, kv * group);
                       const long long bound = pairs_bound(p, count, (long long)rows * group);
-                      CHECK((p.paired > 0) == (p.row_blocks > 1 && count > 1 && (!p.whole || 2 * bound < 1ll * count * p.row_blocks)));
+                      const bool counted = p.row_blocks > 1 && count > 1 && (!p.whole || 2 * bound < 1ll * count * p.row_blocks);
+                      CHECK(p.paired ? counted && attn_grid(c, p) * 1024 < 1ll << 32
+                                     : !counted || (bound + 4096) * kv * 1024 > (1ll << 32) - (1 << 23));
                       CHECK(!coded(x) || p.shared || p.row_waves * p.groups <= 8);  // what their kernels are held to
                       if (!p.paired) continue;
                       CHECK(p.shares >= 1 && attn_grid(c, p) >= (long long)p.paired * kv && attn_grid(c, p) % XCDS == 0);
@@ -140,7 +142,7 @@ extern "C" const char* paged_pairs_checks(void) {
   // the largest that the checks of a batch let through
   AttnPlan p{};
   p.least = p.shares = 1;
-  CHECK(pair_cut(p, 1ll << 55, 1 << 30, 1, 9).run == 1 << 26 && pair_cut(p, 0, 0, 1 << 30, 0).kind == APART);
+  CHECK(pair_cut(p, 1ll << 55, 1 << 30, 2, 1, 9).run == 1 << 26 && pair_cut(p, 0, 0, 2, 1 << 30, 0).kind == APART);
   const PairRuns r = pair_runs(1 << 25, 1 << 26), one = pair_runs(1 << 25, 1);
   CHECK(r.parts == 1 && r.each == 1 << 25 && (long long)one.parts * one.each >= 1 << 25);
   return "ok";

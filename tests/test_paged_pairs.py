@@ -169,3 +169,50 @@ def test_a_graph_of_mixed_batches_reads_the_lengths_of_its_replay(kind):
                                          cache.attend_window(one, q[rows].contiguous(), 1000, 5))):
                 off, norm = ((x.double().norm(dim=2) for x in (all_[rows] - alone, alone)))
                 assert torch.all(off <= 2 * tol * norm)
+
+
+def test_index_batches_whose_pairs_no_launch_holds_are_not_refused(sanitized):
+    """A million sequences, most of them padding, with a bound of 4 tokens of 256 heads over 8: 8 million pairs may be there."""
+    from bf16_hyper_connection_amd import hcr
+    for code, ctx in ((1, 20000), (2, 20000)):
+        make = "hcr_cache_create_q8(V(K), V(2 * K), V(3 * K), V(4 * K), None, 2, 1000, 8, 64, 64, P(h))" if code == 2 else \
+            "hcr_cache_create(V(K), V(2 * K), None, 1000, 8, 64, 64, P(h))"
+        rc = int(sanitized(
+            "import sys; sys.path.insert(0, '.')\nfrom bf16_hyper_connection_amd import paged\n"
+            "K = 1 << 46\nh, V, P = ctypes.c_void_p(), ctypes.c_void_p, ctypes.byref\n"
+            f"assert L.{make} == 0\n"
+            f"b = paged.hcr_batch(1000000, 16, 4, {ctx}, 1 << 10, 16, 1 << 30, 1 << 40)\n"
+            "L.hcr_attn.argtypes = [V, V, ctypes.c_int, ctypes.c_double, V, ctypes.c_int, V, V, ctypes.c_size_t, V]\n"
+            "print(L.hcr_attn(h, P(b), 256, 0.1, 5 * K, 1, 6 * K, 7 * K, 1 << 40, None))"))
+        assert rc == hcr.HCR_EHIP, (code, ctx)  # every check passed: the stand-in's answer
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", cu.KINDS + ["bf16"])
+@pytest.mark.parametrize("alike", [True, False])
+def test_many_sequences_of_several_row_blocks(kind, alike):
+    """More sequences than a wave has lanes over the same pages, of as many row blocks each and not: each as by itself."""
+    ensure_built()
+    kv, group, T, n = 32, 64, 20 if kind != "bf16" else 80, 70
+    s = cu.scene(kind, 143, kv, 64, 64, [(T, 4500)])
+    cache = cu.dev_cache(s)
+    g = gen.rng(144)
+    tokens = [T if alike or i % 3 == 0 else int(g.integers(0, 4)) for i in range(n)]
+    ctx = [int(c) for c in g.integers(T, 4501, n)]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    starts = np.cumsum([0] + tokens)
+    batch = paged.Batch(torch.tensor(starts, **i32), torch.tensor(ctx, **i32),
+                        torch.from_numpy(np.repeat(s.table, n, 0)).cuda(), T, 4500)
+    q = torch.randn(int(starts[-1]), kv * group, 64, device="cuda", generator=torch.Generator("cuda").manual_seed(5)) * 2
+    q = q.to(torch.bfloat16)
+    for call in (lambda b, x: cache.attend(b, x), lambda b, x: cache.attend_window(b, x, 4300, 3)):
+        out = call(batch, q)
+        for i in (0, 1, 2, 33, 63, 64, 69):
+            if not tokens[i]:
+                continue
+            one = paged.Batch(torch.tensor([0, tokens[i]], **i32), torch.tensor([ctx[i]], **i32), batch.block_table[:1], tokens[i], 4500)
+            rows = slice(int(starts[i]), int(starts[i + 1]))
+            alone = call(one, q[rows].contiguous())
+            tol = pu.rows_tolerance(q[rows].double().cpu().numpy(), cu.reach(cu.decoded(s)[0]), 64 ** -0.5, 4500, False)
+            off, norm = (x.double().norm(dim=2) for x in (out[rows] - alone, alone))
+            assert torch.all(off <= 2 * tol * norm), i
