@@ -13,7 +13,8 @@
  * holds depends on that position alone, however windows were cut and whatever was written
  * over.  A head that holds a value that is not finite has the scale NaN and stands for NaN as
  * a whole; zeros, and heads whose scale rounds to 0, have the scale 0.  hcr_attn and
- * hcr_attn_blocks attend over what the codes stand for, in FP32; hcr_block_scores and
+ * hcr_attn_blocks attend over what the codes stand for, in FP32 (a probability takes its value's
+ * scale along into its BF16 parts: of scales under 2^-100 low bits are lost); hcr_block_scores and
  * hcr_block_topk take such a cache as any other (mean keys are of what the codes stand for).
  * Pages that were filled otherwise may hold any codes and scales: a key that is no number (the
  * E4M3 codes 0x7F and 0xFF, a scale of NaN) makes every output NaN of the rows that see it, a

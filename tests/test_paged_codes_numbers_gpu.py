@@ -1,5 +1,6 @@
-"""Values of a cache of E4M3 codes that are no numbers: each reaches its own dimension of the rows that see it and nothing
-else, in whatever tile and cut it lies; a value's scale that is none reaches all dimensions of them, a key every output."""
+"""Numbers at their ends in a cache of codes.  E4M3 codes of values that are no numbers: each reaches its own dimension of
+the rows that see it and nothing else, in whatever tile and cut it lies; a scale that is none reaches all dimensions of
+them.  Scales from 2^-96 up to where sums stay finite."""
 
 import numpy as np
 import pytest
@@ -77,3 +78,14 @@ def test_scales_that_are_no_numbers_reach_the_rows_that_see_them(kind, head_dim,
         see = np.array([(c - T + t >= (c + at if at < 0 else 0)) for _, c in windows for t in range(T)])
         assert np.array_equal(got, see) and np.array_equal(some, see)
         pu.check_rows(out, {m: w for m, w in want.items() if not see[m]}, tol, name)
+
+
+@pytest.mark.parametrize("kind", cu.KINDS)
+@pytest.mark.parametrize("head_dim,page,kv,group,T", SHAPES)
+@pytest.mark.parametrize("exponent", [-96, -60, 60, 104])
+def test_values_of_small_and_large_scales(kind, head_dim, page, kv, group, T, exponent):
+    """From where a probability times its value's scale has all of its BF16 parts up to where sums stay finite."""
+    s = cu.scene(kind, 162, kv, head_dim, page, [(T, T + 2), (T, 300 + T), (T, 3000)])
+    s.v_scales = (s.v_scales.astype(np.float64) * 2.0 ** exponent).astype(np.float32)
+    out, want, tol = cu.attend(s, kv * group)
+    pu.check_rows(out, want, tol, f"2^{exponent}")
