@@ -42,12 +42,12 @@
 // a work-group has 10 tiles behind 6 us of first loads, three row waves share each of them, so that a CU has 64 KB on
 // their way where it has 256 KB with one row wave, and the second launch takes 7.  (Rows past 16 over codes and windows
 // go to hcr_attn_rows.h.)
-// Codes, the same calls: 420,000 positions (E4M3, float outputs) 271 us, 6.5 TB/s; 64 sequences (int8) 108 us, 5.8 TB/s;
+// Codes, the same calls: 420,000 positions (E4M3, float outputs) 273 us, 6.4 TB/s; 64 sequences (int8) 116 us, 5.4 TB/s;
 // one of 700 positions 10.0 us, mostly waits for first loads, one behind the other (lengths, table, keys).  64 windows
-// of 4,096 of BF16 164 us, 6.6 TB/s.
-// Not taken: tiles of 32 for codes of D = 128 with 16 waves (batch 143 us, short call 11.8), tiles of 64 for D = 256 (25
+// of 4,096 of BF16 165 us, 6.5 TB/s.
+// Not taken: tiles of 32 for codes of D = 128 with 16 waves (batch 143 us where whole sets took 108, short call 11.8), tiles of 64 for D = 256 (25
 // registers spilled), two to four row tiles a wave over codes (36 rows of D = 256 130 to 190 us where four waves that
-// share them take 117: past 256 registers each use is a copy).
+// share them take 115: past 256 registers each use is a copy).
 
 #pragma once
 

@@ -8,7 +8,7 @@
 //   operands,
 //   O^T += V^T P^T : a wave's dimensions with every row tile, all 64 positions.
 // A wave's accumulators are the outputs of its dimensions: nothing is joined but the sums.  Two barriers a tile, of LDS
-// alone: keys of the next tile are on their way behind this one's products, values behind theirs.
+// alone, behind the first tile of whole sequences a third where a maximum moves: keys of the next tile are on their way behind this one's products, values behind theirs.
 //
 // Bound by the vector units beside the matrix cores, and by waits where a work-group is alone on its CU: of prompts through
 // a window of 1,024 (32 heads of 128 over 8, BF16, 64 rows a work-group) a tile takes one 2.4 us alone and three of them
@@ -16,7 +16,7 @@
 // instructions for 4 codes, int8 6), exponents and the three BF16 parts of float outputs.  Measured on MI355X: those
 // prompts (2,049 tokens, 34.5 GFLOP) 82 us, 0.42 PFLOP/s; 36 rows of 4 sequences of up to 9,001 (int8, D = 256, float
 // outputs) 30 us, 2.9 TB/s, and 7 for the join: 9 tiles a work-group behind the waits for its first loads; of one of
-// 100,000 114 us, 3.7 TB/s (24 rows 97); 24 rows through a window of 8,192 17 us and 4 for the join.
+// 100,000 115 us, 3.6 TB/s (24 rows 94; E4M3 100); 24 rows through a window of 8,192 17 us and 4 for the join.
 #pragma once
 
 #include "hcr_attn_device.h"

@@ -6,8 +6,8 @@
 // dimensions of one position, a lane's part of a row as they are.  Values: 16 bytes are some positions of one dimension;
 // they are turned in registers, four bytes (codes) or two values (BF16) at a time, and go through LDS.
 //
-// Bound by the bytes.  Measured on MI355X: 51,190 positions of 8 sequences, 8 kv heads of 128, int8 to BF16 (318 MB) 71
-// us, 4.5 TB/s, where a 4 GiB device copy moves 4.7.  On the way there: 32 positions a work-group 85 us; 64 positions, 16
+// Bound by the bytes.  Measured on MI355X: 51,200 positions of 8 sequences, 8 kv heads of 128, int8 to BF16 (318 MB) 72
+// us, 4.4 TB/s, where a 4 GiB device copy moves 4.7 (to floats 123 us, 4.3 TB/s; BF16 pages 88 us, 4.8 TB/s).  On the way there: 32 positions a work-group 85 us; 64 positions, 16
 // bytes of a lane's own row at a time 83; neighbouring lanes' 16 bytes beside each other and stores past the caches 71.
 #include "hcr_append_device.h"
 

@@ -308,9 +308,10 @@ static AttnPlan rows_plan(const CacheArgs& c, const WindowArgs& w, const BatchAr
 
 // Over codes and windows rows that fill more than one tile share a work-group's four waves: a row tile a wave would read
 // (and widen) every page once a tile.  Measured, 8 kv heads (us, shared against a tile a wave): D = 256, 36 rows over
-// 100,000 positions of int8 114 against 185, of E4M3 107 against 152; D = 128 over 200,000: 20 rows 104 against 119, 48
-// 133 against 185, 64 161 against 200; D = 64, 20 rows 70 against 78; prompts of BF16 through a window 86 against 92.  Its
-// tiles have 64 positions, so pages of 32 (BF16 through a window) keep a tile a wave.  Up to 16 rows one wave has all of
+// 100,000 positions of int8 115 against 185, of E4M3 100 against 152; D = 128 over 200,000: 20 rows 97 against 119, 48
+// 124 against 185, 64 147 against 200; D = 64, 20 rows 67 against 78; prompts of BF16 through a window 82 against 92.  Its
+// tiles have 64 positions, so pages of 32 (BF16 through a window) keep a tile a wave
+// (a prompt of 1,024, D = 128: through a window of 1,024 64 where pages of 64 take 46, of 5,000 227 and 120).  Up to 16 rows one wave has all of
 // a tile's operands as loaded, with no barrier in its loop.
 AttnPlan attn_plan_more(const CacheArgs& c, const CodeArgs& x, const WindowArgs& w, const BatchArgs& b, int heads,
                         int n_sel) {

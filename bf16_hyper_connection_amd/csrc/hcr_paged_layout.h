@@ -93,7 +93,8 @@ HCR_HD int ceil_div(int a, int b) { return (a + b - 1) / b; }
 constexpr int TILE = 32;
 constexpr int TILE_SHIFT = 5;
 // A wave's tile of codes has 64 positions, so that it has as many bytes on their way as of BF16 (and 32 of D = 256, whose
-// accumulators leave no room for more): 64 sequences of up to 8,192 positions, D = 128, 108 us where tiles of 32 took 143.
+// accumulators leave no room for more): 64 sequences of up to 8,192 positions, D = 128, whole, 108 us where tiles of 32
+// took 143.
 constexpr int tile_shift(bool codes, int D) { return codes && D != 256 ? TILE_SHIFT + 1 : TILE_SHIFT; }
 // Tiles of work-groups whose four waves share their rows (hcr_attn_rows.h): 16 keys a wave.
 constexpr int ROWS_SHIFT = 6;
@@ -104,8 +105,10 @@ HCR_HD bool code_page_ok(int page) { return page_ok(page) && page >= 64; }
 constexpr int attn_waves(int D, int q_tiles) { return D == 64 ? 16 : D == 256 && q_tiles > 1 ? 4 : 8; }
 // Work-groups of four waves that share their rows, on a CU: the registers are held to that.  As many as spill no more
 // than a dozen of them (measured, codes: D = 128, 20 rows of 200,000 positions 103 us with four, 113 with two; D = 64 70
-// against 84, 64 rows through a window of 1,024 68 with four, 77 with three; D = 256, 36 rows of 100,000, E4M3 97 with two,
-// 113 with three, which spill 27, int8 108 with either, 4 sequences of up to 9,001 38 against 42).
+// against 84, 64 rows through a window of 1,024 68 with four, 77 with three).  D = 256 of three row tiles: with three
+// work-groups E4M3 spills 27 (36 rows, two against three: 4 sequences of up to 9,001 38 and 47, one of 100,000 100 and
+// 114, of 400,000 359 both), int8 none, which gains by the third only over long sequences (42 and 44, 115 and 111, 399
+// and 383): two for both.
 constexpr int rows_held(int D, int q_tiles) { return D == 256 ? (q_tiles > 2 ? 2 : 3) : D == 128 && q_tiles > 2 ? 3 : 4; }
 
 // How a call is cut.  Its sets of rows (a sequence's window; one token for listed pages) have their tiles one set
