@@ -113,19 +113,24 @@ int new_cache(const CacheArgs& c, const CodeArgs& x, hcr_cache_t* out) {
   return HCR_OK;
 }
 
-// Several sets of several row blocks: the device counts the pairs of a set and a row block (pair_cut), whole ones where less
-// than half of the sets times row blocks may be there.  fill: work-groups that the chip holds at once.  Measured (us a
-// call, D = 128, 32 heads over 8, against a plan in which each row block of the longest prompt took runs over all sets):
+// Several sets of several row blocks: the device counts the pairs of a set and a row block (pair_cut).  Where the bounds
+// would have a work-group take 2,048 positions and more (the search takes each about 3 us: 40 sequences of up to 9 tokens, 32
+// heads of 64 over 2, BF16 (int8): at up to 2,500 positions 37.9 us without it, 39.6 with it (42.7, 47.4), at 9,000 75.7 and
+// 71.0 (80.4 and 77.3)); of whole sets where there would be several rounds of work-groups, less than half of them with
+// rows.  fill: work-groups that the chip holds at once.
+// Measured (us a call, D = 128, 32 heads over 8, against a plan in which each row block of the longest prompt takes runs
+// over all sets):
 //   a prompt of 2,048 and 63 single tokens of up to 8,192: int8 331 against 7,730, BF16 801 against 14,420, through a window
 //   of 5,000 330 against 6,220; of up to 4,096 (whole) int8 225 against 467, BF16 448 against 1,262.  300 sequences of
 //   5,000, 3 prompts of 700 among them, D = 64: int8 608 against 16,100; 512 tokens at 60,000 beside three single ones
 //   1,051 against 2,360; 3 prompts of 1,000 to 1 through a window of 6,000 298 against 400; 4 of 300 at 9,000 (BF16, D =
-//   64) 609 against 781.  Alike sets pay for the count (3 of 128 at 9,000 141 against 138, 4 of 100 at 60,000 through a
-//   window of 6,000 134 against 128); whole ones of 2,048 and 1, which are not counted, would (89 against 87)
-static void plan_pairs(AttnPlan& p, const CacheArgs& c, const BatchArgs& b, int group, int fill) {
-  if (p.row_blocks == 1 || b.n_seqs == 1) return;
+//   64) 609 against 781.  Alike sets pay for the count (3 of 128 at 9,000 141 against 138, 200 of 30 at
+//   5,000, D = 64 1,504 against 1,493, BF16 1,650 against 1,588)
+static void plan_pairs(AttnPlan& p, const CacheArgs& c, const BatchArgs& b, int group, int fill, long long span) {
+  if (p.row_blocks == 1 || b.n_seqs == 1 || (!p.whole && b.n_seqs * span < 2048ll * p.items)) return;
   const long long pairs = pairs_bound(p, b.n_seqs, (long long)b.n_tokens * group);
-  if (p.whole && 2 * pairs >= (long long)b.n_seqs * p.row_blocks) return;
+  const long long each = (long long)b.n_seqs * p.row_blocks;
+  if (p.whole && (2 * pairs >= each || each * c.kv_heads < 4096)) return;
   const int shares = fill / c.kv_heads > 1 ? fill / c.kv_heads : 1;
   const long long paired = pairs + (p.whole ? 0 : 2 * shares);
   if ((paired + XCDS) * c.kv_heads * 1024 > THREADS_MAX) return;  // what a launch does not hold is cut as it was
@@ -236,7 +241,7 @@ static AttnPlan plan_for(const CacheArgs& c, const BatchArgs& b, int heads, int 
     items = runs * sets;
   }
   p.items = p.whole ? (int)sets : items > 1 ? (int)items : 1;
-  if (!n_sel) plan_pairs(p, c, b, group, fill);
+  if (!n_sel) plan_pairs(p, c, b, group, fill, span);
   return p;
 }
 
@@ -302,7 +307,7 @@ static AttnPlan rows_plan(const CacheArgs& c, const WindowArgs& w, const BatchAr
     items = runs * sets;
   }
   p.items = p.whole ? (int)sets : items > 1 ? (int)items : 1;
-  if (!n_sel) plan_pairs(p, c, b, group, fill);
+  if (!n_sel) plan_pairs(p, c, b, group, fill, (long long)tiles << ROWS_SHIFT);
   return p;
 }
 

@@ -119,7 +119,13 @@ static const char* check_pairs() {
                       const BatchArgs b{nullptr, nullptr, nullptr, ctx / page + 1, count, rows, tokens, ctx};
                       const AttnPlan p = plan_of(c, x, w, b, kv * group);
                       const long long bound = pairs_bound(p, count, (long long)rows * group);
-                      const bool counted = p.row_blocks > 1 && count > 1 && (!p.whole || 2 * bound < 1ll * count * p.row_blocks);
+                      // counted where a work-group would go through many positions, or most work-groups have no rows
+                      const int shift = shift_of(c, x, p), block = ceil_div(attn_rows(p), group) + 1;
+                      const int tiles = window_bound(w, ctx, p.shared && block < tokens ? block : tokens, shift);
+                      const long long each = 1ll * count * p.row_blocks;
+                      const bool counted = p.row_blocks > 1 && count > 1 &&
+                                           (p.whole ? 2 * bound < each && each * kv >= 4096
+                                                    : ((long long)count * tiles << shift) >= 2048ll * p.items);
                       CHECK(p.paired ? counted && attn_grid(c, p) * 1024 < 1ll << 32
                                      : !counted || (bound + 4096) * kv * 1024 > (1ll << 32) - (1 << 23));
                       CHECK(!coded(x) || p.shared || p.row_waves * p.groups <= 8);  // what their kernels are held to
@@ -193,4 +199,12 @@ extern "C" int paged_more_run_pages(int code, int D, int kv, int page, int heads
   int run = p.whole ? tiles : n_sel ? run_tiles_listed(p, tiles, b.n_tokens) : run_tiles(p, n_seqs * tiles);
   if (run > tiles) run = tiles;
   return run >> (c.shift - shift);
+}
+
+// Whether a call over pages of `page` positions counts its pairs.
+extern "C" int paged_plan_paired(int code, int D, int kv, int page, int heads, int size, int n_seqs, int n_tokens, int max_tokens,
+                                 int max_ctx) {
+  const CacheArgs c{nullptr, nullptr, nullptr, 10, kv, D, log2_of(page)};
+  const BatchArgs b{nullptr, nullptr, nullptr, 1 << 20, n_seqs, n_tokens, max_tokens, max_ctx};
+  return plan_of(c, CodeArgs{nullptr, nullptr, code}, WindowArgs{size, 0}, b, heads).paired > 0;
 }

@@ -92,43 +92,71 @@ BATCHES = {  # windows (new tokens, positions), bounds above what there is
     "past 64 sequences": ([(0, 50)] * 30 + [(1, 7000)] + [(1, 40)] * 40 + [(140, 300)] + [(1, 11)] * 30 + [(35, 4500)], {}),
     "loose bounds": ([(1, 600), (70, 800), (1, 2300), (2, 1)], dict(max_tokens=400, max_ctx=9000)),
     "tokens before the first position": ([(130, 100), (1, 6000), (40, 20)], {}),
+    "whole sequences": ([(1, 20 + 3 * i) for i in range(60)] + [(300, 300)], {}),
+    "alike prompts": ([(64, 4500), (60, 3100), (57, 60)], {}),
 }
+SHAPES = [(128, 64, 8, 16), (64, 64, 16, 16), (256, 64, 8, 12)]  # head_dim, page, kv heads, group
+
+
+def bounds_of(windows, bounds):
+    return bounds.get("max_tokens", max(t for t, _ in windows)), bounds.get("max_ctx", max(c for _, c in windows))
+
+
+def test_index_the_scenes_pairs_are_counted(sanitized):
+    calls = [(code, D, kv, page, kv * group, size, len(w), sum(t for t, _ in w), *bounds_of(w, b))
+             for w, b in BATCHES.values() for D, page, kv, group in SHAPES for code in (1, 2, 3) for size in (0, 90, 6000)]
+    counted = sanitized(f"print(*[L.paged_plan_paired(*c) for c in {calls}])").split()
+    assert len(counted) == len(calls)
+    for name, (w, b) in BATCHES.items():
+        for size in (0, 6000):
+            for code in (1, 2, 3):
+                of = [int(x) for c, x in zip(calls, counted) if c[0] == code and c[5] == size and c[6] == len(w)]
+                assert sum(of) >= 2, (name, size, code, of)
+
+
+def check_one_head(s, kind, kv, group, head, out, q, window=None, n_first=0):
+    """One kv head's rows against the reference."""
+    keys, values = (x[:, head:head + 1] for x in cu.decoded(s))
+    mine = slice(head * group, (head + 1) * group)
+    qf = oracle.bf16_bits_to_f64(np.ascontiguousarray(q[:, mine]))
+    sc = q.shape[2] ** -0.5
+    if window is None:
+        want = oracle.paged.attend(s.batch, keys, values, qf, sc)
+    else:
+        want = oracle.paged_codes.attend_window(s.batch, keys, values, qf, sc, window, n_first)
+    tol = pu.rows_tolerance(qf, cu.reach(keys), sc, int(max(s.ctx_len.max(), 1)), out.dtype == torch.bfloat16)
+    pu.check_rows(out[:, mine], want, tol, f"{kind} head {head}")
 
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", cu.KINDS + ["bf16"])
-@pytest.mark.parametrize("head_dim,page,kv,group", [(128, 64, 1, 5), (64, 128, 2, 8), (256, 64, 1, 6)])
+@pytest.mark.parametrize("head_dim,page,kv,group", SHAPES)
 @pytest.mark.parametrize("name", sorted(BATCHES))
 def test_attend(kind, head_dim, page, kv, group, name):
     ensure_built()
     windows, bounds = BATCHES[name]
     s = cu.scene(kind, 140, kv, head_dim, page, windows, table_extra=150)
-    if kind == "bf16":  # their scenes take the same path
-        heads = kv * group
-        q = pu.queries(140, s.n_tokens + 3, heads, head_dim)
-        qf = oracle.bf16_bits_to_f64(q)
-        keys, values = cu.decoded(s)
-        want = oracle.paged.attend(s.batch, keys, values, qf, head_dim ** -0.5)
-        tol = pu.rows_tolerance(qf, cu.reach(keys), head_dim ** -0.5, int(s.ctx_len.max()), False)
-        out = torch.full((s.n_tokens + 3, heads, head_dim), 5.0, device="cuda")
-        cu.dev_cache(s).attend(pu.dev_batch(s, **bounds), pu.dev_bits(q), out=out)
-        assert torch.all(out[s.n_tokens:] == 5.0)
-    else:
-        out, want, tol = cu.attend(s, kv * group, extra_rows=3, **bounds)
-    pu.check_rows(out, want, tol, name)
+    q = pu.queries(140, s.n_tokens + 3, kv * group, head_dim)
+    out = torch.full((s.n_tokens + 3, kv * group, head_dim), 5.0, device="cuda")
+    cu.dev_cache(s).attend(pu.dev_batch(s, **bounds), pu.dev_bits(q), out=out)
+    torch.cuda.synchronize()
+    assert torch.all(out[s.n_tokens:] == 5.0)
+    check_one_head(s, kind, kv, group, 1, out, q)
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("kind", cu.KINDS + ["bf16"])
-@pytest.mark.parametrize("head_dim,page,kv,group", [(128, 64, 1, 5), (64, 32, 2, 8), (256, 64, 1, 6)])
+@pytest.mark.parametrize("kind,head_dim,page,kv,group", [("int8", 128, 64, 8, 16), ("bf16", 128, 64, 8, 16), ("bf16", 64, 32, 16, 16),
+                                                         ("e4m3", 64, 64, 16, 16), ("int8", 256, 64, 8, 12)])
 @pytest.mark.parametrize("window,n_first", [(90, 0), (6000, 70)])
 @pytest.mark.parametrize("name", sorted(BATCHES))
 def test_attend_window(kind, head_dim, page, kv, group, window, n_first, name):
     ensure_built()
     windows, bounds = BATCHES[name]
-    s = cu.scene(kind, 141, kv, head_dim, page if kind == "bf16" else max(page, 64), windows, table_extra=300)
-    out, want, tol = cu.attend(s, kv * group, out_dtype=torch.bfloat16, window=window, n_first=n_first, **bounds)
-    pu.check_rows(out, want, tol, name)
+    s = cu.scene(kind, 141, kv, head_dim, page, windows, table_extra=300)
+    q = pu.queries(141, s.n_tokens, kv * group, head_dim)
+    out = cu.dev_cache(s).attend_window(pu.dev_batch(s, **bounds), pu.dev_bits(q), window, n_first, out_dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    check_one_head(s, kind, kv, group, kv - 1, out, q, window, n_first)
 
 
 @pytest.mark.gpu
@@ -137,14 +165,14 @@ def test_a_graph_of_mixed_batches_reads_the_lengths_of_its_replay(kind):
     """Which sequence is the prompt, and how long they all are, changes between replays."""
     ensure_built()
     windows = [(200, 200), (1, 6000), (1, 33), (40, 3000)]
-    s = cu.scene(kind, 142, 2, 128, 64, [(1, 6000)] * 4)
+    s = cu.scene(kind, 142, 16, 64, 64, [(1, 6000)] * 4)
     cache = cu.dev_cache(s)
     i32 = dict(dtype=torch.int32, device="cuda")
     starts, lens = torch.zeros(5, **i32), torch.ones(4, **i32)
     batch = paged.Batch(starts, lens, torch.from_numpy(s.table).cuda(), 200, 6000)
-    bits = pu.queries(142, 242, 8, 128)
+    bits = pu.queries(142, 242, 128, 64)
     q = pu.dev_bits(bits)
-    tol = pu.rows_tolerance(oracle.bf16_bits_to_f64(bits), cu.reach(cu.decoded(s)[0]), 128 ** -0.5, 6000, False)
+    tol = pu.rows_tolerance(oracle.bf16_bits_to_f64(bits), cu.reach(cu.decoded(s)[0]), 64 ** -0.5, 6000, False)
 
     def calls():
         return [cache.attend(batch, q), cache.attend_window(batch, q, 1000, 5)]
@@ -193,7 +221,7 @@ def test_index_batches_whose_pairs_no_launch_holds_are_not_refused(sanitized):
 def test_many_sequences_of_several_row_blocks(kind, alike):
     """More sequences than a wave has lanes over the same pages, of as many row blocks each and not: each as by itself."""
     ensure_built()
-    kv, group, T, n = 32, 64, 20 if kind != "bf16" else 80, 70
+    kv, group, T, n = 32, 64, 34 if kind != "bf16" else 80, 70
     s = cu.scene(kind, 143, kv, 64, 64, [(T, 4500)])
     cache = cu.dev_cache(s)
     g = gen.rng(144)
