@@ -170,12 +170,14 @@ static void plan_pairs(AttnPlan& p, const CacheArgs& c, const BatchArgs& b, int 
 //              one is mostly the wait for its first loads
 // The bounds are in positions, whatever a tile has (BF16 and codes of D = 256 32, codes of D <= 128 64).
 // Over codes (the same calls, whole or with four waves against the other):
-//   whole      fewer sets than CUs: a set in one work-group takes longer with its length, in runs with the number of sets.
-//              One, D = 128, three caches in turn: 640 positions 9.9 against 10.3, 768 9.7 against 10.4, 832 11.9 against
-//              10.6 (16 caches 12.2 against 11.2 at 768, 17.8 against 11.6 at 1,400); a call that is not in a graph takes
-//              2.5 more for the second launch.  D = 64: 768 8.4 against 10.1, 1,024 9.8 against 10.0; D = 256: 384 10.8
-//              against 11.4, 448 12.4 against 11.2.  4: 768 11.9 against 12.0, 832 13.8 against 12.0; 16: 1,024 15.8 against
-//              17.4, 1,200 16.9 against 20.1; 16 of D = 256: 640 17.9 against 18.2, 768 20.9 against 18.5.
+//   whole      fewer sets than CUs: a set in one work-group takes longer with its length, in runs with the number of sets,
+//              more past 64, which a wave does not see at once.  One, D = 128, three caches in turn: 640 positions 9.9
+//              against 10.3, 768 9.7 against 10.4, 832 11.9 against 10.6; a call that is not in a graph takes 2.5 more for
+//              the second launch.  D = 64: 768 8.4 against 10.1, 1,024 9.8 against 10.0; D = 256: 384 10.8 against 11.4,
+//              448 12.4 against 11.2.  128 work-groups (16 sets of 8 heads, rotated caches), D = 128: 1,200 16.7 against
+//              17.4, 1,600 20.2 against 17.9; 192: 2,200 25.4 against 33.8, 3,000 32.7 against 34.7; D = 256 128: 700 19.9
+//              against 19.2, 192: 1,600 35.7 against 35.6; D = 64 128: 2,200 16.8 against 20.0.  72 sets of one head, D =
+//              128: 1,200 16.3 against 20.2, 2,200 23.7 against 23.3
 //              32 sets, D = 128: of 3,000 33.5 against 38.9, 4,096 42 against 43; D = 256: 3,000 64 against 57.  64
 //              and more to 4,096 as above: one of 8,192 beside 63 of 100 takes 24 in runs, 66 whole, one of 5,000 28
 //              and 45 (lengths from an eighth of 8,192 up to it 114 and 105, all of 8,192 174 and 177)
@@ -206,14 +208,20 @@ static AttnPlan plan_for(const CacheArgs& c, const BatchArgs& b, int heads, int 
   const long long full = sets * units;  // work-groups of whole sets
   // positions up to which a work-group takes a whole set, and up to which four waves a work-group do
   long long whole_to, few_to;
-  if (full < CUS)
-    whole_to = (wide ? (rows > 16 ? 192 : 384) : 96 * most_groups) + (codes && full > 64 ? 4 * (full - 64) : 0);
-  else if (n_sel)
+  if (full < CUS) {
+    whole_to = wide ? (rows > 16 ? 192 : 384) : 96 * most_groups;
+    if (codes) {
+      const long long over = full > 64 ? full - 64 : 0, most = wide ? 2048 : 4096;
+      whole_to = (c.head_dim == 64 ? 1024 : whole_to) * (sets > 64 ? 2 : 1) * (4096 + over * over) / 4096;
+      if (whole_to > most) whole_to = most;
+    }
+  } else if (n_sel) {
     whole_to = span;  // lists are alike
-  else if (alone)
+  } else if (alone) {
     whole_to = 1024;
-  else
+  } else {
     whole_to = full < 2 * CUS && !(codes && !wide) ? 2048 : 4096;
+  }
   p.whole = span <= whole_to;
   if (p.whole)
     few_to = full < 2 * CUS ? -1 : codes ? 1024 : 512;

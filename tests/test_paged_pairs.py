@@ -77,7 +77,7 @@ def test_index_no_set_of_more_than_4096_positions_is_one_work_groups(sanitized, 
         size, sets, ctx, whole = map(int, line.split())
         if code != 1 or size:
             # fewer sets than CUs: those that end as soon as runs and their join
-            most = (384 if head_dim == 256 else 768) + 4 * max(8 * sets - 64, 0)
+            most = {64: 1024, 128: 768, 256: 384}[head_dim] * (4096 + max(8 * sets - 64, 0) ** 2) / 4096
             if whole and sets < 32 and code != 1:
                 assert min(ctx, size or ctx) <= most, line
             if whole:
